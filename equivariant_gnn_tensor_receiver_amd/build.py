@@ -50,7 +50,8 @@ UNITS = ([(f"stream_{n}", "stream_gf.hip", STREAM_FLAGS + [f"-DTP_MODE={m}", f"-
          + [(u, u + ext, []) for u, ext in (("gemm", ".hip"), ("channelwise", ".hip"), ("graph", ".hip"), ("radial", ".hip"), ("fixed", ".hip"),
                                              ("scratch", ".hip"), ("ragged", ".hip"), ("api", ".cpp"),
                                              ("stream_dispatch", ".cpp"), ("plan", ".cpp"),
-                                             ("timing", ".cpp"))])
+                                             ("timing", ".cpp"), ("layer_norm", ".hip"), ("linear", ".hip"),
+                                             ("muon", ".hip"), ("layers", ".cpp"))])
 
 
 def run(cmd):
@@ -70,7 +71,7 @@ def generate():
 
 def _newest_input(src: str) -> float:
     """Newest of a unit's source, every header, the generated tables and this script."""
-    files = ([os.path.join(CSRC, src), os.path.join(ROOT, "include", "tpconv.h"), __file__]
+    files = ([os.path.join(CSRC, src), __file__] + glob.glob(os.path.join(ROOT, "include", "*.h"))
              + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(GEN, "*")))
     return max(os.path.getmtime(f) for f in files if os.path.isfile(f))
 

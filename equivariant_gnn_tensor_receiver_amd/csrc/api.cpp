@@ -25,10 +25,6 @@
 #include "plan.h"
 #include "timing.h"
 
-struct tpconv_plan_s {
-  tpconv::Plan plan;
-};
-
 namespace tpconv {
 namespace {
 

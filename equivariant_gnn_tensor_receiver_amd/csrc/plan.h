@@ -107,3 +107,8 @@ int build_plan(const char* irreps_in, const char* irreps_out, int sh_lmax, int K
                int env_p, int x_dtype, int w_dtype, int connection, Plan& plan);
 
 }  // namespace tpconv
+
+// The C ABI's plan handle.
+struct tpconv_plan_s {
+  tpconv::Plan plan;
+};

@@ -5,11 +5,13 @@
 
 namespace tpconv {
 
-// Kernel classes; the numbering matches tpconv_kernel in include/tpconv.h.
+// Kernel classes; the numbering matches tpconv_kernel in include/tpconv.h and
+// tpconv_layer_kernel in include/tpconv_layers.h.
 enum KernelClass : int {
   kcStreamFwd = 0, kcStreamJvp, kcStreamSnd, kcStreamSndT, kcStreamBwdPos,
   kcGemmOut, kcGemmGs, kcGemmGx, kcGemmGw, kcGwReduce, kcFill, kcGraph,
-  kcCwContract, kcCwGw, kcCwReduce, kcStreamHess, kcStateDot, kcCount
+  kcCwContract, kcCwGw, kcCwReduce, kcStreamHess, kcStateDot,
+  kcNorm, kcLinear, kcMuon, kcCount
 };
 
 // While timing is enabled, brackets the launches issued in its lifetime with
