@@ -69,6 +69,404 @@ __device__ __forceinline__ const NormIrrep& find_irrep(const NormArgs& a, int bl
   return a.ir[i];
 }
 
+typedef float floatx4 __attribute__((ext_vector_type(4)));
+
+// The four channels a thread holds of one row: a run of four (VEC: one wide
+// load) or four that lie `step` apart.  Channels past the row read as zero.
+template <bool VEC>
+struct Quad {
+  int c0, step, mul;
+  __device__ __forceinline__ Quad(int lane, int lanes, int mul_)
+      : c0(VEC ? 4 * lane : lane), step(VEC ? 1 : lanes), mul(mul_) {}
+  __device__ __forceinline__ int at(int q) const { return c0 + q * step; }
+  __device__ __forceinline__ bool has(int q) const { return at(q) < mul; }
+  __device__ __forceinline__ void load(const float* p, bool ok, float (&v)[4]) const {
+    if constexpr (VEC) {
+      floatx4 x = {0.f, 0.f, 0.f, 0.f};
+      if (ok && c0 < mul) x = *reinterpret_cast<const floatx4*>(p + c0);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] = x[q];
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] = ok && has(q) ? p[at(q)] : 0.f;
+    }
+  }
+  __device__ __forceinline__ void load(const uint16_t* p, bool ok, float (&v)[4]) const {
+    if constexpr (VEC) {
+      uint2 x = {0, 0};
+      if (ok && c0 < mul) x = *reinterpret_cast<const uint2*>(p + c0);
+      v[0] = __uint_as_float(x.x << 16);
+      v[1] = __uint_as_float(x.x & 0xffff0000u);
+      v[2] = __uint_as_float(x.y << 16);
+      v[3] = __uint_as_float(x.y & 0xffff0000u);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] = ok && has(q) ? load_feat(p, at(q)) : 0.f;
+    }
+  }
+  __device__ __forceinline__ void store(float* p, const float (&v)[4]) const {
+    if constexpr (VEC) {
+      if (c0 < mul) *reinterpret_cast<floatx4*>(p + c0) = (floatx4){v[0], v[1], v[2], v[3]};
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (has(q)) p[at(q)] = v[q];
+    }
+  }
+  __device__ __forceinline__ void store(uint16_t* p, const float (&v)[4]) const {
+    if constexpr (VEC) {
+      if (c0 < mul) {
+        const bf16x2 lo = {(__bf16)v[0], (__bf16)v[1]}, hi = {(__bf16)v[2], (__bf16)v[3]};
+        *reinterpret_cast<uint2*>(p + c0) = {__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (has(q)) store1(p, at(q), v[q]);
+    }
+  }
+  // weight and bias are the caller's and need no wide alignment
+  __device__ __forceinline__ void load_param(const float* p, float none, float (&v)[4]) const {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = p && has(q) ? p[at(q)] : p ? 0.f : none;
+  }
+};
+
+// ---- narrow blocks (at most 256 channels) -------------------------------------------
+// A group of `lanes` lanes (a power of two, four channels per lane) takes one
+// (node, irrep) and keeps its N rows in registers: one read, statistics by lane
+// swaps, one write.
+
+template <int N, bool VEC, typename TX, typename TY>
+__device__ __forceinline__ void forward_narrow(const NormArgs& a, const NormIrrep& ir) {
+  const int lanes = ir.lanes, t = threadIdx.x & (lanes - 1), per = kThreads / lanes, slot = threadIdx.x / lanes;
+  const Quad<VEC> qd(t, lanes, ir.mul);
+  const float len = (float)(ir.mul * N);
+  float w[4], b[4];
+  qd.load_param(a.w ? a.w + ir.w_off : nullptr, 1.f, w);
+  qd.load_param(ir.scalar && a.b ? a.b + ir.b_off : nullptr, 0.f, b);
+  for (int64_t v0 = (int64_t)(blockIdx.x - ir.first_block) * per; v0 < a.N; v0 += (int64_t)ir.blocks * per) {
+    const int64_t v = v0 + slot;
+    const bool ok = v < a.N;
+    const int64_t at = v * a.F + ir.off;
+    float x[N][4];
+#pragma unroll
+    for (int m = 0; m < N; ++m) qd.load(static_cast<const TX*>(a.x) + at + m * ir.mul, ok, x[m]);
+    float mu = 0.f;
+    if (N == 1 && ir.scalar) {
+      mu = group_sum((x[0][0] + x[0][1]) + (x[0][2] + x[0][3]), lanes) / len;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) x[0][q] = qd.has(q) ? x[0][q] - mu : 0.f;
+    }
+    float s = 0.f;
+#pragma unroll
+    for (int m = 0; m < N; ++m)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) s = __builtin_fmaf(x[m][q], x[m][q], s);
+    const float r = 1.f / sqrtf(group_sum(s, lanes) / len + a.eps);
+    if (!ok) continue;
+#pragma unroll
+    for (int m = 0; m < N; ++m) {
+      float y[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) y[q] = __builtin_fmaf(x[m][q] * r, w[q], b[q]);
+      qd.store(static_cast<TY*>(a.y) + at + m * ir.mul, y);
+    }
+    if (a.stats && t == 0) {
+      float* st = a.stats + (v * a.nirreps + (&ir - a.ir)) * 2;
+      st[0] = mu;
+      st[1] = r;
+    }
+  }
+}
+
+template <int N, bool VEC, typename TX>
+__device__ __forceinline__ void backward_narrow(const NormArgs& a, const NormIrrep& ir, float (*red)[512]) {
+  const int lanes = ir.lanes, t = threadIdx.x & (lanes - 1), per = kThreads / lanes, slot = threadIdx.x / lanes;
+  const int rank = blockIdx.x - ir.first_block;
+  const Quad<VEC> qd(t, lanes, ir.mul);
+  const float len = (float)(ir.mul * N);
+  float w[4], sw[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+  qd.load_param(a.w ? a.w + ir.w_off : nullptr, 1.f, w);
+  for (int64_t v0 = (int64_t)rank * per; v0 < a.N; v0 += (int64_t)ir.blocks * per) {
+    const int64_t v = v0 + slot;
+    const bool ok = v < a.N;
+    const int64_t at = v * a.F + ir.off;
+    float x[N][4], g[N][4];
+#pragma unroll
+    for (int m = 0; m < N; ++m) {
+      qd.load(static_cast<const TX*>(a.x) + at + m * ir.mul, ok, x[m]);
+      qd.load(a.gy + at + m * ir.mul, ok, g[m]);
+    }
+    float mu = 0.f, r = 0.f;
+    if (a.stats) {
+      if (ok) {
+        const float* st = a.stats + (v * a.nirreps + (&ir - a.ir)) * 2;
+        mu = st[0];
+        r = st[1];
+      }
+    } else if (N == 1 && ir.scalar) {
+      mu = group_sum((x[0][0] + x[0][1]) + (x[0][2] + x[0][3]), lanes) / len;
+    }
+    if (N == 1 && ir.scalar)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) x[0][q] = qd.has(q) ? x[0][q] - mu : 0.f;
+    if (!a.stats) {
+      float s = 0.f;
+#pragma unroll
+      for (int m = 0; m < N; ++m)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) s = __builtin_fmaf(x[m][q], x[m][q], s);
+      r = 1.f / sqrtf(group_sum(s, lanes) / len + a.eps);
+    }
+    float sh = 0.f, shz = 0.f;
+#pragma unroll
+    for (int m = 0; m < N; ++m)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        x[m][q] *= r;  // z
+        sw[q] = ok ? __builtin_fmaf(g[m][q], x[m][q], sw[q]) : sw[q];
+        sb[q] += g[m][q];
+        g[m][q] *= w[q];  // h
+        sh += g[m][q];
+        shz = __builtin_fmaf(g[m][q], x[m][q], shz);
+      }
+    const float mz = group_sum(shz, lanes) / len;
+    const float mh = N == 1 && ir.scalar ? group_sum(sh, lanes) / len : 0.f;
+    if (!a.gx || !ok) continue;
+#pragma unroll
+    for (int m = 0; m < N; ++m) {
+      float d[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) d[q] = r * (g[m][q] - x[m][q] * mz - mh);
+      qd.store(a.gx + at + m * ir.mul, d);
+    }
+  }
+  if (!a.part) return;
+  // the block's sums: over the groups of a wave by lane swaps, over the waves in order
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    for (int d = lanes; d < 64; d <<= 1) {
+      sw[q] += __shfl_xor(sw[q], d);
+      sb[q] += __shfl_xor(sb[q], d);
+    }
+  const int wave = threadIdx.x >> 6;
+  if ((int)(threadIdx.x & 63) < lanes)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (qd.has(q)) {
+        red[wave][qd.at(q)] = sw[q];
+        red[wave][256 + qd.at(q)] = sb[q];
+      }
+  __syncthreads();
+  float* part = a.part + ir.part_off + (int64_t)rank * ir.mul * (1 + ir.scalar);
+  const int c = threadIdx.x;
+  if (c >= ir.mul) return;
+  part[c] = (red[0][c] + red[1][c]) + (red[2][c] + red[3][c]);
+  if (ir.scalar) part[ir.mul + c] = (red[0][256 + c] + red[1][256 + c]) + (red[2][256 + c] + red[3][256 + c]);
+}
+
+template <typename TX, typename TY>
+__global__ __launch_bounds__(kThreads) void norm_forward_narrow_kernel(const NormArgs /*args*/) {
+  const NormArgs& a = *(const NormArgs*)__builtin_amdgcn_kernarg_segment_ptr();
+  const NormIrrep& ir = find_irrep(a, blockIdx.x);
+  switch (ir.n * 2 + ir.vec) {
+    case 2: forward_narrow<1, false, TX, TY>(a, ir); break;
+    case 3: forward_narrow<1, true, TX, TY>(a, ir); break;
+    case 6: forward_narrow<3, false, TX, TY>(a, ir); break;
+    case 7: forward_narrow<3, true, TX, TY>(a, ir); break;
+    case 10: forward_narrow<5, false, TX, TY>(a, ir); break;
+    case 11: forward_narrow<5, true, TX, TY>(a, ir); break;
+    case 14: forward_narrow<7, false, TX, TY>(a, ir); break;
+    default: forward_narrow<7, true, TX, TY>(a, ir); break;
+  }
+}
+
+template <typename TX>
+__global__ __launch_bounds__(kThreads) void norm_backward_narrow_kernel(const NormArgs /*args*/) {
+  const NormArgs& a = *(const NormArgs*)__builtin_amdgcn_kernarg_segment_ptr();
+  __shared__ float red[4][512];
+  const NormIrrep& ir = find_irrep(a, blockIdx.x);
+  switch (ir.n * 2 + ir.vec) {
+    case 2: backward_narrow<1, false, TX>(a, ir, red); break;
+    case 3: backward_narrow<1, true, TX>(a, ir, red); break;
+    case 6: backward_narrow<3, false, TX>(a, ir, red); break;
+    case 7: backward_narrow<3, true, TX>(a, ir, red); break;
+    case 10: backward_narrow<5, false, TX>(a, ir, red); break;
+    case 11: backward_narrow<5, true, TX>(a, ir, red); break;
+    case 14: backward_narrow<7, false, TX>(a, ir, red); break;
+    default: backward_narrow<7, true, TX>(a, ir, red); break;
+  }
+}
+
+// ---- wide scalar rows (one row of 257 to 8192 channels) ------------------------------
+// A block of threads per node; a thread keeps its 4 V channels of the row, of
+// the weights and of the parameter gradients in registers over all its nodes.
+
+__device__ __forceinline__ void block_sum2(float& u, float& v, float2* tmp) {
+  u = group_sum(u, 64);
+  v = group_sum(v, 64);
+  if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = {u, v};
+  __syncthreads();
+  u = (tmp[0].x + tmp[1].x) + (tmp[2].x + tmp[3].x);
+  v = (tmp[0].y + tmp[1].y) + (tmp[2].y + tmp[3].y);
+  __syncthreads();
+}
+
+template <int V, bool VEC>
+__device__ __forceinline__ Quad<VEC> wide_quad(const NormIrrep& ir, int j) {
+  // VEC: runs of 1024 channels per j; else the four channels of j lie 256 apart
+  Quad<VEC> qd(threadIdx.x, kThreads, ir.mul);
+  qd.c0 += j * 4 * kThreads;
+  return qd;
+}
+
+template <int V, bool VEC, typename TX, typename TY>
+__device__ __forceinline__ void forward_wide(const NormArgs& a, const NormIrrep& ir, float* tmp) {
+  const float len = (float)ir.mul;
+  for (int64_t v = blockIdx.x - ir.first_block; v < a.N; v += ir.blocks) {
+    const int64_t at = v * a.F + ir.off;
+    float x[V][4];
+#pragma unroll
+    for (int j = 0; j < V; ++j) wide_quad<V, VEC>(ir, j).load(static_cast<const TX*>(a.x) + at, true, x[j]);
+    float mu = 0.f, s = 0.f;
+    if (ir.scalar) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) s += (x[j][0] + x[j][1]) + (x[j][2] + x[j][3]);
+      mu = block_sum(s, tmp) / len;
+      s = 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        x[j][q] = wide_quad<V, VEC>(ir, j).has(q) ? x[j][q] - mu : 0.f;
+        s = __builtin_fmaf(x[j][q], x[j][q], s);
+      }
+    const float r = 1.f / sqrtf(block_sum(s, tmp) / len + a.eps);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const Quad<VEC> qd = wide_quad<V, VEC>(ir, j);
+      float w[4], b[4], y[4];
+      qd.load_param(a.w ? a.w + ir.w_off : nullptr, 1.f, w);
+      qd.load_param(ir.scalar && a.b ? a.b + ir.b_off : nullptr, 0.f, b);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) y[q] = __builtin_fmaf(x[j][q] * r, w[q], b[q]);
+      qd.store(static_cast<TY*>(a.y) + at, y);
+    }
+    if (a.stats && threadIdx.x == 0) {
+      float* st = a.stats + (v * a.nirreps + (&ir - a.ir)) * 2;
+      st[0] = mu;
+      st[1] = r;
+    }
+  }
+}
+
+template <int V, bool VEC, typename TX>
+__device__ __forceinline__ void backward_wide(const NormArgs& a, const NormIrrep& ir, float2* tmp) {
+  const float len = (float)ir.mul;
+  const int rank = blockIdx.x - ir.first_block;
+  float w[V][4], sw[V][4], sb[V][4], x[V][4], g[V][4];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    wide_quad<V, VEC>(ir, j).load_param(a.w ? a.w + ir.w_off : nullptr, 1.f, w[j]);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) sw[j][q] = sb[j][q] = 0.f;
+  }
+  for (int64_t v = rank; v < a.N; v += ir.blocks) {
+    const int64_t at = v * a.F + ir.off;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      wide_quad<V, VEC>(ir, j).load(static_cast<const TX*>(a.x) + at, true, x[j]);
+      wide_quad<V, VEC>(ir, j).load(a.gy + at, true, g[j]);
+    }
+    float mu = 0.f, r, none = 0.f;
+    if (a.stats) {
+      const float* st = a.stats + (v * a.nirreps + (&ir - a.ir)) * 2;
+      mu = st[0];
+      r = st[1];
+    } else {
+      if (ir.scalar) {
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) s += (x[j][0] + x[j][1]) + (x[j][2] + x[j][3]);
+        block_sum2(s, none, tmp);
+        mu = s / len;
+      }
+      float s = 0.f;
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float d = wide_quad<V, VEC>(ir, j).has(q) ? x[j][q] - mu : 0.f;
+          s = __builtin_fmaf(d, d, s);
+        }
+      block_sum2(s, none, tmp);
+      r = 1.f / sqrtf(s / len + a.eps);
+    }
+    float sh = 0.f, shz = 0.f;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        // (past the row z is not zero, but its g is)
+        x[j][q] = (x[j][q] - mu) * r;
+        const float h = g[j][q] * w[j][q];
+        sw[j][q] = __builtin_fmaf(g[j][q], x[j][q], sw[j][q]);
+        sb[j][q] += g[j][q];
+        sh += h;
+        shz = __builtin_fmaf(h, x[j][q], shz);
+      }
+    block_sum2(sh, shz, tmp);
+    const float mz = shz / len, mh = ir.scalar ? sh / len : 0.f;
+    if (!a.gx) continue;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      float d[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) d[q] = r * (g[j][q] * w[j][q] - x[j][q] * mz - mh);
+      wide_quad<V, VEC>(ir, j).store(a.gx + at, d);
+    }
+  }
+  if (!a.part) return;
+  float* part = a.part + ir.part_off + (int64_t)rank * ir.mul * (1 + ir.scalar);
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const Quad<VEC> qd = wide_quad<V, VEC>(ir, j);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (qd.has(q)) {
+        part[qd.at(q)] = sw[j][q];
+        if (ir.scalar) part[ir.mul + qd.at(q)] = sb[j][q];
+      }
+  }
+}
+
+template <int V, typename TX, typename TY>
+__global__ __launch_bounds__(kThreads) void norm_forward_wide_kernel(const NormArgs /*args*/) {
+  const NormArgs& a = *(const NormArgs*)__builtin_amdgcn_kernarg_segment_ptr();
+  __shared__ float tmp[4];
+  const NormIrrep& ir = find_irrep(a, blockIdx.x);
+  if (ir.vec)
+    forward_wide<V, true, TX, TY>(a, ir, tmp);
+  else
+    forward_wide<V, false, TX, TY>(a, ir, tmp);
+}
+
+template <int V, typename TX>
+__global__ __launch_bounds__(kThreads) void norm_backward_wide_kernel(const NormArgs /*args*/) {
+  const NormArgs& a = *(const NormArgs*)__builtin_amdgcn_kernarg_segment_ptr();
+  __shared__ float2 tmp[4];
+  const NormIrrep& ir = find_irrep(a, blockIdx.x);
+  if (ir.vec)
+    backward_wide<V, true, TX>(a, ir, tmp);
+  else
+    backward_wide<V, false, TX>(a, ir, tmp);
+}
+
+// ---- everything else (several rows of more than 256 channels, longer rows) -----------
+// A block of threads per (node, irrep) that reads the block again for each sum.
+
 // Mean and 1 / deviation of one block of values, one thread block per (node, irrep).
 template <typename TX>
 __device__ __forceinline__ void block_stats(const void* x, int64_t at, const NormIrrep& ir, float eps, float* tmp,
@@ -161,16 +559,29 @@ __global__ __launch_bounds__(kThreads) void norm_backward_kernel(const NormArgs 
   }
 }
 
-// One thread per parameter of an irrep: the blocks' sums in order.
-__global__ __launch_bounds__(kThreads) void norm_reduce_kernel(const NormArgs /*args*/) {
+// The blocks' sums of 32 parameters of an irrep: 32 threads per parameter take
+// every 32nd block each, and their sums are added in order.
+__global__ __launch_bounds__(1024) void norm_reduce_kernel(const NormArgs /*args*/) {
   const NormArgs& a = *(const NormArgs*)__builtin_amdgcn_kernarg_segment_ptr();
+  __shared__ float red[32][33];
   const NormIrrep& ir = a.ir[blockIdx.y];
-  const int c = blockIdx.x * kThreads + threadIdx.x;
-  const int len = ir.mul * (1 + ir.scalar);
-  if (c >= len) return;
-  const float* p = a.part + ir.part_off + c;
+  const int len = ir.mul * (1 + ir.scalar), col = threadIdx.x & 31, row = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + col;
+  if ((int)blockIdx.x * 32 >= len) return;
   float s = 0.f;
-  for (int k = 0; k < ir.blocks; ++k) s += p[(int64_t)k * len];
+  if (c < len) {
+    const float* p = a.part + ir.part_off + c;
+#pragma unroll 8
+    for (int k = row; k < ir.blocks; k += 32) s += p[(int64_t)k * len];
+  }
+  red[row][col] = s;
+  __syncthreads();
+  for (int h = 16; h > 0; h >>= 1) {
+    if (row < h) red[row][col] += red[row + h][col];
+    __syncthreads();
+  }
+  if (row != 0 || c >= len) return;
+  s = red[0][col];
   if (c < ir.mul) {
     if (a.gw) a.gw[ir.w_off + c] = s;
   } else if (a.gb) {
@@ -178,16 +589,71 @@ __global__ __launch_bounds__(kThreads) void norm_reduce_kernel(const NormArgs /*
   }
 }
 
+enum Kind { kNarrow = 0, kWide1, kWide2, kWide4, kWide8, kLong, kKinds };
+
+// How an irrep's blocks are computed, and its vector width: VEC needs every
+// row of the block to start on four elements of an aligned tensor.
+int irrep_kind(const NormIrrep& ir) {
+  if (ir.mul <= 256) return kNarrow;
+  if (ir.n > 1 || ir.mul > 8192) return kLong;
+  return ir.mul <= 1024 ? kWide1 : ir.mul <= 2048 ? kWide2 : ir.mul <= 4096 ? kWide4 : kWide8;
+}
+
+void set_irreps(NormArgs& a) {
+  auto aligned = [](const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; };
+  const bool base = aligned(a.x, a.x_bf16 ? 8 : 16) && aligned(a.y, a.y_bf16 ? 8 : 16) && aligned(a.gy, 16) &&
+                    aligned(a.gx, 16) && a.F % 4 == 0;
+  for (int i = 0; i < a.nirreps; ++i) {
+    NormIrrep& ir = a.ir[i];
+    ir.vec = base && ir.mul % 4 == 0 && ir.off % 4 == 0;
+    ir.lanes = 1;
+    while (ir.lanes < 64 && ir.lanes * 4 < ir.mul) ir.lanes *= 2;
+  }
+}
+
+// The irreps of one kind as a launch of their own.
+int64_t kind_args(const NormArgs& a, int kind, NormArgs& k) {
+  k = a;
+  int64_t blocks = 0;
+  for (int i = 0; i < a.nirreps; ++i) {
+    NormIrrep& ir = k.ir[i];
+    if (irrep_kind(ir) != kind) ir.blocks = 0;
+    ir.first_block = (int32_t)blocks;
+    blocks += ir.blocks;
+  }
+  return blocks;
+}
+
+#define TP_NORM_XY(KERNEL, ...)                                                                          \
+  (a.x_bf16 ? (a.y_bf16 ? (const void*)KERNEL<__VA_ARGS__ uint16_t, uint16_t>                            \
+                        : (const void*)KERNEL<__VA_ARGS__ uint16_t, float>)                              \
+            : (a.y_bf16 ? (const void*)KERNEL<__VA_ARGS__ float, uint16_t> : (const void*)KERNEL<__VA_ARGS__ float, float>))
+#define TP_NORM_X(KERNEL, ...) \
+  (a.x_bf16 ? (const void*)KERNEL<__VA_ARGS__ uint16_t> : (const void*)KERNEL<__VA_ARGS__ float>)
+#define TP_COMMA ,
+
+hipError_t launch(const void* kernel, NormArgs& k, int64_t blocks, hipStream_t s) {
+  void* args[] = {&k};
+  return hipLaunchKernel(kernel, dim3((unsigned)blocks), dim3(kThreads), args, 0, s);
+}
+
 }  // namespace
 
 int64_t norm_backward_blocks(NormArgs& a) {
-  int32_t first = 0;
-  int64_t part = 0;
+  // about 2048 blocks of narrow irreps, shared by their sizes; 512 per wider irrep, whose rows of
+  // partial sums are as long as the irrep (8 KiB per block at 1024 scalar channels)
+  int64_t total = 0, part = 0;
+  for (int i = 0; i < a.nirreps; ++i) total += irrep_kind(a.ir[i]) == kNarrow ? (int64_t)a.ir[i].mul * a.ir[i].n : 0;
+  set_irreps(a);
   for (int i = 0; i < a.nirreps; ++i) {
     NormIrrep& ir = a.ir[i];
-    ir.first_block = first;
-    ir.blocks = (int32_t)(a.N < 512 ? (a.N > 0 ? a.N : 1) : 512);
-    first += ir.blocks;
+    int64_t most = a.N, want = 512;
+    if (irrep_kind(ir) == kNarrow) {
+      const int per = kThreads / ir.lanes;
+      most = (a.N + per - 1) / per;
+      want = 2048 * (int64_t)ir.mul * ir.n / total + 1;
+    }
+    ir.blocks = (int32_t)(want < most ? want : most > 0 ? most : 1);
     ir.part_off = part;
     part += (int64_t)ir.blocks * ir.mul * (1 + ir.scalar);
   }
@@ -196,39 +662,52 @@ int64_t norm_backward_blocks(NormArgs& a) {
 
 hipError_t launch_norm_forward(NormArgs& a, hipStream_t s) {
   TimingScope ts(kcNorm, s);
-  int32_t first = 0;
+  set_irreps(a);
   for (int i = 0; i < a.nirreps; ++i) {
-    a.ir[i].first_block = first;
-    a.ir[i].blocks = (int32_t)(a.N < 65536 ? a.N : 65536);
-    first += a.ir[i].blocks;
+    NormIrrep& ir = a.ir[i];
+    const int per = irrep_kind(ir) == kNarrow ? kThreads / ir.lanes : 1;
+    const int64_t n = (a.N + per - 1) / per;
+    ir.blocks = (int32_t)(n < 65536 ? n : 65536);
   }
-  const dim3 g((unsigned)first), b(kThreads);
-  if (a.x_bf16 && a.y_bf16)
-    hipLaunchKernelGGL((norm_forward_kernel<uint16_t, uint16_t>), g, b, 0, s, a);
-  else if (a.x_bf16)
-    hipLaunchKernelGGL((norm_forward_kernel<uint16_t, float>), g, b, 0, s, a);
-  else if (a.y_bf16)
-    hipLaunchKernelGGL((norm_forward_kernel<float, uint16_t>), g, b, 0, s, a);
-  else
-    hipLaunchKernelGGL((norm_forward_kernel<float, float>), g, b, 0, s, a);
-  return hipGetLastError();
+  for (int kind = 0; kind < kKinds; ++kind) {
+    NormArgs k;
+    const int64_t blocks = kind_args(a, kind, k);
+    if (blocks == 0) continue;
+    const void* f = kind == kNarrow  ? TP_NORM_XY(norm_forward_narrow_kernel, )
+                    : kind == kWide1 ? TP_NORM_XY(norm_forward_wide_kernel, 1 TP_COMMA)
+                    : kind == kWide2 ? TP_NORM_XY(norm_forward_wide_kernel, 2 TP_COMMA)
+                    : kind == kWide4 ? TP_NORM_XY(norm_forward_wide_kernel, 4 TP_COMMA)
+                    : kind == kWide8 ? TP_NORM_XY(norm_forward_wide_kernel, 8 TP_COMMA)
+                                     : TP_NORM_XY(norm_forward_kernel, );
+    const hipError_t e = launch(f, k, blocks, s);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 hipError_t launch_norm_backward(NormArgs& a, hipStream_t s) {
   TimingScope ts(kcNorm, s);
   norm_backward_blocks(a);
-  const NormIrrep& last = a.ir[a.nirreps - 1];
-  const dim3 g((unsigned)(last.first_block + last.blocks)), b(kThreads);
-  if (a.x_bf16)
-    hipLaunchKernelGGL((norm_backward_kernel<uint16_t>), g, b, 0, s, a);
-  else
-    hipLaunchKernelGGL((norm_backward_kernel<float>), g, b, 0, s, a);
-  if (a.part) {
-    int most = 0;
-    for (int i = 0; i < a.nirreps; ++i) most = a.ir[i].mul * (1 + a.ir[i].scalar) > most ? a.ir[i].mul * (1 + a.ir[i].scalar) : most;
-    hipLaunchKernelGGL(norm_reduce_kernel, dim3((unsigned)((most + kThreads - 1) / kThreads), (unsigned)a.nirreps), b,
-                       0, s, a);
+  for (int kind = 0; kind < kKinds; ++kind) {
+    NormArgs k;
+    const int64_t blocks = kind_args(a, kind, k);
+    if (blocks == 0) continue;
+    const void* f = kind == kNarrow  ? TP_NORM_X(norm_backward_narrow_kernel, )
+                    : kind == kWide1 ? TP_NORM_X(norm_backward_wide_kernel, 1 TP_COMMA)
+                    : kind == kWide2 ? TP_NORM_X(norm_backward_wide_kernel, 2 TP_COMMA)
+                    : kind == kWide4 ? TP_NORM_X(norm_backward_wide_kernel, 4 TP_COMMA)
+                    : kind == kWide8 ? TP_NORM_X(norm_backward_wide_kernel, 8 TP_COMMA)
+                                     : TP_NORM_X(norm_backward_kernel, );
+    const hipError_t e = launch(f, k, blocks, s);
+    if (e != hipSuccess) return e;
   }
+  if (!a.part) return hipSuccess;
+  int most = 0;
+  for (int i = 0; i < a.nirreps; ++i) {
+    const int len = a.ir[i].mul * (1 + a.ir[i].scalar);
+    most = len > most ? len : most;
+  }
+  hipLaunchKernelGGL(norm_reduce_kernel, dim3((unsigned)((most + 31) / 32), (unsigned)a.nirreps), dim3(1024), 0, s, a);
   return hipGetLastError();
 }
 
