@@ -97,8 +97,9 @@ void rows_args(const tpconv_linear_s& h, bool grad, int64_t N, const int32_t* of
   a.in = in;
   a.W = W;
   a.out = out;
-  // 16-byte loads: every row of the tensor and every block within it starts on 16 bytes
-  const int xm = a.in_bf16 ? 8 : 4, wm = a.w_bf16 ? 8 : 4;
+  // wide loads (16 bytes along the reduction; channel pairs of W in the forward): every row of
+  // the tensor and every block within it starts on such a boundary
+  const int xm = a.in_bf16 ? 8 : 4, wm = grad ? (a.w_bf16 ? 8 : 4) : 2;
   a.vec_x = aligned16(in) && a.F_in % xm == 0;
   for (const auto& r : from) a.vec_x = a.vec_x && r.mul % xm == 0;
   a.vec_w = aligned16(W) && h.w_numel % wm == 0;
@@ -137,6 +138,12 @@ void gw_args(const tpconv_linear_s& h, int64_t N, const int32_t* offsets, const 
   a.gy = gy;
   a.gW = gW;
   a.part = part;
+  // channel pairs in one load: every row of every block starts on two elements of an aligned tensor
+  auto aligned = [](const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; };
+  a.vec_x = aligned(x, a.x_bf16 ? 4 : 8) && h.F_in % 2 == 0;
+  for (const auto& r : h.in) a.vec_x = a.vec_x && r.mul % 2 == 0;
+  a.vec_y = aligned(gy, 8) && h.F_out % 2 == 0;
+  for (const auto& r : h.out) a.vec_y = a.vec_y && r.mul % 2 == 0;
   for (const auto& b : h.blocks) {
     LinGwJob& J = a.job[a.njobs++];
     J.n = b.n;

@@ -90,6 +90,7 @@ struct LinRowsArgs {
 // Weight-gradient kernel: W_g[c][c'] = sum over the rows (v, m) of group g in[(v, m), c] gy[(v, m), c'].
 struct LinGwJob {
   int32_t n, mi, mo, xoff, yoff;
+  int32_t width;        // tile width
   int32_t tiles_i, tiles_o;
   int32_t rshift;       // rows per slot = 1 << rshift
   int64_t woff;

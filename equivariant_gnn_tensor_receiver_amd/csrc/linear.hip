@@ -24,6 +24,8 @@
 #include "layers.h"
 #include "timing.h"
 
+#include <type_traits>
+
 namespace tpconv {
 
 namespace {
@@ -83,32 +85,58 @@ __device__ __forceinline__ int64_t div_rows(int64_t r, int n) {
   return n == 1 ? r : n == 3 ? r / 3 : n == 5 ? r / 5 : r / 7;
 }
 
-// Eight values along the reduction: p[0..8) where k + j < len, else zero.
+// Eight values along the reduction of one row: p[k..k+8), as loaded.  Reads
+// past `len` are moved inside the row (vec: len is a multiple of the vector)
+// and the values zeroed by mask_run8 before use, so every load is issued
+// unconditionally and can stay in flight while the previous chunk is multiplied.
 __device__ __forceinline__ void load_run8(const float* p, int k, int len, bool vec, float (&v)[8]) {
   if (vec) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      floatx4 x = {0.f, 0.f, 0.f, 0.f};
-      if (k + 4 * j < len) x = *reinterpret_cast<const floatx4*>(p + 4 * j);
+      const floatx4 x = *reinterpret_cast<const floatx4*>(p + min(k + 4 * j, len - 4));
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[4 * j + e] = x[e];
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = k + j < len ? p[j] : 0.f;
+    for (int j = 0; j < 8; ++j) v[j] = p[min(k + j, len - 1)];
   }
 }
 __device__ __forceinline__ void load_run8(const uint16_t* p, int k, int len, bool vec, u32x4& v) {
   if (vec) {
-    v = (u32x4){0, 0, 0, 0};
-    if (k < len) v = *reinterpret_cast<const u32x4*>(p);
+    v = *reinterpret_cast<const u32x4*>(p + min(k, len - 8));
   } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t a = k + 2 * j < len ? p[2 * j] : 0, b = k + 2 * j + 1 < len ? p[2 * j + 1] : 0;
-      v[j] = a | (b << 16);
-    }
+    for (int j = 0; j < 4; ++j)
+      v[j] = (uint32_t)p[min(k + 2 * j, len - 1)] | ((uint32_t)p[min(k + 2 * j + 1, len - 1)] << 16);
   }
+}
+// Zeroes the values j >= left.
+__device__ __forceinline__ void mask_run8(float (&v)[8], int left) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = j < left ? v[j] : 0.f;
+}
+__device__ __forceinline__ void mask_run8(u32x4& v, int left) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    v[j] = 2 * j + 1 < left ? v[j] : 2 * j < left ? v[j] & 0xffffu : 0u;
+}
+
+// Two neighbouring columns c, c + 1 of one row (c + 1 may lie past `cols`: a
+// value from inside the row, its column is never stored).
+__device__ __forceinline__ void load_pair(const float* p, int c, int cols, bool vec, float& a, float& b) {
+  if (vec) {
+    const float2 x = *reinterpret_cast<const float2*>(p + min(c, cols - 2));
+    a = x.x;
+    b = x.y;
+  } else {
+    a = p[min(c, cols - 1)];
+    b = p[min(c + 1, cols - 1)];
+  }
+}
+__device__ __forceinline__ uint32_t load_pair(const uint16_t* p, int c, int cols, bool vec) {
+  if (vec) return *reinterpret_cast<const uint32_t*>(p + min(c, cols - 2));
+  return (uint32_t)p[min(c, cols - 1)] | ((uint32_t)p[min(c + 1, cols - 1)] << 16);
 }
 
 template <typename T>
@@ -135,22 +163,83 @@ __device__ __forceinline__ void put_run8(uint16_t (*s)[ROWS][LD], int row, int k
   *reinterpret_cast<u32x4*>(&s[0][row][k]) = v;
 }
 
+// The values one thread loads of an operand for one chunk.
+// RunPart: rows of the operand, eight reductions each, contiguous in memory.
 template <typename T>
-struct Run8;
+struct Raw8;
 template <>
-struct Run8<float> {
+struct Raw8<float> {
   float v[8];
-  __device__ __forceinline__ void set(int j, float x) { v[j] = x; }
-  __device__ __forceinline__ void clear() {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = 0.f;
-  }
 };
 template <>
-struct Run8<uint16_t> {
+struct Raw8<uint16_t> {
   u32x4 v;
-  __device__ __forceinline__ void set(int j, uint16_t x) { v[j >> 1] |= (uint32_t)x << (16 * (j & 1)); }
-  __device__ __forceinline__ void clear() { v = (u32x4){0, 0, 0, 0}; }
+};
+
+template <typename T, int ROWS, int KC>
+struct RunPart {
+  static constexpr int kPer = KC / 8;                        // threads per row
+  static constexpr int kPasses = (ROWS * kPer + kThreads - 1) / kThreads;
+  static constexpr bool kWhole = ROWS * kPer >= kThreads;    // else the first threads alone
+  Raw8<T> raw[kPasses];
+  static __device__ __forceinline__ bool mine() { return kWhole || (int)threadIdx.x < ROWS * kPer; }
+  static __device__ __forceinline__ int row(int p) { return p * (kThreads / kPer) + (int)threadIdx.x / kPer; }
+  static __device__ __forceinline__ int k() { return ((int)threadIdx.x % kPer) * 8; }
+  template <int LD>
+  __device__ __forceinline__ void put(uint16_t (*s)[ROWS][LD], int left) {
+    if (!mine()) return;
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+      if (left < KC) mask_run8(raw[p].v, left - k());  // `left` is uniform
+      put_run8<LD, ROWS>(s, row(p), k(), raw[p].v);
+    }
+  }
+};
+
+// PairPart: rows of the operand are columns of the memory; a thread takes two
+// neighbouring columns and eight reductions, and turns them in registers.
+template <typename T, int ROWS, int KC>
+struct PairPart {
+  static constexpr int kPer = ROWS / 2;  // threads per reduction group
+  static constexpr int kPasses = (kPer * (KC / 8) + kThreads - 1) / kThreads;
+  static constexpr bool kWhole = kPer * (KC / 8) >= kThreads;
+  float f[sizeof(T) == 4 ? kPasses : 1][2][8];
+  uint32_t h[sizeof(T) == 2 ? kPasses : 1][8];
+  static __device__ __forceinline__ bool mine() { return kWhole || (int)threadIdx.x < kPer * (KC / 8); }
+  static __device__ __forceinline__ int col() { return 2 * ((int)threadIdx.x % kPer); }
+  static __device__ __forceinline__ int k(int p) { return (p * (kThreads / kPer) + (int)threadIdx.x / kPer) * 8; }
+  __device__ __forceinline__ void load(int p, int j, const float* at, int c, int cols, bool vec) {
+    load_pair(at, c, cols, vec, f[p][0][j], f[p][1][j]);
+  }
+  __device__ __forceinline__ void load(int p, int j, const uint16_t* at, int c, int cols, bool vec) {
+    h[p][j] = load_pair(at, c, cols, vec);
+  }
+  template <int LD>
+  __device__ __forceinline__ void put(uint16_t (*s)[ROWS][LD], int left) {
+    if (!mine()) return;
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+      if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if (left < KC) mask_run8(f[p][e], left - k(p));
+          put_run8<LD, ROWS>(s, col() + e, k(p), f[p][e]);
+        }
+      } else {
+        u32x4 v[2];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          v[0][j] = __builtin_amdgcn_perm(h[p][2 * j + 1], h[p][2 * j], 0x05040100);
+          v[1][j] = __builtin_amdgcn_perm(h[p][2 * j + 1], h[p][2 * j], 0x07060302);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if (left < KC) mask_run8(v[e], left - k(p));
+          put_run8<LD, ROWS>(s, col() + e, k(p), v[e]);
+        }
+      }
+    }
+  }
 };
 
 // acc += A B over the k16 steps of this wave from the staged planes.
@@ -192,175 +281,257 @@ __device__ __forceinline__ void store_out(uint16_t* p, int64_t i, float v) {
   p[i] = __builtin_bit_cast(uint16_t, (__bf16)v);
 }
 
-// 32 x 32 tiles; the block's four waves take a quarter of every 128-long chunk
-// of the reduction each, and their sums are added in order through LDS.
-constexpr int kBM = 32, kBN = 32, kKC = 128, kLD = kKC + 8;  // rows padded by 16 bytes: conflict-free 16-byte reads
+// Tile shapes.  A block of four waves computes BM x BN; with KS = 1 its waves
+// take WM x WN each, with KS = 4 every wave takes a quarter of the reduction of
+// the whole tile and the sums are added in order through LDS.  LDS rows are
+// padded by 16 bytes, so 16-byte reads of 16 rows touch every bank once.
+template <int BM_, int BN_, int WM_, int WN_, int KS_, int KC_>
+struct Shape {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, KS = KS_, KC = KC_, LD = KC_ + 8;
+  static constexpr int MT = WM / 32, NT = WN / 32;
+  static_assert((BM / WM) * (BN / WN) * KS == kThreads / 64, "four waves");
+};
 
-template <typename TI, typename TW, typename TO>
-__global__ __launch_bounds__(kThreads) void lin_rows_kernel(const LinRowsArgs /*args*/) {
-  const LinRowsArgs& a = *(const LinRowsArgs*)__builtin_amdgcn_kernarg_segment_ptr();
-  constexpr int PA = Planes<TI>::count, PB = Planes<TW>::count;
-  __shared__ __align__(16) uint16_t sa[PA][kBM][kLD];
-  __shared__ __align__(16) uint16_t sb[PB][kBN][kLD];
-  __shared__ float part[3][kBM * kBN];
-  __shared__ int32_t s_node[kBM], s_m[kBM];
-  int ji = 0;
-  while (ji + 1 < a.njobs && (int64_t)blockIdx.x >= a.job[ji + 1].first_tile) ++ji;
-  const LinJob& J = a.job[ji];
-  const int64_t lt = blockIdx.x - J.first_tile;
-  const int64_t tm = lt / J.tiles_n;
-  const int n0 = (int)(lt - tm * J.tiles_n) * kBN;
-  Slot s;
-  if (!find_slot(a.offsets, a.G, a.N, J.n, 5, tm, s)) return;
-  const int tid = threadIdx.x, wave = tid >> 6;
-  if (tid < kBM) {
-    const int64_t r = s.row0 + tid;
-    int32_t node = -1, m = 0;
-    if (r < s.rows) {
-      const int64_t p = div_rows(r, J.n);
-      m = (int32_t)(r - p * J.n);
-      node = a.order ? a.order[s.node0 + p] : (int32_t)p;
-    }
-    s_node[tid] = node;
-    s_m[tid] = m;
-  }
-  __syncthreads();
-  floatx16 acc[1][1];
+constexpr int max_int(int a, int b) { return a > b ? a : b; }
+
+// LDS bytes of a shape: the operands' planes, later the partial sums of KS > 1.
+template <typename S, int PA, int PB>
+constexpr int lds_bytes() {
+  return max_int((PA * S::BM + PB * S::BN) * S::LD * 2, (S::KS - 1) * S::BM * S::BN * 4);
+}
+
+// Adds the waves' sums of KS > 1 in order; the result is wave 0's.
+template <typename S>
+__device__ __forceinline__ void join_waves(floatx16 (&acc)[S::MT][S::NT], char* smem) {
+  if constexpr (S::KS > 1) {
+    static_assert(S::MT == 1 && S::NT == 1, "one tile per wave");
+    float(*part)[S::BM * S::BN] = reinterpret_cast<float(*)[S::BM * S::BN]>(smem);
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    if (wave > 0)
 #pragma unroll
-  for (int r = 0; r < 16; ++r) acc[0][0][r] = 0.f;
-  const TI* in = static_cast<const TI*>(a.in);
-  const TW* Wg = static_cast<const TW*>(a.W) + s.g * a.w_per_group;
-  for (int si = 0; si < J.nseg; ++si) {
-    const LinSeg& S = a.seg[J.seg0 + si];
-    for (int k0 = 0; k0 < S.len; k0 += kKC) {
-      // A: 16 threads per row, eight reductions each
-      for (int p = 0; p < kBM * (kKC / 8) / kThreads; ++p) {
-        const int row = p * (kThreads / (kKC / 8)) + tid / (kKC / 8), kk = (tid % (kKC / 8)) * 8;
-        Run8<TI> v;
-        v.clear();
-        const int32_t node = s_node[row];
-        if (node >= 0 && k0 + kk < S.len)
-          load_run8(in + (int64_t)node * a.F_in + S.off + (int64_t)s_m[row] * S.len + k0 + kk, k0 + kk, S.len, a.vec_x, v.v);
-        put_run8<kLD, kBM>(sa, row, kk, v.v);
-      }
-      if (a.wt) {  // B(k, c') = W[c'][k]: contiguous along the reduction
-        for (int p = 0; p < kBN * (kKC / 8) / kThreads; ++p) {
-          const int col = p * (kThreads / (kKC / 8)) + tid / (kKC / 8), kk = (tid % (kKC / 8)) * 8;
-          Run8<TW> v;
-          v.clear();
-          if (n0 + col < J.cols && k0 + kk < S.len)
-            load_run8(Wg + S.woff + (int64_t)(n0 + col) * S.ldw + k0 + kk, k0 + kk, S.len, a.vec_w, v.v);
-          put_run8<kLD, kBN>(sb, col, kk, v.v);
-        }
-      } else {  // B(k, c') = W[k][c']: a thread takes eight reductions of one column
-        for (int p = 0; p < kBN * (kKC / 8) / kThreads; ++p) {
-          const int col = tid % kBN, kk = (p * (kThreads / kBN) + tid / kBN) * 8;
-          Run8<TW> v;
-          v.clear();
-          if (n0 + col < J.cols)
+      for (int r = 0; r < 16; ++r) part[wave - 1][r * 64 + lane] = acc[0][0][r];
+    __syncthreads();
+    if (wave == 0)
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (k0 + kk + j < S.len) v.set(j, Wg[S.woff + (int64_t)(k0 + kk + j) * S.ldw + n0 + col]);
-          put_run8<kLD, kBN>(sb, col, kk, v.v);
-        }
-      }
-      __syncthreads();
-      const int kw = wave * (kKC / 4);  // a wave without reductions left skips its products
-      if (k0 + kw < S.len) multiply<PA, PB, 1, 1, kBM, kBN, kLD>(sa, sb, 0, 0, kw, kKC / 64, acc);
-      __syncthreads();
-    }
-  }
-  const int lane = tid & 63;
-  if (wave > 0)
-#pragma unroll
-    for (int r = 0; r < 16; ++r) part[wave - 1][r * 64 + lane] = acc[0][0][r];
-  __syncthreads();
-  if (wave > 0) return;
-  const int col = n0 + (lane & 31);
-#pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    const float v = ((acc[0][0][r] + part[0][r * 64 + lane]) + part[1][r * 64 + lane]) + part[2][r * 64 + lane];
-    const int row = acc_row(r);
-    if (s_node[row] >= 0 && col < J.cols)
-      store_out(static_cast<TO*>(a.out), (int64_t)s_node[row] * a.F_out + J.off + (int64_t)s_m[row] * J.cols + col, v);
+      for (int r = 0; r < 16; ++r)
+        for (int w = 0; w < S::KS - 1; ++w) acc[0][0][r] += part[w][r * 64 + lane];
   }
 }
 
-// Weight gradient: one 32 x 32 tile of gW_g over the rows of one slot.  A group
+template <typename S, typename TI, typename TW, typename TO, bool WT>
+__global__ __launch_bounds__(kThreads, 2) void lin_rows_kernel(const LinRowsArgs /*args*/) {
+  const LinRowsArgs& a = *(const LinRowsArgs*)__builtin_amdgcn_kernarg_segment_ptr();
+  constexpr int PA = Planes<TI>::count, PB = Planes<TW>::count, BM = S::BM, BN = S::BN, KC = S::KC, LD = S::LD;
+  __shared__ __align__(16) char smem[lds_bytes<S, PA, PB>()];
+  __shared__ int32_t s_node[BM], s_m[BM];
+  uint16_t(*sa)[BM][LD] = reinterpret_cast<uint16_t(*)[BM][LD]>(smem);
+  uint16_t(*sb)[BN][LD] = reinterpret_cast<uint16_t(*)[BN][LD]>(smem + PA * BM * LD * 2);
+  // consecutive tiles (the column tiles of one row tile, then its group's next
+  // rows) run on one XCD and share its L2
+  const int64_t tile = xcd_item(blockIdx.x, gridDim.x);
+  if (tile >= a.tiles) return;
+  int ji = 0;
+  while (ji + 1 < a.njobs && tile >= a.job[ji + 1].first_tile) ++ji;
+  const LinJob& J = a.job[ji];
+  const int64_t lt = tile - J.first_tile;
+  const int64_t tm = lt / J.tiles_n;
+  const int n0 = (int)(lt - tm * J.tiles_n) * BN;
+  Slot s;
+  constexpr int kShift = BM == 128 ? 7 : BM == 64 ? 6 : 5;
+  static_assert(BM == 1 << kShift, "row tile");
+  if (!find_slot(a.offsets, a.G, a.N, J.n, kShift, tm, s)) return;
+  const int tid = threadIdx.x, wave = tid >> 6;
+  if (tid < BM) {
+    const int64_t r = s.row0 + tid;
+    const int64_t rr = min(r, s.rows - 1);  // rows past the end repeat the last one and are not stored
+    const int64_t p = div_rows(rr, J.n);
+    const int32_t node = a.order ? a.order[s.node0 + p] : (int32_t)p;
+    s_node[tid] = node;
+    s_m[tid] = r < s.rows ? (int32_t)(rr - p * J.n) : -1 - (int32_t)(rr - p * J.n);
+  }
+  __syncthreads();
+  floatx16 acc[S::MT][S::NT];
+#pragma unroll
+  for (int i = 0; i < S::MT; ++i)
+#pragma unroll
+    for (int j = 0; j < S::NT; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+  const TI* in = static_cast<const TI*>(a.in);
+  const TW* Wg = static_cast<const TW*>(a.W) + s.g * a.w_per_group;
+
+  using PartA = RunPart<TI, BM, KC>;
+  using PartB = std::conditional_t<WT, RunPart<TW, BN, KC>, PairPart<TW, BN, KC>>;
+  PartA pa;
+  PartB pb;
+  const TI* row_ptr[PartA::kPasses];
+  int row_m[PartA::kPasses];
+#pragma unroll
+  for (int p = 0; p < PartA::kPasses; ++p) {
+    const int m = s_m[PartA::row(p) % BM];
+    row_m[p] = m < 0 ? -1 - m : m;
+    row_ptr[p] = in + (int64_t)s_node[PartA::row(p) % BM] * a.F_in;
+  }
+  auto load = [&](const LinSeg& G, int k0) {
+#pragma unroll
+    for (int p = 0; p < PartA::kPasses; ++p)
+      if (PartA::mine()) load_run8(row_ptr[p] + G.off + row_m[p] * G.len, k0 + PartA::k(), G.len, a.vec_x, pa.raw[p].v);
+    if (PartB::mine()) {
+      if constexpr (WT) {  // B(k, c') = W[c'][k]
+#pragma unroll
+        for (int p = 0; p < PartB::kPasses; ++p)
+          load_run8(Wg + G.woff + (int64_t)min(n0 + PartB::row(p), J.cols - 1) * G.ldw, k0 + PartB::k(), G.len, a.vec_w,
+                    pb.raw[p].v);
+      } else {  // B(k, c') = W[k][c']
+#pragma unroll
+        for (int p = 0; p < PartB::kPasses; ++p)
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            pb.load(p, j, Wg + G.woff + (int64_t)min(k0 + PartB::k(p) + j, G.len - 1) * G.ldw, n0 + PartB::col(), J.cols,
+                    a.vec_w);
+      }
+    }
+  };
+  int si = 0, k0 = 0;
+  if (J.nseg > 0) load(a.seg[J.seg0], 0);
+  while (si < J.nseg) {
+    const int left = a.seg[J.seg0 + si].len - k0;
+    pa.template put<LD>(sa, left);
+    pb.template put<LD>(sb, left);
+    __syncthreads();
+    k0 += KC;
+    if (left <= KC) {
+      k0 = 0;
+      ++si;
+    }
+    if (si < J.nseg) load(a.seg[J.seg0 + si], k0);
+    if constexpr (S::KS > 1) {
+      const int kw = wave * (KC / S::KS);  // a wave without reductions left skips its products
+      if (kw < left) multiply<PA, PB, S::MT, S::NT, BM, BN, LD>(sa, sb, 0, 0, kw, KC / (16 * S::KS), acc);
+    } else {
+      constexpr int kCols = BN / S::WN;
+      multiply<PA, PB, S::MT, S::NT, BM, BN, LD>(sa, sb, (wave / kCols) * S::WM, (wave % kCols) * S::WN, 0, KC / 16, acc);
+    }
+    __syncthreads();
+  }
+  join_waves<S>(acc, smem);
+  if (S::KS > 1 && wave > 0) return;
+  constexpr int kCols = S::KS > 1 ? 1 : BN / S::WN;
+  const int mw = (wave / kCols) * S::WM, nw = (wave % kCols) * S::WN;
+#pragma unroll
+  for (int i = 0; i < S::MT; ++i)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int row = mw + 32 * i + acc_row(r), m = s_m[row];
+      TO* out = static_cast<TO*>(a.out) + (int64_t)s_node[row] * a.F_out + J.off + (int64_t)m * J.cols;
+#pragma unroll
+      for (int j = 0; j < S::NT; ++j) {
+        const int col = n0 + nw + 32 * j + (tid & 31);
+        if (m >= 0 && col < J.cols) store_out(out, col, acc[i][j][r]);
+      }
+    }
+}
+
+// Weight gradient: one BM x BN tile of gW_g over the rows of one slot.  A group
 // with a single slot is written at once, others through partial sums that
 // lin_gw_reduce_kernel adds in order.
-template <typename TX>
-__global__ __launch_bounds__(kThreads) void lin_gw_kernel(const LinGwArgs /*args*/) {
+constexpr int kRowTable = 512;  // rows of a slot whose addresses are in LDS at a time
+
+template <typename S, typename TX>
+__global__ __launch_bounds__(kThreads, 2) void lin_gw_kernel(const LinGwArgs /*args*/) {
   const LinGwArgs& a = *(const LinGwArgs*)__builtin_amdgcn_kernarg_segment_ptr();
-  constexpr int PA = Planes<TX>::count, PB = 3;
-  __shared__ __align__(16) uint16_t sa[PA][kBM][kLD];
-  __shared__ __align__(16) uint16_t sb[PB][kBN][kLD];
-  __shared__ float part[3][kBM * kBN];
-  __shared__ int32_t s_node[kKC], s_m[kKC];
+  constexpr int PA = Planes<TX>::count, PB = 3, BM = S::BM, BN = S::BN, KC = S::KC, LD = S::LD;
+  __shared__ __align__(16) char smem[lds_bytes<S, PA, PB>()];
+  __shared__ int64_t s_x[kRowTable], s_y[kRowTable];
+  uint16_t(*sa)[BM][LD] = reinterpret_cast<uint16_t(*)[BM][LD]>(smem);
+  uint16_t(*sb)[BN][LD] = reinterpret_cast<uint16_t(*)[BN][LD]>(smem + PA * BM * LD * 2);
+  const int64_t tile = xcd_item(blockIdx.x, gridDim.x);
+  if (tile >= a.tiles) return;
   int ji = 0;
-  while (ji + 1 < a.njobs && (int64_t)blockIdx.x >= a.job[ji + 1].first_tile) ++ji;
+  while (ji + 1 < a.njobs && tile >= a.job[ji + 1].first_tile) ++ji;
   const LinGwJob& J = a.job[ji];
-  const int64_t lt = blockIdx.x - J.first_tile;
+  const int64_t lt = tile - J.first_tile;
   const int tiles = J.tiles_i * J.tiles_o;
   const int64_t slot = lt / tiles;
   const int ti = (int)(lt - slot * tiles);
-  const int i0 = (ti / J.tiles_o) * kBM, o0 = (ti % J.tiles_o) * kBN;
+  const int i0 = (ti / J.tiles_o) * BM, o0 = (ti % J.tiles_o) * BN;
   Slot s;
   if (!find_slot(a.offsets, a.G, a.N, J.n, J.rshift, slot, s)) return;
-  const int64_t row_end = min(s.rows, s.row0 + (int64_t(1) << J.rshift));
+  const int rows = (int)min(s.rows - s.row0, int64_t(1) << J.rshift);
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  floatx16 acc[1][1];
+  floatx16 acc[S::MT][S::NT];
 #pragma unroll
-  for (int r = 0; r < 16; ++r) acc[0][0][r] = 0.f;
-  const TX* x = static_cast<const TX*>(a.x);
-  for (int64_t r0 = s.row0; r0 < row_end; r0 += kKC) {
-    if (tid < kKC) {
-      const int64_t r = r0 + tid;
-      int32_t node = -1, m = 0;
-      if (r < row_end) {
+  for (int i = 0; i < S::MT; ++i)
+#pragma unroll
+    for (int j = 0; j < S::NT; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+  const TX* x = static_cast<const TX*>(a.x) + J.xoff;
+  const float* gy = a.gy + J.yoff;
+  using PartA = PairPart<TX, BM, KC>;
+  using PartB = PairPart<float, BN, KC>;
+  PartA pa;
+  PartB pb;
+  auto load = [&](int r0) {
+    if (r0 % kRowTable == 0) {  // the next rows' addresses (no thread reads the old ones any more)
+      __syncthreads();
+      for (int i = tid; i < kRowTable; i += kThreads) {
+        const int64_t r = s.row0 + min(r0 + i, rows - 1);
         const int64_t p = div_rows(r, J.n);
-        m = (int32_t)(r - p * J.n);
-        node = a.order ? a.order[s.node0 + p] : (int32_t)p;
+        const int32_t m = (int32_t)(r - p * J.n);
+        const int64_t node = a.order ? a.order[s.node0 + p] : p;
+        s_x[i] = node * a.F_in + (int64_t)m * J.mi;
+        s_y[i] = node * a.F_out + (int64_t)m * J.mo;
       }
-      s_node[tid] = node;
-      s_m[tid] = m;
+      __syncthreads();
     }
-    __syncthreads();
-    for (int p = 0; p < kBM * (kKC / 8) / kThreads; ++p) {
-      const int c = tid % kBM, kk = (p * (kThreads / kBM) + tid / kBM) * 8;
-      Run8<TX> v;
-      Run8<float> w;
-      v.clear();
-      w.clear();
+    const int t0 = r0 % kRowTable;
+    if (PartA::mine())
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int32_t node = s_node[kk + j], m = s_m[kk + j];
-        if (node < 0) continue;
-        if (i0 + c < J.mi) v.set(j, x[(int64_t)node * a.F_in + J.xoff + (int64_t)m * J.mi + i0 + c]);
-        if (o0 + c < J.mo) w.set(j, a.gy[(int64_t)node * a.F_out + J.yoff + (int64_t)m * J.mo + o0 + c]);
-      }
-      put_run8<kLD, kBM>(sa, c, kk, v.v);
-      put_run8<kLD, kBN>(sb, c, kk, w.v);
-    }
+      for (int p = 0; p < PartA::kPasses; ++p)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          pa.load(p, j, x + s_x[t0 + PartA::k(p) + j], i0 + PartA::col(), J.mi, a.vec_x);
+    if (PartB::mine())
+#pragma unroll
+      for (int p = 0; p < PartB::kPasses; ++p)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          pb.load(p, j, gy + s_y[t0 + PartB::k(p) + j], o0 + PartB::col(), J.mo, a.vec_y);
+  };
+  load(0);
+  for (int r0 = 0; r0 < rows; r0 += KC) {
+    const int left = rows - r0;
+    pa.template put<LD>(sa, left);
+    pb.template put<LD>(sb, left);
     __syncthreads();
-    const int kw = wave * (kKC / 4);
-    if (r0 + kw < row_end) multiply<PA, PB, 1, 1, kBM, kBN, kLD>(sa, sb, 0, 0, kw, kKC / 64, acc);
+    if (left > KC) load(r0 + KC);
+    if constexpr (S::KS > 1) {
+      const int kw = wave * (KC / S::KS);
+      if (kw < left) multiply<PA, PB, S::MT, S::NT, BM, BN, LD>(sa, sb, 0, 0, kw, KC / (16 * S::KS), acc);
+    } else {
+      constexpr int kCols = BN / S::WN;
+      multiply<PA, PB, S::MT, S::NT, BM, BN, LD>(sa, sb, (wave / kCols) * S::WM, (wave % kCols) * S::WN, 0, KC / 16, acc);
+    }
     __syncthreads();
   }
-  if (wave > 0)
-#pragma unroll
-    for (int r = 0; r < 16; ++r) part[wave - 1][r * 64 + lane] = acc[0][0][r];
-  __syncthreads();
-  if (wave > 0) return;
+  join_waves<S>(acc, smem);
+  if (S::KS > 1 && wave > 0) return;
+  constexpr int kCols = S::KS > 1 ? 1 : BN / S::WN;
+  const int mw = (wave / kCols) * S::WM, nw = (wave % kCols) * S::WN;
   const bool whole = s.rows <= (int64_t(1) << J.rshift);
   float* dst = whole ? a.gW + s.g * a.w_per_group + J.woff : a.part + J.part_off + slot * ((int64_t)J.mi * J.mo);
-  const int co = o0 + (lane & 31);
 #pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    const float v = ((acc[0][0][r] + part[0][r * 64 + lane]) + part[1][r * 64 + lane]) + part[2][r * 64 + lane];
-    const int ci = i0 + acc_row(r);
-    if (ci < J.mi && co < J.mo) dst[(int64_t)ci * J.mo + co] = v;
-  }
+  for (int i = 0; i < S::MT; ++i)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int ci = i0 + mw + 32 * i + acc_row(r);
+#pragma unroll
+      for (int j = 0; j < S::NT; ++j) {
+        const int co = o0 + nw + 32 * j + (lane & 31);
+        if (ci < J.mi && co < J.mo) dst[(int64_t)ci * J.mo + co] = acc[i][j][r];
+      }
+    }
 }
 
 // gW of the groups with several slots (their partial sums in slot order) or none (zero).
@@ -381,8 +552,6 @@ __global__ __launch_bounds__(kThreads) void lin_gw_reduce_kernel(const LinGwArgs
   for (int64_t i = 0; i < slots; ++i) v += p[i * size];
   a.gW[g * a.w_per_group + J.woff + le] = v;
 }
-
-// Weights no block covers do not exist, so the jobs cover w_per_group.
 
 // ---- grouping: a stable counting sort of the nodes by group ----------------------
 
@@ -506,52 +675,114 @@ hipError_t launch_lin_groups(const int32_t* group, int64_t N, int G, int32_t* of
   return hipGetLastError();
 }
 
-hipError_t launch_lin_rows(LinRowsArgs& a, hipStream_t s) {
-  TimingScope ts(kcLinear, s);
-  a.tiles = 0;
-  for (int j = 0; j < a.njobs; ++j) {
-    LinJob& J = a.job[j];
-    J.tiles_n = (J.cols + kBN - 1) / kBN;
-    J.first_tile = a.tiles;
-    a.tiles += ((a.N * J.n) / kBM + a.G) * J.tiles_n;
-  }
-  if (a.tiles >= INT32_MAX) return hipErrorInvalidValue;
-  const dim3 g((unsigned)a.tiles), b(kThreads);
-#define TP_ROWS(TI, TW, TO) hipLaunchKernelGGL((lin_rows_kernel<TI, TW, TO>), g, b, 0, s, a)
-  const int key = (a.in_bf16 ? 4 : 0) + (a.w_bf16 ? 2 : 0) + (a.out_bf16 ? 1 : 0);
-  switch (key) {
-    case 0: TP_ROWS(float, float, float); break;
-    case 1: TP_ROWS(float, float, uint16_t); break;
-    case 2: TP_ROWS(float, uint16_t, float); break;
-    case 3: TP_ROWS(float, uint16_t, uint16_t); break;
-    case 4: TP_ROWS(uint16_t, float, float); break;
-    case 5: TP_ROWS(uint16_t, float, uint16_t); break;
-    case 6: TP_ROWS(uint16_t, uint16_t, float); break;
-    default: TP_ROWS(uint16_t, uint16_t, uint16_t); break;
-  }
-#undef TP_ROWS
+namespace {
+
+// The grid of `tiles` blocks in XCD order: a multiple of the eight XCDs.
+unsigned xcd_grid(int64_t tiles) { return (unsigned)((tiles + 7) / 8 * 8); }
+
+// Rows kernel shapes: 128 rows by 128, 64 or 32 columns, and 32 x 32 with the
+// reduction split over the waves for launches of few rows.  One-piece operands
+// take longer chunks (the same LDS holds more of the reduction).
+template <int BN, bool ONE>
+struct RowsShape {
+  using type = Shape<128, BN, BN == 32 ? 32 : 64, BN == 128 ? 64 : 32, 1, ONE ? 64 : 32>;
+};
+template <bool ONE>
+struct RowsShape<0, ONE> {
+  using type = Shape<32, 32, 32, 32, 4, 128>;
+};
+
+template <int BN, typename TI, typename TW, typename TO, bool WT>
+hipError_t launch_rows_typed(const LinRowsArgs& a, hipStream_t s) {
+  using S = typename RowsShape<BN, Planes<TI>::count == 1 && Planes<TW>::count == 1>::type;
+  hipLaunchKernelGGL((lin_rows_kernel<S, TI, TW, TO, WT>), dim3(xcd_grid(a.tiles)), dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 
+template <int BN>
+hipError_t launch_rows_shape(const LinRowsArgs& a, hipStream_t s) {
+  using H = uint16_t;
+  if (a.wt)
+    return a.w_bf16 ? launch_rows_typed<BN, float, H, float, true>(a, s) : launch_rows_typed<BN, float, float, float, true>(a, s);
+  switch ((a.in_bf16 ? 4 : 0) + (a.w_bf16 ? 2 : 0) + (a.out_bf16 ? 1 : 0)) {
+    case 0: return launch_rows_typed<BN, float, float, float, false>(a, s);
+    case 1: return launch_rows_typed<BN, float, float, H, false>(a, s);
+    case 2: return launch_rows_typed<BN, float, H, float, false>(a, s);
+    case 3: return launch_rows_typed<BN, float, H, H, false>(a, s);
+    case 4: return launch_rows_typed<BN, H, float, float, false>(a, s);
+    case 5: return launch_rows_typed<BN, H, float, H, false>(a, s);
+    case 6: return launch_rows_typed<BN, H, H, float, false>(a, s);
+    default: return launch_rows_typed<BN, H, H, H, false>(a, s);
+  }
+}
+
+// Column tile of an output block: the padded columns, wider tiles preferred
+// (they re-read the rows less often).
+int rows_width(int cols) {
+  const int p128 = (cols + 127) / 128 * 128, p64 = (cols + 63) / 64 * 64, p32 = (cols + 31) / 32 * 32;
+  if (p128 * 4 <= p64 * 5) return 128;
+  return p64 * 4 <= p32 * 5 ? 64 : 32;
+}
+
+// Weight-gradient tile of a block: the padded area, larger tiles preferred.
+int gw_width(int mi, int mo) {
+  auto area = [&](int64_t t) { return ((mi + t - 1) / t * t) * ((mo + t - 1) / t * t); };
+  if (area(128) * 2 <= area(64) * 3) return 128;
+  return area(64) <= area(32) * 2 ? 64 : 32;
+}
+
+}  // namespace
+
+hipError_t launch_lin_rows(LinRowsArgs& a, hipStream_t s) {
+  TimingScope ts(kcLinear, s);
+  for (int width : {128, 64, 32}) {
+    LinRowsArgs k = a;
+    k.njobs = 0;
+    int64_t big = 0;
+    for (int j = 0; j < a.njobs; ++j)
+      if (rows_width(a.job[j].cols) == width) {
+        LinJob& J = k.job[k.njobs++];
+        J = a.job[j];
+        J.tiles_n = (J.cols + width - 1) / width;
+        big += ((a.N * J.n + 127) / 128) * J.tiles_n;
+      }
+    if (k.njobs == 0) continue;
+    const bool few = big < 64;
+    const int bm = few ? 32 : 128, bn = few ? 32 : width;
+    k.tiles = 0;
+    for (int j = 0; j < k.njobs; ++j) {
+      LinJob& J = k.job[j];
+      J.tiles_n = (J.cols + bn - 1) / bn;
+      J.first_tile = k.tiles;
+      k.tiles += ((a.N * J.n) / bm + a.G) * J.tiles_n;
+    }
+    if (k.tiles >= INT32_MAX - 8) return hipErrorInvalidValue;
+    const hipError_t e = few            ? launch_rows_shape<0>(k, s)
+                         : width == 128 ? launch_rows_shape<128>(k, s)
+                         : width == 64  ? launch_rows_shape<64>(k, s)
+                                        : launch_rows_shape<32>(k, s);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 int64_t lin_gw_plan(LinGwArgs& a) {
-  // rows per slot: about 2048 blocks over all jobs, at least 256 rows each
+  // rows per slot: about 512 blocks over all jobs, at least 128 rows each
   int64_t work = 0;
   for (int j = 0; j < a.njobs; ++j) {
     LinGwJob& J = a.job[j];
-    J.tiles_i = (J.mi + kBM - 1) / kBM;
-    J.tiles_o = (J.mo + kBN - 1) / kBN;
+    J.width = gw_width(J.mi, J.mo);
+    J.tiles_i = (J.mi + J.width - 1) / J.width;
+    J.tiles_o = (J.mo + J.width - 1) / J.width;
     work += a.N * J.n * J.tiles_i * J.tiles_o;
   }
-  int shift = 8;
-  while (shift < 30 && (work >> shift) > 2048) ++shift;
+  int shift = 7;
+  while (shift < 30 && (work >> shift) > 512) ++shift;
   int64_t part = 0, elems = 0;
-  a.tiles = 0;
   for (int j = 0; j < a.njobs; ++j) {
     LinGwJob& J = a.job[j];
     J.rshift = shift;
     J.slots = ((a.N * J.n) >> shift) + a.G;
-    J.first_tile = a.tiles;
-    a.tiles += J.slots * J.tiles_i * J.tiles_o;
     J.part_off = part;
     part += J.slots * J.mi * J.mo;
     J.first_elem = elems;
@@ -564,13 +795,38 @@ int64_t lin_gw_plan(LinGwArgs& a) {
 hipError_t launch_lin_gw(LinGwArgs& a, hipStream_t s) {
   TimingScope ts(kcLinear, s);
   lin_gw_plan(a);
-  if (a.tiles >= INT32_MAX || a.elems >= (int64_t)INT32_MAX * kThreads) return hipErrorInvalidValue;
+  if (a.elems >= (int64_t)INT32_MAX * kThreads) return hipErrorInvalidValue;
   const dim3 b(kThreads);
-  if (a.N > 0) {
-    if (a.x_bf16)
-      hipLaunchKernelGGL((lin_gw_kernel<uint16_t>), dim3((unsigned)a.tiles), b, 0, s, a);
+  for (int width : {128, 64, 32}) {
+    LinGwArgs k = a;
+    k.njobs = 0;
+    k.tiles = 0;
+    for (int j = 0; j < a.njobs; ++j)
+      if (a.job[j].width == width) {
+        LinGwJob& J = k.job[k.njobs++];
+        J = a.job[j];
+        J.first_tile = k.tiles;
+        k.tiles += J.slots * J.tiles_i * J.tiles_o;
+      }
+    if (k.njobs == 0) continue;
+    if (k.tiles >= INT32_MAX - 8) return hipErrorInvalidValue;
+    const dim3 g(xcd_grid(k.tiles));
+#define TP_GW(...)                                                                        \
+  do {                                                                                    \
+    if (a.x_bf16)                                                                         \
+      hipLaunchKernelGGL((lin_gw_kernel<Shape<__VA_ARGS__>, uint16_t>), g, b, 0, s, k);   \
+    else                                                                                  \
+      hipLaunchKernelGGL((lin_gw_kernel<Shape<__VA_ARGS__>, float>), g, b, 0, s, k);      \
+  } while (0)
+    if (width == 128)
+      TP_GW(128, 128, 64, 64, 1, 32);
+    else if (width == 64)
+      TP_GW(64, 64, 32, 32, 1, 64);
     else
-      hipLaunchKernelGGL((lin_gw_kernel<float>), dim3((unsigned)a.tiles), b, 0, s, a);
+      TP_GW(32, 32, 32, 32, 4, 128);
+#undef TP_GW
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
   }
   hipLaunchKernelGGL(lin_gw_reduce_kernel, dim3(blocks(a.elems, kThreads), (unsigned)a.G), b, 0, s, a);
   return hipGetLastError();
