@@ -17,6 +17,7 @@
 #include "layers.h"
 #include "timing.h"
 
+#include <algorithm>
 #include <utility>
 
 namespace tpconv {
@@ -223,6 +224,314 @@ __global__ __launch_bounds__(kThreads) void muon_gemm_kernel(const Bank /*args*/
   }
 }
 
+// ---- small matrices: all steps of one matrix in one block of threads ---------------
+// Padded shapes RP x CP that fit the registers and the 160 KB of LDS of one CU.
+// X stays in fp32 accumulator registers over all steps; LDS holds its planes
+// (row-major for X X^T, then transposed for B X) and those of A, later B.  The
+// only global traffic is the update's own.
+
+struct SmallBlock {
+  int32_t rows, cols;
+  int64_t offset, stride;
+  int64_t first;  // first matrix of the block in the launch
+};
+
+struct SmallArgs {
+  MuonUpdate u;
+  int32_t update, nsteps, nblocks;
+  float eps;
+  MuonStep step[kMaxMuonSteps + 1];
+  SmallBlock block[kMaxMuonBlocks];
+};
+
+template <int RP_, int CP_, int NW_, int TPW_>
+struct Small {
+  static constexpr int RP = RP_, CP = CP_, NW = NW_, TPW = TPW_;
+  static constexpr int RT = RP / 32, CT = CP / 32;
+  static constexpr int APW = RT == 4 ? 2 : 1;               // tiles of A per wave
+  static constexpr int AW = RT * RT / APW;                  // waves that hold tiles of A
+  static constexpr int KS = NW / AW;                        // waves that share the reduction of X X^T
+  static constexpr int LX = CP + 8, LT = RP + 8;            // LDS rows, padded by 16 bytes
+  static constexpr int kX = RP * LX > CP * LT ? RP * LX : CP * LT;
+  static constexpr int kBytes = 2 * (2 * kX + 2 * RP * LT) + (KS - 1) * AW * APW * 1024 * 4;
+  static_assert(RT * CT == NW * TPW && AW * KS == NW, "tiles per wave");
+  static_assert(kBytes <= 160 * 1024, "LDS");
+};
+
+template <int TILES>
+__device__ __forceinline__ void mul_tiles(const _Float16* p, int lp, int plane_p, const _Float16* q, int lq, int plane_q,
+                                          int k0, int steps, floatx16 (&acc)[TILES]) {
+  // p: rows of TILES stacked 32-row tiles, q: rows of one 32-column tile
+  const int lane = threadIdx.x & 63, i = lane & 31, h = lane >> 5;
+#pragma unroll 2
+  for (int s = 0; s < steps; ++s) {
+    const int k = k0 + 16 * s + 8 * h;
+    const half8 qh = *reinterpret_cast<const half8*>(q + i * lq + k);
+    const half8 ql = *reinterpret_cast<const half8*>(q + plane_q + i * lq + k);
+    half8 ph[TILES], pl[TILES];
+#pragma unroll
+    for (int t = 0; t < TILES; ++t) {
+      ph[t] = *reinterpret_cast<const half8*>(p + (32 * t + i) * lp + k);
+      pl[t] = *reinterpret_cast<const half8*>(p + plane_p + (32 * t + i) * lp + k);
+    }
+#pragma unroll
+    for (int t = 0; t < TILES; ++t) acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph[t], ql, acc[t], 0, 0, 0);
+#pragma unroll
+    for (int t = 0; t < TILES; ++t) acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(pl[t], qh, acc[t], 0, 0, 0);
+#pragma unroll
+    for (int t = 0; t < TILES; ++t) acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph[t], qh, acc[t], 0, 0, 0);
+  }
+}
+
+// The tile (rows i0.., columns j0..) of v * 2^e into planes whose rows are the
+// tile's columns: four consecutive rows of a column are one 8-byte write.
+__device__ __forceinline__ void put_columns(_Float16* s, int ld, int plane, int i0, int j0, const floatx16& v, float f) {
+  const int lane = threadIdx.x & 63, j = j0 + (lane & 31), h = lane >> 5;
+#pragma unroll
+  for (int rq = 0; rq < 4; ++rq) {
+    half4 hi, lo;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      _Float16 a, b;
+      split2(v[4 * rq + e] * f, a, b);
+      hi[e] = a;
+      lo[e] = b;
+    }
+    _Float16* at = s + j * ld + i0 + 8 * rq + 4 * h;
+    *reinterpret_cast<half4*>(at) = hi;
+    *reinterpret_cast<half4*>(at + plane) = lo;
+  }
+}
+
+// The same into planes whose rows are the tile's rows.
+__device__ __forceinline__ void put_rows(_Float16* s, int ld, int plane, int i0, int j0, const floatx16& v, float f) {
+  const int lane = threadIdx.x & 63, j = j0 + (lane & 31), h = lane >> 5;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    _Float16 a, b;
+    split2(v[r] * f, a, b);
+    _Float16* at = s + (i0 + 8 * (r >> 2) + 4 * h + (r & 3)) * ld + j;
+    at[0] = a;
+    at[plane] = b;
+  }
+}
+
+template <typename S>
+__global__ __launch_bounds__(64 * S::NW) void muon_small_kernel(const SmallArgs /*args*/) {
+  const SmallArgs& a = *(const SmallArgs*)__builtin_amdgcn_kernarg_segment_ptr();
+  __shared__ __align__(16) char smem[S::kBytes];
+  __shared__ float s_norm[S::NW];
+  constexpr int RP = S::RP, RT = S::RT, TPW = S::TPW, APW = S::APW, AW = S::AW, KS = S::KS, LX = S::LX, LT = S::LT;
+  constexpr int kXPlane = S::kX, kAPlane = RP * LT;
+  _Float16* sx = reinterpret_cast<_Float16*>(smem);
+  _Float16* sq = sx + 2 * kXPlane;
+  float* sr = reinterpret_cast<float*>(sq + 2 * kAPlane);
+  int bi = 0;
+  while (bi + 1 < a.nblocks && (int64_t)blockIdx.x >= a.block[bi + 1].first) ++bi;
+  const SmallBlock& m = a.block[bi];
+  const int64_t base = m.offset + (blockIdx.x - m.first) * m.stride;
+  const bool transposed = m.rows > m.cols;
+  const int nr = transposed ? m.cols : m.rows, nc = transposed ? m.rows : m.cols;
+  const int si = transposed ? 1 : m.cols, sj = transposed ? m.cols : 1;  // X[i][j] is U at i * si + j * sj
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, lj = lane & 31, lh = lane >> 5;
+
+  // X in registers: tile t of the wave covers rows 32 (tile % RT), columns 32 (tile / RT)
+  floatx16 x[TPW];
+  float q = 0.f;
+#pragma unroll
+  for (int t = 0; t < TPW; ++t) {
+    const int tile = wave * TPW + t, i0 = 32 * (tile % RT) + 4 * lh, j = 32 * (tile / RT) + lj;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int i = i0 + 8 * (r >> 2) + (r & 3);
+      float v = 0.f;
+      if (i < nr && j < nc) {
+        const int64_t e = base + (int64_t)i * si + (int64_t)j * sj;
+        if (a.update) {
+          const float g = (1.f - a.u.beta) * a.u.grad[e], mo = a.u.beta * a.u.mom[e] + g;
+          a.u.mom_out[e] = mo;
+          v = a.u.nesterov ? g + a.u.beta * mo : mo;
+        } else {
+          v = a.u.u[e];
+        }
+      }
+      x[t][r] = v;
+      q = __builtin_fmaf(v, v, q);
+    }
+  }
+  for (int d = 32; d > 0; d >>= 1) q += __shfl_xor(q, d);
+  if (lane == 0) s_norm[wave] = q;
+  __syncthreads();
+  q = 0.f;
+  for (int w = 0; w < S::NW; ++w) q += s_norm[w];
+  const float inv = 1.f / fmaxf(sqrtf(q), a.eps);
+#pragma unroll
+  for (int t = 0; t < TPW; ++t)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) x[t][r] *= inv;
+
+  for (int k = 0; k < a.nsteps; ++k) {
+    const MuonStep st = a.step[k];
+#pragma unroll
+    for (int t = 0; t < TPW; ++t) {
+      const int tile = wave * TPW + t;
+      put_rows(sx, LX, kXPlane, 32 * (tile % RT), 32 * (tile / RT), x[t], pow2(st.ex));
+    }
+    __syncthreads();
+    // A = X X^T: KS waves per tile group take a part of the columns each
+    const int aw = wave % AW, ks = wave / AW;
+    const int ai = 32 * ((aw * APW) % RT), aj = 32 * ((aw * APW) / RT);
+    floatx16 acc[APW];
+#pragma unroll
+    for (int t = 0; t < APW; ++t)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[t][r] = 0.f;
+    mul_tiles<APW>(sx + ai * LX, LX, kXPlane, sx + aj * LX, LX, kXPlane, ks * (S::CP / KS), S::CP / (16 * KS), acc);
+    if constexpr (KS > 1) {
+      if (ks > 0)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) sr[((ks - 1) * AW + aw) * 1024 + r * 64 + lane] = acc[0][r];
+    }
+    __syncthreads();
+    const float fa = pow2(-2 * st.ex);
+    if (ks == 0) {
+#pragma unroll
+      for (int t = 0; t < APW; ++t) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          if constexpr (KS > 1)
+            for (int w = 0; w < KS - 1; ++w) acc[t][r] += sr[(w * AW + aw) * 1024 + r * 64 + lane];
+          acc[t][r] *= fa;
+        }
+        put_columns(sq, LT, kAPlane, ai + 32 * t, aj, acc[t], pow2(st.ea));  // A is symmetric
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < TPW; ++t) {
+      const int tile = wave * TPW + t;
+      put_columns(sx, LT, kXPlane, 32 * (tile % RT), 32 * (tile / RT), x[t], pow2(st.ex));  // X^T
+    }
+    __syncthreads();
+    // B = b A + c A A, over A
+    floatx16 sqr[APW];
+    if (ks == 0) {
+#pragma unroll
+      for (int t = 0; t < APW; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) sqr[t][r] = 0.f;
+      mul_tiles<APW>(sq + ai * LT, LT, kAPlane, sq + aj * LT, LT, kAPlane, 0, RP / 16, sqr);
+    }
+    __syncthreads();
+    if (ks == 0) {
+      const float fc = st.c * pow2(-2 * st.ea);
+#pragma unroll
+      for (int t = 0; t < APW; ++t) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) sqr[t][r] = st.b * acc[t][r] + fc * sqr[t][r];
+        put_columns(sq, LT, kAPlane, ai + 32 * t, aj, sqr[t], pow2(st.eb));
+      }
+    }
+    __syncthreads();
+    // X <- a X + B X, the wave's own tiles (all in one column of tiles, or single)
+    const float fx = pow2(-st.ex - st.eb);
+    if constexpr (RT > 1 || TPW == 1) {
+      floatx16 bx[TPW];
+#pragma unroll
+      for (int t = 0; t < TPW; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) bx[t][r] = 0.f;
+      const int tile = wave * TPW;
+      mul_tiles<TPW>(sq + 32 * (tile % RT) * LT, LT, kAPlane, sx + 32 * (tile / RT) * LT, LT, kXPlane, 0, RP / 16, bx);
+#pragma unroll
+      for (int t = 0; t < TPW; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) x[t][r] = st.a * x[t][r] + fx * bx[t][r];
+    } else {
+#pragma unroll
+      for (int t = 0; t < TPW; ++t) {
+        floatx16 bx[1];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) bx[0][r] = 0.f;
+        mul_tiles<1>(sq, LT, kAPlane, sx + 32 * (wave * TPW + t) * LT, LT, kXPlane, 0, RP / 16, bx);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) x[t][r] = st.a * x[t][r] + fx * bx[0][r];
+      }
+    }
+    __syncthreads();
+  }
+
+  const float keep = 1.f - a.u.lr * a.u.decay;
+  const float rate = a.u.lr * (m.cols > m.rows ? sqrtf((float)m.cols / (float)m.rows) : 1.f);
+#pragma unroll
+  for (int t = 0; t < TPW; ++t) {
+    const int tile = wave * TPW + t, i0 = 32 * (tile % RT) + 4 * lh, j = 32 * (tile / RT) + lj;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int i = i0 + 8 * (r >> 2) + (r & 3);
+      if (i >= nr || j >= nc) continue;
+      const int64_t e = base + (int64_t)i * si + (int64_t)j * sj;
+      float v = x[t][r];
+      if (a.update) {
+        v = keep * a.u.W[e] - rate * v;
+        if (a.u.w_bf16) a.u.w_bf16[e] = __builtin_bit_cast(uint16_t, (__bf16)v);
+      }
+      a.u.out[e] = v;
+    }
+  }
+}
+
+// The padded shapes, by rows then columns.
+enum SmallKind { kS32x32, kS32x64, kS32x128, kS32x256, kS32x512, kS64x64, kS64x128, kS64x256, kS128x128, kSmallKinds };
+
+// The smallest padded shape of an r x c matrix (r <= c); -1: none, the matrix takes the tiled path.
+int small_kind(int r, int c) {
+  if (r <= 32) return c <= 32 ? kS32x32 : c <= 64 ? kS32x64 : c <= 128 ? kS32x128 : c <= 256 ? kS32x256 : c <= 512 ? kS32x512 : -1;
+  if (r <= 64) return c <= 64 ? kS64x64 : c <= 128 ? kS64x128 : c <= 256 ? kS64x256 : -1;
+  return r <= 128 && c <= 128 ? kS128x128 : -1;
+}
+int small_kind(const MuonBlock& b) {
+  return b.rows < b.cols ? small_kind(b.rows, b.cols) : small_kind(b.cols, b.rows);
+}
+
+template <typename S>
+hipError_t launch_small(const SmallArgs& k, int64_t matrices, hipStream_t s) {
+  hipLaunchKernelGGL((muon_small_kernel<S>), dim3((unsigned)matrices), dim3(64 * S::NW), 0, s, k);
+  return hipGetLastError();
+}
+
+hipError_t launch_small_kinds(const MuonPlan& p, const MuonUpdate& u, hipStream_t s) {
+  for (int kind = 0; kind < kSmallKinds; ++kind) {
+    SmallArgs k{};
+    int64_t n = 0;
+    for (int i = 0; i < p.nblocks; ++i) {
+      const MuonBlock& b = p.block[i];
+      if (b.count == 0 || small_kind(b) != kind) continue;
+      k.block[k.nblocks++] = {b.rows, b.cols, b.offset, b.stride, n};
+      n += b.count;
+    }
+    if (n == 0) continue;
+    k.u = u;
+    k.update = u.W != nullptr;
+    k.nsteps = p.nsteps;
+    k.eps = p.eps;
+    std::copy(p.step, p.step + kMaxMuonSteps + 1, k.step);
+    hipError_t e = hipSuccess;
+    switch (kind) {
+      case kS32x32: e = launch_small<Small<32, 32, 1, 1>>(k, n, s); break;
+      case kS32x64: e = launch_small<Small<32, 64, 2, 1>>(k, n, s); break;
+      case kS32x128: e = launch_small<Small<32, 128, 4, 1>>(k, n, s); break;
+      case kS32x256: e = launch_small<Small<32, 256, 8, 1>>(k, n, s); break;
+      case kS32x512: e = launch_small<Small<32, 512, 8, 2>>(k, n, s); break;
+      case kS64x64: e = launch_small<Small<64, 64, 4, 1>>(k, n, s); break;
+      case kS64x128: e = launch_small<Small<64, 128, 8, 1>>(k, n, s); break;
+      case kS64x256: e = launch_small<Small<64, 256, 8, 2>>(k, n, s); break;
+      default: e = launch_small<Small<128, 128, 8, 2>>(k, n, s); break;
+    }
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 size_t align_up(size_t b) { return (b + 255) / 256 * 256; }
 
 void set_bank(const MuonPlan& p, int i, Bank& b) {
@@ -250,7 +559,7 @@ size_t muon_workspace(const MuonPlan& p) {
   for (int i = 0; i < p.nblocks; ++i) {
     Bank b{};
     set_bank(p, i, b);
-    const size_t n = b.m.count > 0 ? bank_bytes(b) : 0;
+    const size_t n = b.m.count > 0 && small_kind(b.m) < 0 ? bank_bytes(b) : 0;
     most = n > most ? n : most;
   }
   return most;  // the blocks run one after the other in the same workspace
@@ -258,10 +567,12 @@ size_t muon_workspace(const MuonPlan& p) {
 
 hipError_t launch_muon(const MuonPlan& p, const MuonUpdate& u, void* ws, hipStream_t s) {
   TimingScope ts(kcMuon, s);
+  const hipError_t e = launch_small_kinds(p, u, s);
+  if (e != hipSuccess) return e;
   for (int i = 0; i < p.nblocks; ++i) {
     Bank b{};
     set_bank(p, i, b);
-    if (b.m.count == 0) continue;
+    if (b.m.count == 0 || small_kind(b.m) >= 0) continue;
     b.u = u;
     b.update = u.W != nullptr;
     const size_t x = (size_t)b.m.count * b.rp * b.cp, a = (size_t)b.m.count * b.rp * b.rp;
