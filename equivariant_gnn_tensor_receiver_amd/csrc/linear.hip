@@ -405,6 +405,7 @@ __global__ __launch_bounds__(kThreads, 2) void lin_rows_kernel(const LinRowsArgs
       ++si;
     }
     if (si < J.nseg) load(a.seg[J.seg0 + si], k0);
+    __builtin_amdgcn_sched_barrier(0);  // the loads stay ahead of the products
     if constexpr (S::KS > 1) {
       const int kw = wave * (KC / S::KS);  // a wave without reductions left skips its products
       if (kw < left) multiply<PA, PB, S::MT, S::NT, BM, BN, LD>(sa, sb, 0, 0, kw, KC / (16 * S::KS), acc);
@@ -506,6 +507,7 @@ __global__ __launch_bounds__(kThreads, 2) void lin_gw_kernel(const LinGwArgs /*a
     pb.template put<LD>(sb, left);
     __syncthreads();
     if (left > KC) load(r0 + KC);
+    __builtin_amdgcn_sched_barrier(0);  // the loads stay ahead of the products
     if constexpr (S::KS > 1) {
       const int kw = wave * (KC / S::KS);
       if (kw < left) multiply<PA, PB, S::MT, S::NT, BM, BN, LD>(sa, sb, 0, 0, kw, KC / (16 * S::KS), acc);

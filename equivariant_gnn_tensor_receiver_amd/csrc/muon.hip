@@ -29,25 +29,31 @@ typedef _Float16 half4 __attribute__((ext_vector_type(4)));
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 
 constexpr int kThreads = 256;
-constexpr int kTile = 64;            // rows and columns of a block's tile
-constexpr int kKC = 64;              // reductions per chunk
-constexpr int kLD = kKC + 8;
-constexpr int kNormChunk = 8192;     // elements per block of the norm
+constexpr int kKC = 64;              // reductions per chunk of the tiled products
+constexpr int kLD = kKC + 8;         // LDS rows padded by 16 bytes
+// Rows of the planes in memory are 128 bytes longer than the padded matrix: at
+// a power-of-two row length one chunk of all rows of a tile lies in the same
+// L2 channels.
+constexpr int kSkew = 64;
+constexpr int kNormChunk = 4096;     // elements per block of the norm
 
 // What one launch works on: a bank of `count` matrices.
 struct Bank {
   MuonUpdate u;
   MuonBlock m;
-  int32_t r, c, rp, cp;    // X is r x c (r <= c); padded to multiples of kTile
+  int32_t r, c, rp, cp;    // X is r x c (r <= c); padded to multiples of the larger tile
+  int32_t rl, cl;          // row lengths of the planes (rp and cp, and kSkew)
+  int32_t square_tile, apply_tile;  // tile widths of the r x r products and of B X
   int32_t transposed;      // rows > cols: X = U^T
   int32_t chunks;          // blocks per matrix of the norm
   float eps, scale;        // scale: sqrt(max(1, cols / rows))
   int32_t update;          // 0: orthogonalize, 1: optimiser step
   float* norm;             // [count][chunks] sums of squares
-  _Float16 *xh, *xl;       // [count][rp][cp]
-  _Float16 *th, *tl;       // [count][cp][rp]: X^T
+  int64_t xsize, tsize, asize;  // halfs per matrix of the planes of X, X^T, and A or B
+  _Float16 *xh, *xl;       // [count][rp][cl]
+  _Float16 *th, *tl;       // [count][cp][rl]: X^T
   _Float16 *nh, *nl;       // X^T of the next step (a launch reads one and writes the other)
-  _Float16 *ah, *al, *bh, *bl;  // [count][rp][rp]
+  _Float16 *ah, *al, *bh, *bl;  // [count][rp][rl]
 };
 
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
@@ -71,11 +77,26 @@ __global__ __launch_bounds__(kThreads) void muon_norm_kernel(const Bank /*args*/
   const int64_t base = b.m.offset + (int64_t)blockIdx.y * b.m.stride;
   const int64_t lo = (int64_t)blockIdx.x * kNormChunk, hi = min(n, lo + kNormChunk);
   float q = 0.f;
-  for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) {
-    const int64_t e = base + i;
-    if (b.update) b.u.mom_out[e] = b.u.beta * b.u.mom[e] + (1.f - b.u.beta) * b.u.grad[e];
-    const float v = u_at(b, e);
-    q = __builtin_fmaf(v, v, q);
+  for (int64_t i0 = lo + threadIdx.x; i0 < hi; i0 += 4 * kThreads) {
+    float g[4], m[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {  // every load of the round is in flight at once; past the end the last element again
+      const int64_t e = base + min(i0 + k * kThreads, hi - 1);
+      g[k] = b.update ? b.u.grad[e] : b.u.u[e];
+      m[k] = b.update ? b.u.mom[e] : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t i = i0 + k * kThreads;
+      if (i >= hi) break;
+      float v = g[k];
+      if (b.update) {
+        const float mo = b.u.beta * m[k] + (1.f - b.u.beta) * g[k];
+        b.u.mom_out[base + i] = mo;
+        v = b.u.nesterov ? (1.f - b.u.beta) * g[k] + b.u.beta * mo : mo;
+      }
+      q = __builtin_fmaf(v, v, q);
+    }
   }
   tmp[threadIdx.x] = q;
   __syncthreads();
@@ -86,26 +107,40 @@ __global__ __launch_bounds__(kThreads) void muon_norm_kernel(const Bank /*args*/
   if (threadIdx.x == 0) b.norm[(int64_t)blockIdx.y * b.chunks + blockIdx.x] = tmp[0];
 }
 
-// X = U / max(|U|, eps) into the planes of X and X^T (zero in the padding).
+// X = U / max(|U|, eps) into the planes of X and X^T (zero in the padding), by
+// 64 x 64 tiles turned through LDS so that reads and writes run along rows.
 __global__ __launch_bounds__(kThreads) void muon_init_kernel(const Bank /*args*/, int ex) {
   const Bank& b = *(const Bank*)__builtin_amdgcn_kernarg_segment_ptr();
+  __shared__ float tile[64][65];
+  __shared__ float tmp[kThreads];
+  const int64_t bz = blockIdx.z;
   float q = 0.f;
-  for (int i = 0; i < b.chunks; ++i) q += b.norm[(int64_t)blockIdx.y * b.chunks + i];
-  const float inv = 1.f / fmaxf(sqrtf(q), b.eps);
-  const int64_t pad = (int64_t)b.rp * b.cp;
-  const int64_t base = b.m.offset + (int64_t)blockIdx.y * b.m.stride;
-  for (int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x; e < pad; e += (int64_t)gridDim.x * kThreads) {
-    const int i = (int)(e / b.cp), j = (int)(e - (int64_t)i * b.cp);
+  for (int i = threadIdx.x; i < b.chunks; i += kThreads) q += b.norm[bz * b.chunks + i];
+  tmp[threadIdx.x] = q;
+  __syncthreads();
+  for (int s = kThreads / 2; s > 0; s >>= 1) {
+    if ((int)threadIdx.x < s) tmp[threadIdx.x] += tmp[threadIdx.x + s];
+    __syncthreads();
+  }
+  const float f = pow2(ex) / fmaxf(sqrtf(tmp[0]), b.eps);
+  const int i0 = blockIdx.y * 64, j0 = blockIdx.x * 64, lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int64_t base = b.m.offset + bz * b.m.stride;
+  // rows of U: rows of X, or its columns when X = U^T
+  const int u0 = b.transposed ? j0 : i0, v0 = b.transposed ? i0 : j0;
+  for (int k = w; k < 64; k += 4) {
     float v = 0.f;
-    if (i < b.r && j < b.c) {
-      const int64_t at = b.transposed ? (int64_t)j * b.m.cols + i : (int64_t)i * b.m.cols + j;
-      v = u_at(b, base + at) * inv * pow2(ex);
-    }
+    if (u0 + k < b.m.rows && v0 + lane < b.m.cols) v = u_at(b, base + (int64_t)(u0 + k) * b.m.cols + v0 + lane) * f;
+    tile[k][lane] = v;
+  }
+  __syncthreads();
+  for (int k = w; k < 64; k += 4) {
     _Float16 h, l;
-    split2(v, h, l);
-    const int64_t x = blockIdx.y * pad + e, t = blockIdx.y * pad + (int64_t)j * b.rp + i;
+    split2(b.transposed ? tile[lane][k] : tile[k][lane], h, l);
+    const int64_t x = bz * b.xsize + (int64_t)(i0 + k) * b.cl + j0 + lane;
     b.xh[x] = h;
     b.xl[x] = l;
+    split2(b.transposed ? tile[k][lane] : tile[lane][k], h, l);
+    const int64_t t = bz * b.tsize + (int64_t)(j0 + k) * b.rl + i0 + lane;
     b.th[t] = h;
     b.tl[t] = l;
   }
@@ -113,114 +148,231 @@ __global__ __launch_bounds__(kThreads) void muon_init_kernel(const Bank /*args*/
 
 enum Phase { kGram, kPoly, kApply, kLast };
 
-// C[i][j] = sum_k P[i][k] Q[j][k] over one 64 x 64 tile, then the phase's epilogue:
+constexpr int kGemmThreads = 512;
+
+// C[i][j] = sum_k P[i][k] Q[j][k] over one T x T tile, then the phase's epilogue:
 //   kGram:  P = Q = X:           A = C
 //   kPoly:  P = Q = A (A = A^T): B = b A + c C
 //   kApply: P = B, Q = X^T:      X = a X + C, in both layouts
 //   kLast:  the same, written out as X or as the updated weights
-template <int PHASE>
-__global__ __launch_bounds__(kThreads) void muon_gemm_kernel(const Bank /*args*/, MuonStep st, int ex_next) {
+// A and B are symmetric: only tiles on and below the diagonal are computed, and
+// the others written as their mirror images.  Eight waves: T = 128 gives each
+// 64 x 32 (six LDS reads for six products); T = 64 one of four 32 x 32 tiles
+// and half of every chunk of the reduction (few blocks, so more waves per block).
+// Chunks go through two LDS buffers, with the loads of the next two in flight.
+// The results pass through LDS as well, so that every plane is read and written
+// in 16-byte pieces of its rows.
+template <int PHASE, int T>
+__global__ __launch_bounds__(kGemmThreads) void muon_gemm_kernel(const Bank /*args*/, MuonStep st, int ex_next, int tiles) {
   const Bank& b = *(const Bank*)__builtin_amdgcn_kernarg_segment_ptr();
-  __shared__ __align__(16) _Float16 sp[2][kTile][kLD];
-  __shared__ __align__(16) _Float16 sq[2][kTile][kLD];
-  const int64_t xsize = (int64_t)b.rp * b.cp, asize = (int64_t)b.rp * b.rp, bz = blockIdx.z;
-  const int K = PHASE == kGram ? b.cp : b.rp;
-  const _Float16* p[2];
-  const _Float16* q[2];
-  if constexpr (PHASE == kGram) {
-    p[0] = q[0] = b.xh + bz * xsize;
-    p[1] = q[1] = b.xl + bz * xsize;
-  } else if constexpr (PHASE == kPoly) {
-    p[0] = q[0] = b.ah + bz * asize;
-    p[1] = q[1] = b.al + bz * asize;
+  constexpr int MT = T == 128 ? 2 : 1, KS = T == 128 ? 1 : 2;
+  constexpr int kPlane = T * kLD, kOp = 2 * kPlane, kBuf = 2 * kOp;  // halfs
+  constexpr int kUnits = T * (kKC / 8) / kGemmThreads;               // 16-byte units per thread, plane and operand
+  __shared__ __align__(16) _Float16 smem[2 * kBuf];
+  const int K = PHASE == kGram ? b.cp : b.rp, ldk = PHASE == kGram ? b.cl : b.rl;
+  // consecutive tiles run on one XCD and share the operands' rows in its L2
+  const int64_t item = xcd_item(blockIdx.x, gridDim.x);
+  if (item >= tiles * b.m.count) return;
+  const int64_t bz = item / tiles;
+  const int tile = (int)(item - bz * tiles);
+  int i0, j0;
+  if constexpr (PHASE == kGram || PHASE == kPoly) {
+    int t = tile, ti = (int)((sqrtf(8.f * (float)t + 1.f) - 1.f) * 0.5f);
+    while ((ti + 1) * (ti + 2) / 2 <= t) ++ti;
+    while (ti * (ti + 1) / 2 > t) --ti;
+    i0 = ti * T;
+    j0 = (t - ti * (ti + 1) / 2) * T;
   } else {
-    p[0] = b.bh + bz * asize;
-    p[1] = b.bl + bz * asize;
-    q[0] = b.th + bz * xsize;
-    q[1] = b.tl + bz * xsize;
+    const int rt = b.rp / T;
+    j0 = tile / rt * T;
+    i0 = tile % rt * T;
   }
-  const int i0 = blockIdx.y * kTile, j0 = blockIdx.x * kTile;
+  const _Float16* src[4];  // P hi, P lo, Q hi, Q lo
+  if constexpr (PHASE == kGram) {
+    src[0] = src[2] = b.xh + bz * b.xsize;
+    src[1] = src[3] = b.xl + bz * b.xsize;
+  } else if constexpr (PHASE == kPoly) {
+    src[0] = src[2] = b.ah + bz * b.asize;
+    src[1] = src[3] = b.al + bz * b.asize;
+  } else {
+    src[0] = b.bh + bz * b.asize;
+    src[1] = b.bl + bz * b.asize;
+    src[2] = b.th + bz * b.tsize;
+    src[3] = b.tl + bz * b.tsize;
+  }
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, li = lane & 31, lh = lane >> 5;
-  const int mw = (wave >> 1) * 32, nw = (wave & 1) * 32;
-  floatx16 acc;
+  const int srow = tid >> 3, sk = (tid & 7) * 8;  // this thread's 16 bytes of a row
 #pragma unroll
-  for (int r = 0; r < 16; ++r) acc[r] = 0.f;
-  for (int k0 = 0; k0 < K; k0 += kKC) {
+  for (int z = 0; z < 4; ++z) src[z] += (int64_t)((z < 2 ? i0 : j0) + srow) * ldk + sk;
+  constexpr int kAhead = 2;
+  half8 raw[kAhead][4][kUnits];
+  auto load = [&](int d, int k0) {
 #pragma unroll
-    for (int pass = 0; pass < 2; ++pass) {
-      const int row = pass * 32 + (tid >> 3), kk = (tid & 7) * 8;
+    for (int z = 0; z < 4; ++z)
 #pragma unroll
-      for (int z = 0; z < 2; ++z) {
-        *reinterpret_cast<half8*>(&sp[z][row][kk]) =
-            *reinterpret_cast<const half8*>(p[z] + (int64_t)(i0 + row) * K + k0 + kk);
-        *reinterpret_cast<half8*>(&sq[z][row][kk]) =
-            *reinterpret_cast<const half8*>(q[z] + (int64_t)(j0 + row) * K + k0 + kk);
+      for (int u = 0; u < kUnits; ++u)
+        raw[d][z][u] = *reinterpret_cast<const half8*>(src[z] + (int64_t)u * (kGemmThreads / 8) * ldk + k0);
+  };
+  auto put = [&](int d, int buf) {
+#pragma unroll
+    for (int z = 0; z < 4; ++z)
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u)
+        *reinterpret_cast<half8*>(smem + buf * kBuf + z * kPlane + (srow + u * (kGemmThreads / 8)) * kLD + sk) =
+            raw[d][z][u];
+  };
+  const int mw = T == 128 ? (wave >> 2) * 64 : ((wave >> 1) & 1) * 32;
+  const int nw = T == 128 ? (wave & 3) * 32 : (wave & 1) * 32;
+  const int kw = KS == 2 ? (wave >> 2) * (kKC / 2) : 0;
+  floatx16 acc[MT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[t][r] = 0.f;
+  const int chunks = K / kKC;
+  load(0, 0);
+  put(0, 0);
+#pragma unroll
+  for (int d = 1; d <= kAhead; ++d) load(d % kAhead, min(d, chunks - 1) * kKC);
+  __syncthreads();
+  for (int c0 = 0; c0 < chunks; c0 += 2) {
+#pragma unroll
+    for (int d = 0; d < 2; ++d) {
+      const int c = c0 + d;
+      if (c >= chunks) break;
+      const int buf = d, slot = (d + 1) % kAhead;
+      const _Float16* p = smem + buf * kBuf + (mw + li) * kLD + kw + 8 * lh;
+      const _Float16* q = smem + buf * kBuf + kOp + (nw + li) * kLD + kw + 8 * lh;
+#pragma unroll
+      for (int s = 0; s < kKC / (16 * KS); ++s) {
+        half8 ph[MT], pl[MT];
+        const half8 qh = *reinterpret_cast<const half8*>(q + 16 * s);
+        const half8 ql = *reinterpret_cast<const half8*>(q + kPlane + 16 * s);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          ph[t] = *reinterpret_cast<const half8*>(p + 32 * t * kLD + 16 * s);
+          pl[t] = *reinterpret_cast<const half8*>(p + kPlane + 32 * t * kLD + 16 * s);
+        }
+#pragma unroll
+        for (int t = 0; t < MT; ++t) acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph[t], ql, acc[t], 0, 0, 0);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(pl[t], qh, acc[t], 0, 0, 0);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph[t], qh, acc[t], 0, 0, 0);
       }
+      put(slot, buf ^ 1);
+      __builtin_amdgcn_sched_barrier(0);
+      load(slot, min(c + 1 + kAhead, chunks - 1) * kKC);  // (past the end: the last chunk again, not used)
+      __builtin_amdgcn_sched_barrier(0);  // the loads stay ahead of the next products
+      __syncthreads();
+    }
+  }
+  // KS = 2: the waves of one tile exchange halves of their sums, so each
+  // finishes eight of the sixteen rows of registers
+  if constexpr (KS == 2) {
+    float* part = reinterpret_cast<float*>(smem) + (wave & 3) * 1024 + lane;
+    const int mine = (wave >> 2) * 8;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const float other = mine ? acc[0][r] : acc[0][8 + r];
+      part[64 * (8 - mine + r)] = other;
     }
     __syncthreads();
 #pragma unroll
-    for (int s = 0; s < kKC / 16; ++s) {
-      const int k = 16 * s + 8 * lh;
-      const half8 ph = *reinterpret_cast<const half8*>(&sp[0][mw + li][k]);
-      const half8 pl = *reinterpret_cast<const half8*>(&sp[1][mw + li][k]);
-      const half8 qh = *reinterpret_cast<const half8*>(&sq[0][nw + li][k]);
-      const half8 ql = *reinterpret_cast<const half8*>(&sq[1][nw + li][k]);
-      acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph, ql, acc, 0, 0, 0);
-      acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(pl, qh, acc, 0, 0, 0);
-      acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph, qh, acc, 0, 0, 0);
-    }
+    for (int r = 0; r < 8; ++r) acc[0][r] = (mine ? acc[0][8 + r] : acc[0][r]) + part[64 * (mine + r)];
     __syncthreads();
   }
-  const int j = j0 + nw + li;
+  // Two LDS tiles of two planes: `cols` holds the tile by columns (rows of X^T,
+  // or of the symmetric A and B), `rows` by rows.
+  constexpr int kOut = T + 8, kTilePlane = T * kOut, kPieces = T * T / 8 / kGemmThreads;
+  _Float16* cols = smem;
+  _Float16* rows = smem + 2 * kTilePlane;
+  const int64_t col_at = bz * (PHASE == kGram || PHASE == kPoly ? b.asize : b.tsize) + (int64_t)j0 * b.rl + i0;
+  auto piece = [&](int u, int& row, int& k) {
+    const int n = tid + u * kGemmThreads;
+    row = n / (T / 8);
+    k = (n % (T / 8)) * 8;
+  };
+  if constexpr (PHASE != kGram) {  // the old tile: A of kPoly, X of the others
+    const _Float16* from[2] = {(PHASE == kPoly ? b.ah : b.th) + col_at, (PHASE == kPoly ? b.al : b.tl) + col_at};
 #pragma unroll
-  for (int rq = 0; rq < 4; ++rq) {
-    const int i = i0 + mw + 8 * rq + 4 * lh;  // four consecutive rows of one column
-    half4 h4, l4;
+    for (int z = 0; z < 2; ++z)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float v = acc[4 * rq + e];
-      if constexpr (PHASE == kGram || PHASE == kPoly) {
-        const int64_t at = bz * asize + (int64_t)(i + e) * b.rp + j;
-        _Float16 h, l;
-        if constexpr (PHASE == kGram) {
-          split2(v * pow2(st.ea - 2 * st.ex), h, l);
-          b.ah[at] = h;
-          b.al[at] = l;
+      for (int u = 0; u < kPieces; ++u) {
+        int row, k;
+        piece(u, row, k);
+        *reinterpret_cast<half8*>(cols + z * kTilePlane + row * kOut + k) =
+            *reinterpret_cast<const half8*>(from[z] + (int64_t)row * b.rl + k);
+      }
+    __syncthreads();
+  }
+  const int lj = nw + li, first = KS == 2 ? (wave >> 2) * 2 : 0;
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int rq = 0; rq < 4 / KS; ++rq) {
+      const int i = mw + 32 * t + 8 * (rq + first) + 4 * lh;  // four consecutive rows of one column of the tile
+      _Float16* at = cols + lj * kOut + i;
+      half4 oh = {0, 0, 0, 0}, ol = {0, 0, 0, 0}, h4, l4;
+      if constexpr (PHASE != kGram) {
+        oh = *reinterpret_cast<const half4*>(at);
+        ol = *reinterpret_cast<const half4*>(at + kTilePlane);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float old = (float)oh[e] + (float)ol[e], c = acc[t][4 * rq + e];
+        float v;
+        if constexpr (PHASE == kGram)
+          v = c * pow2(st.ea - 2 * st.ex);
+        else if constexpr (PHASE == kPoly)
+          v = (st.b * (old * pow2(-st.ea)) + st.c * (c * pow2(-2 * st.ea))) * pow2(st.eb);
+        else
+          v = st.a * (old * pow2(-st.ex)) + c * pow2(-st.ex - st.eb);
+        if constexpr (PHASE == kLast) {
+          const int gi = i0 + i + e, gj = j0 + lj;
+          if (gi < b.r && gj < b.c) {
+            const int64_t o = b.m.offset + bz * b.m.stride +
+                              (b.transposed ? (int64_t)gj * b.m.cols + gi : (int64_t)gi * b.m.cols + gj);
+            if (b.update) {
+              v = (1.f - b.u.lr * b.u.decay) * b.u.W[o] - b.u.lr * b.scale * v;
+              if (b.u.w_bf16) b.u.w_bf16[o] = __builtin_bit_cast(uint16_t, (__bf16)v);
+            }
+            b.u.out[o] = v;
+          }
         } else {
-          const float av = ((float)b.ah[at] + (float)b.al[at]) * pow2(-st.ea);
-          split2((st.b * av + st.c * (v * pow2(-2 * st.ea))) * pow2(st.eb), h, l);
-          b.bh[at] = h;
-          b.bl[at] = l;
-        }
-      } else {
-        const int64_t at = bz * xsize + (int64_t)(i + e) * b.cp + j;
-        const float x = ((float)b.xh[at] + (float)b.xl[at]) * pow2(-st.ex);
-        const float y = st.a * x + v * pow2(-st.ex - st.eb);
-        if constexpr (PHASE == kApply) {
           _Float16 h, l;
-          split2(y * pow2(ex_next), h, l);
-          b.xh[at] = h;
-          b.xl[at] = l;
+          split2(PHASE == kApply ? v * pow2(ex_next) : v, h, l);
           h4[e] = h;
           l4[e] = l;
-        } else if (i + e < b.r && j < b.c) {
-          const int64_t o = b.m.offset + bz * b.m.stride +
-                            (b.transposed ? (int64_t)j * b.m.cols + i + e : (int64_t)(i + e) * b.m.cols + j);
-          if (b.update) {
-            const float w = (1.f - b.u.lr * b.u.decay) * b.u.W[o] - b.u.lr * b.scale * y;
-            b.u.out[o] = w;
-            if (b.u.w_bf16) b.u.w_bf16[o] = __builtin_bit_cast(uint16_t, (__bf16)w);
-          } else {
-            b.u.out[o] = y;
-          }
+          rows[(i + e) * kOut + lj] = h;
+          rows[kTilePlane + (i + e) * kOut + lj] = l;
         }
       }
+      if constexpr (PHASE != kLast) {
+        *reinterpret_cast<half4*>(at) = h4;
+        *reinterpret_cast<half4*>(at + kTilePlane) = l4;
+      }
     }
-    if constexpr (PHASE == kApply) {
-      const int64_t t = bz * xsize + (int64_t)j * b.rp + i;
-      *reinterpret_cast<half4*>(b.nh + t) = h4;
-      *reinterpret_cast<half4*>(b.nl + t) = l4;
-    }
+  if constexpr (PHASE != kLast) {
+    __syncthreads();
+    _Float16* to[2] = {(PHASE == kGram ? b.ah : PHASE == kPoly ? b.bh : b.nh) + col_at,
+                       (PHASE == kGram ? b.al : PHASE == kPoly ? b.bl : b.nl) + col_at};
+    const int ld = PHASE == kApply ? b.cl : b.rl;
+    const int64_t row_at = bz * (PHASE == kApply ? b.xsize : b.asize) + (int64_t)i0 * ld + j0;
+    _Float16* mirror[2] = {(PHASE == kGram ? b.ah : PHASE == kPoly ? b.bh : b.xh) + row_at,
+                           (PHASE == kGram ? b.al : PHASE == kPoly ? b.bl : b.xl) + row_at};
+#pragma unroll
+    for (int z = 0; z < 2; ++z)
+#pragma unroll
+      for (int u = 0; u < kPieces; ++u) {
+        int row, k;
+        piece(u, row, k);
+        *reinterpret_cast<half8*>(to[z] + (int64_t)row * b.rl + k) =
+            *reinterpret_cast<const half8*>(cols + z * kTilePlane + row * kOut + k);
+        if (PHASE == kApply || i0 != j0)
+          *reinterpret_cast<half8*>(mirror[z] + (int64_t)row * ld + k) =
+              *reinterpret_cast<const half8*>(rows + z * kTilePlane + row * kOut + k);
+      }
   }
 }
 
@@ -539,17 +691,37 @@ void set_bank(const MuonPlan& p, int i, Bank& b) {
   b.transposed = b.m.rows > b.m.cols;
   b.r = b.transposed ? b.m.cols : b.m.rows;
   b.c = b.transposed ? b.m.rows : b.m.cols;
-  b.rp = (b.r + kTile - 1) / kTile * kTile;
-  b.cp = (b.c + kTile - 1) / kTile * kTile;
+  // 128-wide tiles where they are enough for the 256 CUs
+  const int64_t R = (b.r + 127) / 128, C = (b.c + 127) / 128;
+  b.square_tile = R * (R + 1) / 2 * b.m.count >= 256 ? 128 : 64;
+  b.apply_tile = R * C * b.m.count >= 192 ? 128 : 64;
+  const int pad = b.square_tile > b.apply_tile ? b.square_tile : b.apply_tile;
+  b.rp = (b.r + pad - 1) / pad * pad;
+  b.cp = (b.c + pad - 1) / pad * pad;
+  b.rl = b.rp + kSkew;
+  b.cl = b.cp + kSkew;
+  b.xsize = (int64_t)b.rp * b.cl;
+  b.tsize = (int64_t)b.cp * b.rl;
+  b.asize = (int64_t)b.rp * b.rl;
   b.chunks = (int32_t)(((int64_t)b.m.rows * b.m.cols + kNormChunk - 1) / kNormChunk);
   b.eps = p.eps;
   b.scale = b.m.cols > b.m.rows ? sqrtf((float)b.m.cols / (float)b.m.rows) : 1.f;
 }
 
+template <int PHASE>
+void launch_phase(const Bank& b, int tile, const MuonStep& st, int ex_next, hipStream_t s) {
+  const int R = b.rp / tile, C = b.cp / tile, tiles = PHASE == kGram || PHASE == kPoly ? R * (R + 1) / 2 : R * C;
+  const dim3 g((unsigned)((tiles * b.m.count + 7) / 8 * 8));
+  if (tile == 128)
+    hipLaunchKernelGGL((muon_gemm_kernel<PHASE, 128>), g, dim3(kGemmThreads), 0, s, b, st, ex_next, tiles);
+  else
+    hipLaunchKernelGGL((muon_gemm_kernel<PHASE, 64>), g, dim3(kGemmThreads), 0, s, b, st, ex_next, tiles);
+}
+
 // X in two planes, X^T in two buffers of two planes, A and B.
 size_t bank_bytes(const Bank& b) {
-  const size_t x = (size_t)b.m.count * b.rp * b.cp * 2, a = (size_t)b.m.count * b.rp * b.rp * 2;
-  return align_up((size_t)b.m.count * b.chunks * 4) + align_up(6 * x) + align_up(4 * a);
+  const size_t n = (size_t)b.m.count * 2;
+  return align_up((size_t)b.m.count * b.chunks * 4) + n * (2 * b.xsize + 4 * b.tsize + 4 * b.asize);
 }
 
 }  // namespace
@@ -575,32 +747,34 @@ hipError_t launch_muon(const MuonPlan& p, const MuonUpdate& u, void* ws, hipStre
     if (b.m.count == 0 || small_kind(b.m) >= 0) continue;
     b.u = u;
     b.update = u.W != nullptr;
-    const size_t x = (size_t)b.m.count * b.rp * b.cp, a = (size_t)b.m.count * b.rp * b.rp;
     b.norm = static_cast<float*>(ws);
-    _Float16* h = reinterpret_cast<_Float16*>(static_cast<char*>(ws) + align_up((size_t)b.m.count * b.chunks * 4));
-    b.xh = h;
-    b.xl = h + x;
-    b.th = h + 2 * x;
-    b.tl = h + 3 * x;
-    b.nh = h + 4 * x;
-    b.nl = h + 5 * x;
-    b.ah = reinterpret_cast<_Float16*>(reinterpret_cast<char*>(h) + align_up(12 * x));
-    b.al = b.ah + a;
-    b.bh = b.ah + 2 * a;
-    b.bl = b.ah + 3 * a;
-    const unsigned n = (unsigned)b.m.count, R = b.rp / kTile, C = b.cp / kTile;
+    _Float16* at = reinterpret_cast<_Float16*>(static_cast<char*>(ws) + align_up((size_t)b.m.count * b.chunks * 4));
+    auto take = [&](int64_t size) {
+      _Float16* p = at;
+      at += b.m.count * size;
+      return p;
+    };
+    b.xh = take(b.xsize);
+    b.xl = take(b.xsize);
+    b.th = take(b.tsize);
+    b.tl = take(b.tsize);
+    b.nh = take(b.tsize);
+    b.nl = take(b.tsize);
+    b.ah = take(b.asize);
+    b.al = take(b.asize);
+    b.bh = take(b.asize);
+    b.bl = take(b.asize);
+    const unsigned n = (unsigned)b.m.count;
     hipLaunchKernelGGL(muon_norm_kernel, dim3(b.chunks, n), dim3(kThreads), 0, s, b);
-    const int64_t pad = (int64_t)b.rp * b.cp;
-    hipLaunchKernelGGL(muon_init_kernel, dim3((unsigned)((pad + 4 * kThreads - 1) / (4 * kThreads)), n), dim3(kThreads),
-                       0, s, b, p.step[0].ex);
+    hipLaunchKernelGGL(muon_init_kernel, dim3(b.cp / 64, b.rp / 64, n), dim3(kThreads), 0, s, b, p.step[0].ex);
     for (int k = 0; k < p.nsteps; ++k) {
-      const MuonStep& st = p.step[k];
-      hipLaunchKernelGGL((muon_gemm_kernel<kGram>), dim3(R, R, n), dim3(kThreads), 0, s, b, st, 0);
-      hipLaunchKernelGGL((muon_gemm_kernel<kPoly>), dim3(R, R, n), dim3(kThreads), 0, s, b, st, 0);
+      const int ex_next = p.step[k + 1].ex;
+      launch_phase<kGram>(b, b.square_tile, p.step[k], ex_next, s);
+      launch_phase<kPoly>(b, b.square_tile, p.step[k], ex_next, s);
       if (k + 1 < p.nsteps)
-        hipLaunchKernelGGL((muon_gemm_kernel<kApply>), dim3(C, R, n), dim3(kThreads), 0, s, b, st, p.step[k + 1].ex);
+        launch_phase<kApply>(b, b.apply_tile, p.step[k], ex_next, s);
       else
-        hipLaunchKernelGGL((muon_gemm_kernel<kLast>), dim3(C, R, n), dim3(kThreads), 0, s, b, st, 0);
+        launch_phase<kLast>(b, b.apply_tile, p.step[k], ex_next, s);
       std::swap(b.th, b.nh);
       std::swap(b.tl, b.nl);
     }
