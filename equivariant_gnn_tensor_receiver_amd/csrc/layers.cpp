@@ -39,7 +39,6 @@ namespace {
 tpconv_status dev(hipError_t e) { return e == hipSuccess ? TPCONV_SUCCESS : TPCONV_ERROR_DEVICE; }
 bool bad_dtype(int t) { return t != TPCONV_F32 && t != TPCONV_BF16; }
 bool bad_count(int64_t n) { return n < 0 || n >= INT32_MAX; }
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 // Irreps of one side and their feature offsets.
 tpconv_status parse_side(const char* text, std::vector<Irrep>& ir, std::vector<int32_t>& off, int64_t& F) {
@@ -80,7 +79,6 @@ NormArgs norm_args(const tpconv_norm_s& h, int64_t N) {
 void rows_args(const tpconv_linear_s& h, bool grad, int64_t N, const int32_t* offsets, const int32_t* order,
                const void* in, const void* W, void* out, LinRowsArgs& a) {
   std::memset(&a, 0, sizeof(a));
-  const auto& from = grad ? h.out : h.in;
   const auto& to = grad ? h.in : h.out;
   const auto& to_off = grad ? h.in_off : h.out_off;
   a.G = h.groups;
@@ -97,12 +95,6 @@ void rows_args(const tpconv_linear_s& h, bool grad, int64_t N, const int32_t* of
   a.in = in;
   a.W = W;
   a.out = out;
-  // wide loads (16 bytes along the reduction; channel pairs of W in the forward): every row of
-  // the tensor and every block within it starts on such a boundary
-  const int xm = a.in_bf16 ? 8 : 4, wm = grad ? (a.w_bf16 ? 8 : 4) : 2;
-  a.vec_x = aligned16(in) && a.F_in % xm == 0;
-  for (const auto& r : from) a.vec_x = a.vec_x && r.mul % xm == 0;
-  a.vec_w = aligned16(W) && h.w_numel % wm == 0;
   int ns = 0;
   for (size_t o = 0; o < to.size(); ++o) {
     LinJob& J = a.job[a.njobs++];
@@ -117,7 +109,6 @@ void rows_args(const tpconv_linear_s& h, bool grad, int64_t N, const int32_t* of
       S.len = grad ? b.mo : b.mi;
       S.ldw = b.mo;
       S.woff = b.woff;
-      a.vec_w = a.vec_w && b.mo % wm == 0 && b.woff % wm == 0;
       J.nseg++;
     }
   }
@@ -138,12 +129,6 @@ void gw_args(const tpconv_linear_s& h, int64_t N, const int32_t* offsets, const 
   a.gy = gy;
   a.gW = gW;
   a.part = part;
-  // channel pairs in one load: every row of every block starts on two elements of an aligned tensor
-  auto aligned = [](const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; };
-  a.vec_x = aligned(x, a.x_bf16 ? 4 : 8) && h.F_in % 2 == 0;
-  for (const auto& r : h.in) a.vec_x = a.vec_x && r.mul % 2 == 0;
-  a.vec_y = aligned(gy, 8) && h.F_out % 2 == 0;
-  for (const auto& r : h.out) a.vec_y = a.vec_y && r.mul % 2 == 0;
   for (const auto& b : h.blocks) {
     LinGwJob& J = a.job[a.njobs++];
     J.n = b.n;
@@ -423,7 +408,7 @@ tpconv_status tpconv_linear_backward(tpconv_linear linear, int64_t num_nodes, co
                                      const int32_t* order, const void* x, const void* W, const float* grad_y,
                                      float* grad_x, float* grad_W, void* workspace, size_t workspace_bytes,
                                      void* stream) {
-  tpconv_status st = linear_inputs(linear, num_nodes, offsets, order);
+  const tpconv_status st = linear_inputs(linear, num_nodes, offsets, order);
   if (st != TPCONV_SUCCESS) return st;
   if (!grad_x && !grad_W) return TPCONV_ERROR_INVALID_VALUE;
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -432,17 +417,15 @@ tpconv_status tpconv_linear_backward(tpconv_linear linear, int64_t num_nodes, co
   if (!grad_y || (grad_x && !W && linear->w_numel > 0) || (grad_W && !x)) return TPCONV_ERROR_INVALID_VALUE;
   const size_t need = grad_W ? linear_workspace(*linear, TPCONV_OP_BACKWARD, num_nodes) : 0;
   if (need > 0 && (!workspace || workspace_bytes < need)) return TPCONV_ERROR_WORKSPACE;
-  if (grad_x) {
-    LinRowsArgs a;
-    rows_args(*linear, true, num_nodes, offsets, order, grad_y, W, grad_x, a);
-    if ((st = dev(launch_lin_rows(a, s))) != TPCONV_SUCCESS) return st;
-  }
-  if (grad_W && !linear->blocks.empty()) {
-    LinGwArgs a;
-    gw_args(*linear, num_nodes, offsets, order, x, grad_y, grad_W, static_cast<float*>(workspace), a);
-    return dev(launch_lin_gw(a, s));
-  }
-  return TPCONV_SUCCESS;
+  LinBackwardArgs a;
+  std::memset(&a, 0, sizeof(a));
+  if (grad_x) rows_args(*linear, true, num_nodes, offsets, order, grad_y, W, grad_x, a.rows);
+  if (grad_W && !linear->blocks.empty())
+    gw_args(*linear, num_nodes, offsets, order, x, grad_y, grad_W, static_cast<float*>(workspace), a.gw);
+  a.rows.w_bf16 = linear->w_dtype == TPCONV_BF16;
+  a.gw.x_bf16 = linear->x_dtype == TPCONV_BF16;
+  if (a.rows.njobs == 0 && a.gw.njobs == 0) return TPCONV_SUCCESS;
+  return dev(launch_lin_backward(a, s));
 }
 
 // ---- orthogonalised update ----------------------------------------------------------

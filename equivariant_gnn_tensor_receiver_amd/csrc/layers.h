@@ -72,10 +72,11 @@ struct LinJob {
   int32_t off, cols;   // feature offset and channels of the output block
   int32_t seg0, nseg;
   int32_t tiles_n;     // column tiles
+  int32_t by_row;      // row tiles numbered by their first row (fewer rows than groups)
   int64_t first_tile;  // first block of the job in the launch
 };
 struct LinRowsArgs {
-  int32_t njobs, G, vec_x, vec_w;
+  int32_t njobs, G;
   int32_t in_bf16, w_bf16, out_bf16, wt;  // wt: B(c, c') = W[c'][c] (input gradient)
   int64_t N, F_in, F_out, w_per_group, tiles;
   const int32_t* offsets;  // NULL: one group
@@ -90,17 +91,18 @@ struct LinRowsArgs {
 // Weight-gradient kernel: W_g[c][c'] = sum over the rows (v, m) of group g in[(v, m), c] gy[(v, m), c'].
 struct LinGwJob {
   int32_t n, mi, mo, xoff, yoff;
-  int32_t width;        // tile width
   int32_t tiles_i, tiles_o;
   int32_t rshift;       // rows per slot = 1 << rshift
+  int32_t by_row;       // slots numbered by their first row (fewer rows than groups)
   int64_t woff;
   int64_t first_tile;   // first block of the job
-  int64_t slots;        // row slots: (N n >> rshift) + G
+  int64_t slots;        // row slots: (N n >> rshift) + G, or N n
   int64_t part_off;     // [slots][mi][mo] partial sums
   int64_t first_elem;   // first element of the job in the reduction launch
 };
 struct LinGwArgs {
-  int32_t njobs, G, x_bf16, vec_x, vec_y;
+  int32_t njobs, G, x_bf16;
+  int32_t width;  // tile width
   int64_t N, F_in, F_out, w_per_group, tiles, elems;
   const int32_t* offsets;
   const int32_t* order;
@@ -111,10 +113,17 @@ struct LinGwArgs {
   LinGwJob job[kMaxLinBlocks];
 };
 
+// Both gradients: njobs = 0 leaves one out.
+struct LinBackwardArgs {
+  LinRowsArgs rows;    // gy -> gx
+  LinGwArgs gw;
+  int64_t rows_first;  // first block of the input gradient
+};
+
 hipError_t launch_lin_rows(LinRowsArgs& a, hipStream_t s);
 // Fills the slots of the jobs and returns the floats of partial sums.
 int64_t lin_gw_plan(LinGwArgs& a);
-hipError_t launch_lin_gw(LinGwArgs& a, hipStream_t s);
+hipError_t launch_lin_backward(LinBackwardArgs& a, hipStream_t s);
 size_t lin_groups_workspace(int64_t N, int G);
 hipError_t launch_lin_groups_validate(const int32_t* group, int64_t N, int G, int32_t* flag, hipStream_t s);
 hipError_t launch_lin_groups(const int32_t* group, int64_t N, int G, int32_t* offsets, int32_t* order, void* ws,

@@ -58,42 +58,74 @@ struct Slot {
   int g;
   int64_t node0, rows, row0;
 };
-__device__ __forceinline__ bool find_slot(const int32_t* offsets, int G, int64_t N, int n, int shift, int64_t t,
-                                          Slot& s) {
+__device__ __forceinline__ bool find_slot(const int32_t* offsets, int G, int64_t N, int n, int shift, bool by_row,
+                                          int64_t t, Slot& s) {
   if (!offsets) {
     s = {0, 0, N * n, t << shift};
     return s.row0 < s.rows;
   }
   const int lane = threadIdx.x & 63;
-  int count = 0;
-  for (int base = 0; base < G; base += 64) {
+  // lane l looks at group base + l; the last group that starts at or before t
+  // is the tile's (group 0 starts at tile 0), its ends are in two lanes
+  int64_t o0 = 0, o1 = 0;
+  int32_t before_last = 0;
+  for (int base = 0; base <= G; base += 64) {
     const int g = base + lane;
-    const bool before = g < G && (((int64_t)offsets[g < G ? g : 0] * n) >> shift) + g <= t;
-    const uint64_t mask = __ballot(before);
-    count += __popcll(mask);
-    if (~mask) break;
+    const int32_t off = offsets[g <= G ? g : G];
+    const int64_t start = (int64_t)off * n;
+    const uint64_t mask = __ballot(g < G && (by_row ? start : (start >> shift) + g) <= t);
+    const int count = __popcll(mask);
+    if (count < 64) {
+      s.g = base + count - 1;
+      o0 = count > 0 ? __builtin_amdgcn_readlane(off, count - 1) : before_last;
+      o1 = __builtin_amdgcn_readlane(off, count);
+      break;
+    }
+    before_last = __builtin_amdgcn_readlane(off, 63);
   }
-  s.g = count - 1;  // group 0 starts at tile 0, so count >= 1
-  const int64_t o0 = offsets[s.g], o1 = offsets[s.g + 1];
   s.node0 = o0;
   s.rows = (o1 - o0) * n;
+  if (by_row) {
+    s.row0 = t - o0 * n;
+    return s.row0 < s.rows && (s.row0 & ((int64_t(1) << shift) - 1)) == 0;
+  }
   s.row0 = (t - (((o0 * n) >> shift) + s.g)) << shift;
   return s.row0 < s.rows;
+}
+
+// The job of a block: the last one whose first tile is at or before it, one lane per job.
+template <typename J>
+__device__ __forceinline__ int find_job(const J* job, int njobs, int64_t tile) {
+  static_assert(kMaxLinBlocks <= 64 && kMaxGroups <= 64, "one lane per job");
+  const int lane = threadIdx.x & 63;
+  return __popcll(__ballot(lane < njobs && job[lane < njobs ? lane : 0].first_tile <= tile)) - 1;
 }
 
 __device__ __forceinline__ int64_t div_rows(int64_t r, int n) {
   return n == 1 ? r : n == 3 ? r / 3 : n == 5 ? r / 5 : r / 7;
 }
 
-// Eight values along the reduction of one row: p[k..k+8), as loaded.  Reads
-// past `len` are moved inside the row (vec: len is a multiple of the vector)
-// and the values zeroed by mask_run8 before use, so every load is issued
-// unconditionally and can stay in flight while the previous chunk is multiplied.
-__device__ __forceinline__ void load_run8(const float* p, int k, int len, bool vec, float (&v)[8]) {
-  if (vec) {
+// Wide accesses at any element's address (the hardware needs no more alignment).
+typedef float floatx4_any __attribute__((ext_vector_type(4), aligned(4)));
+typedef float floatx2_any __attribute__((ext_vector_type(2), aligned(4)));
+typedef unsigned int u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef unsigned int u32_any __attribute__((aligned(2)));
+
+// Eight values along the reduction of one row: p[k..k+8), as loaded.  Runs past
+// `len` read on into the memory behind the row (a run wholly past it reads the
+// row's start) and mask_run8 zeroes what they got before use, so every load is
+// wide, issued unconditionally, and can stay in flight while the previous chunk
+// is multiplied.  Blocks that could read past the tensor's `end` that way (not
+// WIDE) take the elements of such a run one by one.  WIDE is a compile-time
+// copy of the main loop: with the choice made at every load the compiler waits
+// for the loads in flight where the two ways meet (force-sized forward 41 -> 52 us).
+template <bool WIDE>
+__device__ __forceinline__ void load_run8(const float* p, int k, int len, const float* end, float (&v)[8]) {
+  const float* q = p + (k < len ? k : 0);
+  if (WIDE || q + 8 <= end) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const floatx4 x = *reinterpret_cast<const floatx4*>(p + min(k + 4 * j, len - 4));
+      const floatx4 x = *reinterpret_cast<const floatx4_any*>(q + 4 * j);
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[4 * j + e] = x[e];
     }
@@ -102,9 +134,11 @@ __device__ __forceinline__ void load_run8(const float* p, int k, int len, bool v
     for (int j = 0; j < 8; ++j) v[j] = p[min(k + j, len - 1)];
   }
 }
-__device__ __forceinline__ void load_run8(const uint16_t* p, int k, int len, bool vec, u32x4& v) {
-  if (vec) {
-    v = *reinterpret_cast<const u32x4*>(p + min(k, len - 8));
+template <bool WIDE>
+__device__ __forceinline__ void load_run8(const uint16_t* p, int k, int len, const uint16_t* end, u32x4& v) {
+  const uint16_t* q = p + (k < len ? k : 0);
+  if (WIDE || q + 8 <= end) {
+    v = *reinterpret_cast<const u32x4_any*>(q);
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -122,11 +156,12 @@ __device__ __forceinline__ void mask_run8(u32x4& v, int left) {
     v[j] = 2 * j + 1 < left ? v[j] : 2 * j < left ? v[j] & 0xffffu : 0u;
 }
 
-// Two neighbouring columns c, c + 1 of one row (c + 1 may lie past `cols`: a
-// value from inside the row, its column is never stored).
-__device__ __forceinline__ void load_pair(const float* p, int c, int cols, bool vec, float& a, float& b) {
-  if (vec) {
-    const float2 x = *reinterpret_cast<const float2*>(p + min(c, cols - 2));
+// Two neighbouring columns c, c + 1 of one row; columns past `cols` take a
+// value from inside the row (they are never stored).  WIDE: see wide_pairs.
+template <bool WIDE>
+__device__ __forceinline__ void load_pair(const float* p, int c, int cols, float& a, float& b) {
+  if constexpr (WIDE) {
+    const floatx2_any x = *reinterpret_cast<const floatx2_any*>(p + min(c, cols - 2));
     a = x.x;
     b = x.y;
   } else {
@@ -134,10 +169,13 @@ __device__ __forceinline__ void load_pair(const float* p, int c, int cols, bool 
     b = p[min(c + 1, cols - 1)];
   }
 }
-__device__ __forceinline__ uint32_t load_pair(const uint16_t* p, int c, int cols, bool vec) {
-  if (vec) return *reinterpret_cast<const uint32_t*>(p + min(c, cols - 2));
+template <bool WIDE>
+__device__ __forceinline__ uint32_t load_pair(const uint16_t* p, int c, int cols) {
+  if constexpr (WIDE) return *reinterpret_cast<const u32_any*>(p + min(c, cols - 2));
   return (uint32_t)p[min(c, cols - 1)] | ((uint32_t)p[min(c + 1, cols - 1)] << 16);
 }
+// Whether the columns [c0, c0 + width) of rows of `cols` can be loaded in pairs: none straddles the row's end.
+__device__ __forceinline__ bool wide_pairs(int c0, int width, int cols) { return cols % 2 == 0 || c0 + width < cols; }
 
 template <typename T>
 struct Planes;
@@ -207,12 +245,19 @@ struct PairPart {
   uint32_t h[sizeof(T) == 2 ? kPasses : 1][8];
   static __device__ __forceinline__ bool mine() { return kWhole || (int)threadIdx.x < kPer * (KC / 8); }
   static __device__ __forceinline__ int col() { return 2 * ((int)threadIdx.x % kPer); }
-  static __device__ __forceinline__ int k(int p) { return (p * (kThreads / kPer) + (int)threadIdx.x / kPer) * 8; }
-  __device__ __forceinline__ void load(int p, int j, const float* at, int c, int cols, bool vec) {
-    load_pair(at, c, cols, vec, f[p][0][j], f[p][1][j]);
+  // (64 or more threads per group: the group is uniform over the wave, and said so)
+  static __device__ __forceinline__ int k(int p) {
+    const int g = (int)threadIdx.x / kPer;
+    return (p * (kThreads / kPer) + (kPer >= 64 ? __builtin_amdgcn_readfirstlane(g) : g)) * 8;
   }
-  __device__ __forceinline__ void load(int p, int j, const uint16_t* at, int c, int cols, bool vec) {
-    h[p][j] = load_pair(at, c, cols, vec);
+  static constexpr bool kUniform = kPer >= 64;
+  template <bool WIDE>
+  __device__ __forceinline__ void load(int p, int j, const float* at, int c, int cols) {
+    load_pair<WIDE>(at, c, cols, f[p][0][j], f[p][1][j]);
+  }
+  template <bool WIDE>
+  __device__ __forceinline__ void load(int p, int j, const uint16_t* at, int c, int cols) {
+    h[p][j] = load_pair<WIDE>(at, c, cols);
   }
   template <int LD>
   __device__ __forceinline__ void put(uint16_t (*s)[ROWS][LD], int left) {
@@ -285,19 +330,31 @@ __device__ __forceinline__ void store_out(uint16_t* p, int64_t i, float v) {
 // take WM x WN each, with KS = 4 every wave takes a quarter of the reduction of
 // the whole tile and the sums are added in order through LDS.  LDS rows are
 // padded by 16 bytes, so 16-byte reads of 16 rows touch every bank once.
-template <int BM_, int BN_, int WM_, int WN_, int KS_, int KC_>
+// AHEAD chunks of loads are in flight (more than one pays where few blocks wait
+// for memory: four rows over 64 experts took 16.3 us with one, see RowsShape).
+template <int BM_, int BN_, int WM_, int WN_, int KS_, int KC_, int AHEAD_ = 1>
 struct Shape {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, KS = KS_, KC = KC_, LD = KC_ + 8;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, KS = KS_, KC = KC_, LD = KC_ + 8, kAhead = AHEAD_;
   static constexpr int MT = WM / 32, NT = WN / 32;
   static_assert((BM / WM) * (BN / WN) * KS == kThreads / 64, "four waves");
 };
 
 constexpr int max_int(int a, int b) { return a > b ? a : b; }
 
-// LDS bytes of a shape: the operands' planes, later the partial sums of KS > 1.
+// LDS bytes: the operands' planes (later the partial sums of KS > 1) and the
+// tables of row addresses.
 template <typename S, int PA, int PB>
-constexpr int lds_bytes() {
+constexpr int plane_bytes() {
   return max_int((PA * S::BM + PB * S::BN) * S::LD * 2, (S::KS - 1) * S::BM * S::BN * 4);
+}
+constexpr int kRowTable = 256;  // weight gradient: rows of a slot whose addresses are in LDS at a time
+template <typename S, int PA, int PB>
+constexpr int rows_lds() {
+  return plane_bytes<S, PA, PB>() + 2 * S::BM * 4;
+}
+template <typename S, int PA>
+constexpr int gw_lds() {
+  return plane_bytes<S, PA, 3>() + 2 * kRowTable * 8;
 }
 
 // Adds the waves' sums of KS > 1 in order; the result is wave 0's.
@@ -319,27 +376,24 @@ __device__ __forceinline__ void join_waves(floatx16 (&acc)[S::MT][S::NT], char* 
 }
 
 template <typename S, typename TI, typename TW, typename TO, bool WT>
-__global__ __launch_bounds__(kThreads, 2) void lin_rows_kernel(const LinRowsArgs /*args*/) {
-  const LinRowsArgs& a = *(const LinRowsArgs*)__builtin_amdgcn_kernarg_segment_ptr();
+__device__ __forceinline__ void lin_rows(const LinRowsArgs& a, int64_t block, char* smem) {
   constexpr int PA = Planes<TI>::count, PB = Planes<TW>::count, BM = S::BM, BN = S::BN, KC = S::KC, LD = S::LD;
-  __shared__ __align__(16) char smem[lds_bytes<S, PA, PB>()];
-  __shared__ int32_t s_node[BM], s_m[BM];
+  int32_t* s_node = reinterpret_cast<int32_t*>(smem + plane_bytes<S, PA, PB>());
+  int32_t* s_m = s_node + BM;
   uint16_t(*sa)[BM][LD] = reinterpret_cast<uint16_t(*)[BM][LD]>(smem);
   uint16_t(*sb)[BN][LD] = reinterpret_cast<uint16_t(*)[BN][LD]>(smem + PA * BM * LD * 2);
   // consecutive tiles (the column tiles of one row tile, then its group's next
   // rows) run on one XCD and share its L2
-  const int64_t tile = xcd_item(blockIdx.x, gridDim.x);
+  const int64_t tile = xcd_item(block, (a.tiles + 7) / 8 * 8);
   if (tile >= a.tiles) return;
-  int ji = 0;
-  while (ji + 1 < a.njobs && tile >= a.job[ji + 1].first_tile) ++ji;
-  const LinJob& J = a.job[ji];
+  const LinJob& J = a.job[find_job(a.job, a.njobs, tile)];
   const int64_t lt = tile - J.first_tile;
   const int64_t tm = lt / J.tiles_n;
   const int n0 = (int)(lt - tm * J.tiles_n) * BN;
   Slot s;
   constexpr int kShift = BM == 128 ? 7 : BM == 64 ? 6 : 5;
   static_assert(BM == 1 << kShift, "row tile");
-  if (!find_slot(a.offsets, a.G, a.N, J.n, kShift, tm, s)) return;
+  if (!find_slot(a.offsets, a.G, a.N, J.n, kShift, J.by_row, tm, s)) return;
   const int tid = threadIdx.x, wave = tid >> 6;
   if (tid < BM) {
     const int64_t r = s.row0 + tid;
@@ -359,62 +413,97 @@ __global__ __launch_bounds__(kThreads, 2) void lin_rows_kernel(const LinRowsArgs
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
   const TI* in = static_cast<const TI*>(a.in);
   const TW* Wg = static_cast<const TW*>(a.W) + s.g * a.w_per_group;
+  const TI* in_end = in + a.N * a.F_in;
+  const TW* w_end = static_cast<const TW*>(a.W) + a.G * a.w_per_group;
 
   using PartA = RunPart<TI, BM, KC>;
   using PartB = std::conditional_t<WT, RunPart<TW, BN, KC>, PairPart<TW, BN, KC>>;
-  PartA pa;
-  PartB pb;
+  constexpr int kAhead = S::kAhead;
   const TI* row_ptr[PartA::kPasses];
   int row_m[PartA::kPasses];
+  // reads past a row could leave the tensor: rows at its end whose length is not a multiple of a run
+  bool near_end = false, odd = false;
+  for (int i = 0; i < J.nseg; ++i) {
+    const LinSeg& G = a.seg[J.seg0 + i];
+    const bool tail = G.len % 8 != 0;
+    odd = odd || tail;
+    if constexpr (WT) near_end = near_end || (tail && Wg + G.woff + (int64_t)min(n0 + BN, J.cols) * G.ldw + 8 > w_end);
+  }
+  if constexpr (!WT) near_end = !wide_pairs(n0, BN, J.cols);
 #pragma unroll
   for (int p = 0; p < PartA::kPasses; ++p) {
     const int m = s_m[PartA::row(p) % BM];
     row_m[p] = m < 0 ? -1 - m : m;
     row_ptr[p] = in + (int64_t)s_node[PartA::row(p) % BM] * a.F_in;
+    near_end = near_end || (odd && row_ptr[p] + a.F_in + 8 > in_end);
   }
-  auto load = [&](const LinSeg& G, int k0) {
+  auto main_loop = [&](auto wide) {
+    constexpr bool WIDE = decltype(wide)::value;
+    PartA pa[kAhead];
+    PartB pb[kAhead];
+    // the next chunk to load and the one to multiply: segment and first reduction
+    int lsi = 0, lk = 0, si = 0, k0 = 0;
+    auto load = [&](int d) {
+      if (lsi >= J.nseg) return;
+      const LinSeg& G = a.seg[J.seg0 + lsi];
+      const int k0 = lk;
+      lk += KC;
+      if (lk >= G.len) {
+        lk = 0;
+        ++lsi;
+      }
 #pragma unroll
-    for (int p = 0; p < PartA::kPasses; ++p)
-      if (PartA::mine()) load_run8(row_ptr[p] + G.off + row_m[p] * G.len, k0 + PartA::k(), G.len, a.vec_x, pa.raw[p].v);
-    if (PartB::mine()) {
-      if constexpr (WT) {  // B(k, c') = W[c'][k]
+      for (int p = 0; p < PartA::kPasses; ++p)
+        if (PartA::mine())
+          load_run8<WIDE>(row_ptr[p] + G.off + row_m[p] * G.len, k0 + PartA::k(), G.len, in_end, pa[d].raw[p].v);
+      if (PartB::mine()) {
+        if constexpr (WT) {  // B(k, c') = W[c'][k]
 #pragma unroll
-        for (int p = 0; p < PartB::kPasses; ++p)
-          load_run8(Wg + G.woff + (int64_t)min(n0 + PartB::row(p), J.cols - 1) * G.ldw, k0 + PartB::k(), G.len, a.vec_w,
-                    pb.raw[p].v);
-      } else {  // B(k, c') = W[k][c']
+          for (int p = 0; p < PartB::kPasses; ++p)
+            load_run8<WIDE>(Wg + G.woff + (int64_t)min(n0 + PartB::row(p), J.cols - 1) * G.ldw, k0 + PartB::k(), G.len, w_end,
+                            pb[d].raw[p].v);
+        } else {  // B(k, c') = W[k][c']
 #pragma unroll
-        for (int p = 0; p < PartB::kPasses; ++p)
+          for (int p = 0; p < PartB::kPasses; ++p)
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            pb.load(p, j, Wg + G.woff + (int64_t)min(k0 + PartB::k(p) + j, G.len - 1) * G.ldw, n0 + PartB::col(), J.cols,
-                    a.vec_w);
+            for (int j = 0; j < 8; ++j)
+              pb[d].template load<WIDE>(p, j, Wg + G.woff + (int64_t)min(k0 + PartB::k(p) + j, G.len - 1) * G.ldw, n0 + PartB::col(), J.cols);
+        }
+      }
+    };
+#pragma unroll
+    for (int d = 0; d < kAhead; ++d) load(d);
+    while (si < J.nseg) {
+#pragma unroll
+      for (int d = 0; d < kAhead; ++d) {
+        if (si >= J.nseg) break;
+        const int left = a.seg[J.seg0 + si].len - k0;
+        pa[d].template put<LD>(sa, left);
+        pb[d].template put<LD>(sb, left);
+        __syncthreads();
+        k0 += KC;
+        if (left <= KC) {
+          k0 = 0;
+          ++si;
+        }
+        load(d);
+        __builtin_amdgcn_sched_barrier(0);  // the loads stay ahead of the products
+        if constexpr (S::KS > 1) {
+          const int kw = wave * (KC / S::KS);  // a wave without reductions left skips its products
+          if (kw < left) multiply<PA, PB, S::MT, S::NT, BM, BN, LD>(sa, sb, 0, 0, kw, KC / (16 * S::KS), acc);
+        } else {
+          constexpr int kCols = BN / S::WN;
+          multiply<PA, PB, S::MT, S::NT, BM, BN, LD>(sa, sb, (wave / kCols) * S::WM, (wave % kCols) * S::WN, 0, KC / 16,
+                                                     acc);
+        }
+        __syncthreads();
       }
     }
   };
-  int si = 0, k0 = 0;
-  if (J.nseg > 0) load(a.seg[J.seg0], 0);
-  while (si < J.nseg) {
-    const int left = a.seg[J.seg0 + si].len - k0;
-    pa.template put<LD>(sa, left);
-    pb.template put<LD>(sb, left);
-    __syncthreads();
-    k0 += KC;
-    if (left <= KC) {
-      k0 = 0;
-      ++si;
-    }
-    if (si < J.nseg) load(a.seg[J.seg0 + si], k0);
-    __builtin_amdgcn_sched_barrier(0);  // the loads stay ahead of the products
-    if constexpr (S::KS > 1) {
-      const int kw = wave * (KC / S::KS);  // a wave without reductions left skips its products
-      if (kw < left) multiply<PA, PB, S::MT, S::NT, BM, BN, LD>(sa, sb, 0, 0, kw, KC / (16 * S::KS), acc);
-    } else {
-      constexpr int kCols = BN / S::WN;
-      multiply<PA, PB, S::MT, S::NT, BM, BN, LD>(sa, sb, (wave / kCols) * S::WM, (wave % kCols) * S::WN, 0, KC / 16, acc);
-    }
-    __syncthreads();
-  }
+  if (__syncthreads_or(near_end))
+    main_loop(std::false_type{});
+  else
+    main_loop(std::true_type{});
   join_waves<S>(acc, smem);
   if (S::KS > 1 && wave > 0) return;
   constexpr int kCols = S::KS > 1 ? 1 : BN / S::WN;
@@ -436,28 +525,25 @@ __global__ __launch_bounds__(kThreads, 2) void lin_rows_kernel(const LinRowsArgs
 // Weight gradient: one BM x BN tile of gW_g over the rows of one slot.  A group
 // with a single slot is written at once, others through partial sums that
 // lin_gw_reduce_kernel adds in order.
-constexpr int kRowTable = 512;  // rows of a slot whose addresses are in LDS at a time
-
 template <typename S, typename TX>
-__global__ __launch_bounds__(kThreads, 2) void lin_gw_kernel(const LinGwArgs /*args*/) {
-  const LinGwArgs& a = *(const LinGwArgs*)__builtin_amdgcn_kernarg_segment_ptr();
+__device__ __forceinline__ void lin_gw(const LinGwArgs& a, int64_t tile, char* smem) {
   constexpr int PA = Planes<TX>::count, PB = 3, BM = S::BM, BN = S::BN, KC = S::KC, LD = S::LD;
-  __shared__ __align__(16) char smem[lds_bytes<S, PA, PB>()];
-  __shared__ int64_t s_x[kRowTable], s_y[kRowTable];
+  int64_t* s_x = reinterpret_cast<int64_t*>(smem + plane_bytes<S, PA, PB>());
+  int64_t* s_y = s_x + kRowTable;
   uint16_t(*sa)[BM][LD] = reinterpret_cast<uint16_t(*)[BM][LD]>(smem);
   uint16_t(*sb)[BN][LD] = reinterpret_cast<uint16_t(*)[BN][LD]>(smem + PA * BM * LD * 2);
-  const int64_t tile = xcd_item(blockIdx.x, gridDim.x);
-  if (tile >= a.tiles) return;
-  int ji = 0;
-  while (ji + 1 < a.njobs && tile >= a.job[ji + 1].first_tile) ++ji;
-  const LinGwJob& J = a.job[ji];
+  // every slot's tiles are shared out evenly over the XCDs (groups differ in
+  // size, so whole slots per XCD would leave most of them waiting), each
+  // XCD taking a run of them: the tiles of one or two column tiles of gy
+  const LinGwJob& J = a.job[find_job(a.job, a.njobs, tile)];
   const int64_t lt = tile - J.first_tile;
   const int tiles = J.tiles_i * J.tiles_o;
   const int64_t slot = lt / tiles;
-  const int ti = (int)(lt - slot * tiles);
-  const int i0 = (ti / J.tiles_o) * BM, o0 = (ti % J.tiles_o) * BN;
+  int ti = (int)(lt - slot * tiles);
+  if (tiles % 8 == 0) ti = (ti & 7) * (tiles >> 3) + (ti >> 3);
+  const int i0 = (ti % J.tiles_i) * BM, o0 = (ti / J.tiles_i) * BN;
   Slot s;
-  if (!find_slot(a.offsets, a.G, a.N, J.n, J.rshift, slot, s)) return;
+  if (!find_slot(a.offsets, a.G, a.N, J.n, J.rshift, J.by_row, slot, s)) return;
   const int rows = (int)min(s.rows - s.row0, int64_t(1) << J.rshift);
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   floatx16 acc[S::MT][S::NT];
@@ -471,52 +557,76 @@ __global__ __launch_bounds__(kThreads, 2) void lin_gw_kernel(const LinGwArgs /*a
   const float* gy = a.gy + J.yoff;
   using PartA = PairPart<TX, BM, KC>;
   using PartB = PairPart<float, BN, KC>;
-  PartA pa;
-  PartB pb;
-  auto load = [&](int r0) {
-    if (r0 % kRowTable == 0) {  // the next rows' addresses (no thread reads the old ones any more)
-      __syncthreads();
-      for (int i = tid; i < kRowTable; i += kThreads) {
-        const int64_t r = s.row0 + min(r0 + i, rows - 1);
-        const int64_t p = div_rows(r, J.n);
-        const int32_t m = (int32_t)(r - p * J.n);
-        const int64_t node = a.order ? a.order[s.node0 + p] : p;
-        s_x[i] = node * a.F_in + (int64_t)m * J.mi;
-        s_y[i] = node * a.F_out + (int64_t)m * J.mo;
-      }
-      __syncthreads();
-    }
-    const int t0 = r0 % kRowTable;
-    if (PartA::mine())
-#pragma unroll
-      for (int p = 0; p < PartA::kPasses; ++p)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          pa.load(p, j, x + s_x[t0 + PartA::k(p) + j], i0 + PartA::col(), J.mi, a.vec_x);
-    if (PartB::mine())
-#pragma unroll
-      for (int p = 0; p < PartB::kPasses; ++p)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          pb.load(p, j, gy + s_y[t0 + PartB::k(p) + j], o0 + PartB::col(), J.mo, a.vec_y);
+  constexpr int kAhead = S::kAhead;
+  // a row's offset from the table, moved to scalar registers where the wave reads one row
+  auto row_at = [&](const int64_t* table, int i, auto uniform) -> int64_t {
+    const int64_t v = table[i];
+    if constexpr (!decltype(uniform)::value) return v;
+    return (int64_t)(((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32) |
+                     (uint32_t)__builtin_amdgcn_readfirstlane((int)v));
   };
-  load(0);
-  for (int r0 = 0; r0 < rows; r0 += KC) {
-    const int left = rows - r0;
-    pa.template put<LD>(sa, left);
-    pb.template put<LD>(sb, left);
-    __syncthreads();
-    if (left > KC) load(r0 + KC);
-    __builtin_amdgcn_sched_barrier(0);  // the loads stay ahead of the products
-    if constexpr (S::KS > 1) {
-      const int kw = wave * (KC / S::KS);
-      if (kw < left) multiply<PA, PB, S::MT, S::NT, BM, BN, LD>(sa, sb, 0, 0, kw, KC / (16 * S::KS), acc);
-    } else {
-      constexpr int kCols = BN / S::WN;
-      multiply<PA, PB, S::MT, S::NT, BM, BN, LD>(sa, sb, (wave / kCols) * S::WM, (wave % kCols) * S::WN, 0, KC / 16, acc);
+  auto main_loop = [&](auto wide) {
+    constexpr bool WIDE = decltype(wide)::value;
+    PartA pa[kAhead];
+    PartB pb[kAhead];
+    auto load = [&](int d, int r0) {
+      if (r0 >= rows) return;
+      if (r0 % kRowTable == 0) {  // the next rows' addresses (no thread reads the old ones any more)
+        __syncthreads();
+        for (int i = tid; i < kRowTable; i += kThreads) {
+          const int64_t r = s.row0 + min(r0 + i, rows - 1);
+          const int64_t p = div_rows(r, J.n);
+          const int32_t m = (int32_t)(r - p * J.n);
+          const int64_t node = a.order ? a.order[s.node0 + p] : p;
+          s_x[i] = node * a.F_in + (int64_t)m * J.mi;
+          s_y[i] = node * a.F_out + (int64_t)m * J.mo;
+        }
+        __syncthreads();
+      }
+      const int t0 = r0 % kRowTable;
+      if (PartA::mine())
+#pragma unroll
+        for (int p = 0; p < PartA::kPasses; ++p)
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            pa[d].template load<WIDE>(p, j, x + row_at(s_x, t0 + PartA::k(p) + j, std::bool_constant<PartA::kUniform>{}), i0 + PartA::col(),
+                    J.mi);
+      if (PartB::mine())
+#pragma unroll
+        for (int p = 0; p < PartB::kPasses; ++p)
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            pb[d].template load<WIDE>(p, j, gy + row_at(s_y, t0 + PartB::k(p) + j, std::bool_constant<PartB::kUniform>{}), o0 + PartB::col(),
+                    J.mo);
+    };
+#pragma unroll
+    for (int d = 0; d < kAhead; ++d) load(d, d * KC);
+    for (int r = 0; r < rows; r += kAhead * KC) {
+#pragma unroll
+      for (int d = 0; d < kAhead; ++d) {
+        const int r0 = r + d * KC, left = rows - r0;
+        if (left <= 0) break;
+        pa[d].template put<LD>(sa, left);
+        pb[d].template put<LD>(sb, left);
+        __syncthreads();
+        load(d, r0 + kAhead * KC);
+        __builtin_amdgcn_sched_barrier(0);  // the loads stay ahead of the products
+        if constexpr (S::KS > 1) {
+          const int kw = wave * (KC / S::KS);
+          if (kw < left) multiply<PA, PB, S::MT, S::NT, BM, BN, LD>(sa, sb, 0, 0, kw, KC / (16 * S::KS), acc);
+        } else {
+          constexpr int kCols = BN / S::WN;
+          multiply<PA, PB, S::MT, S::NT, BM, BN, LD>(sa, sb, (wave / kCols) * S::WM, (wave % kCols) * S::WN, 0, KC / 16,
+                                                     acc);
+        }
+        __syncthreads();
+      }
     }
-    __syncthreads();
-  }
+  };
+  if (wide_pairs(i0, BM, J.mi) && wide_pairs(o0, BN, J.mo))
+    main_loop(std::true_type{});
+  else
+    main_loop(std::false_type{});
   join_waves<S>(acc, smem);
   if (S::KS > 1 && wave > 0) return;
   constexpr int kCols = S::KS > 1 ? 1 : BN / S::WN;
@@ -536,23 +646,50 @@ __global__ __launch_bounds__(kThreads, 2) void lin_gw_kernel(const LinGwArgs /*a
     }
 }
 
+template <typename S, typename TI, typename TW, typename TO, bool WT>
+__global__ __launch_bounds__(kThreads, 2) void lin_rows_kernel(const LinRowsArgs /*args*/) {
+  __shared__ __align__(16) char smem[rows_lds<S, Planes<TI>::count, Planes<TW>::count>()];
+  lin_rows<S, TI, TW, TO, WT>(*(const LinRowsArgs*)__builtin_amdgcn_kernarg_segment_ptr(), blockIdx.x, smem);
+}
+
+// Both gradients in one launch: the weight gradient's tiles, then the input
+// gradient's.  They read the same gy and wait for memory at different times.
+template <typename S, typename SG, typename TX, typename TW>
+__global__ __launch_bounds__(kThreads, 2) void lin_backward_kernel(const LinBackwardArgs /*args*/) {
+  const LinBackwardArgs& a = *(const LinBackwardArgs*)__builtin_amdgcn_kernarg_segment_ptr();
+  __shared__ __align__(16) char smem[max_int(rows_lds<S, 3, Planes<TW>::count>(), gw_lds<SG, Planes<TX>::count>())];
+  if ((int64_t)blockIdx.x < a.rows_first) {
+    if ((int64_t)blockIdx.x < a.gw.tiles) lin_gw<SG, TX>(a.gw, blockIdx.x, smem);
+  } else {
+    lin_rows<S, float, TW, float, true>(a.rows, blockIdx.x - a.rows_first, smem);
+  }
+}
+
 // gW of the groups with several slots (their partial sums in slot order) or none (zero).
-__global__ __launch_bounds__(kThreads) void lin_gw_reduce_kernel(const LinGwArgs /*args*/) {
+// `run` elements per thread: one, or eight where most threads would find nothing to do.
+__global__ __launch_bounds__(kThreads) void lin_gw_reduce_kernel(const LinGwArgs /*args*/, int run) {
   const LinGwArgs& a = *(const LinGwArgs*)__builtin_amdgcn_kernarg_segment_ptr();
-  const int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   const int g = blockIdx.y;
-  if (e >= a.elems) return;
-  int ji = 0;
-  while (ji + 1 < a.njobs && e >= a.job[ji + 1].first_elem) ++ji;
-  const LinGwJob& J = a.job[ji];
   const int64_t o0 = a.offsets ? a.offsets[g] : 0, o1 = a.offsets ? a.offsets[g + 1] : a.N;
-  const int64_t slots = ((o1 - o0) * J.n + (int64_t(1) << J.rshift) - 1) >> J.rshift;
-  if (slots == 1) return;
-  const int64_t size = (int64_t)J.mi * J.mo, le = e - J.first_elem;
-  const float* p = a.part + J.part_off + (((o0 * J.n) >> J.rshift) + g) * size + le;
-  float v = 0.f;
-  for (int64_t i = 0; i < slots; ++i) v += p[i * size];
-  a.gW[g * a.w_per_group + J.woff + le] = v;
+  const int64_t first = (int64_t)blockIdx.x * (kThreads * run), last = min(a.elems, first + kThreads * run);
+  int ji = 0;
+  while (ji + 1 < a.njobs && first >= a.job[ji + 1].first_elem) ++ji;
+  for (; ji < a.njobs && a.job[ji].first_elem < last; ++ji) {  // the jobs this block's run of elements meets
+    const LinGwJob& J = a.job[ji];
+    const int64_t slots = ((o1 - o0) * J.n + (int64_t(1) << J.rshift) - 1) >> J.rshift;
+    if (slots == 1) continue;
+    const int64_t size = (int64_t)J.mi * J.mo;
+    const float* p = a.part + J.part_off + (J.by_row ? o0 * J.n : ((o0 * J.n) >> J.rshift) + g) * size;
+    const int64_t next = J.by_row ? size << J.rshift : size;
+    float* dst = a.gW + g * a.w_per_group + J.woff;
+    const int64_t e1 = min(last - J.first_elem, size);
+    for (int64_t e = max(first - J.first_elem, int64_t(0)) + threadIdx.x; e < e1; e += kThreads) {
+      float v = 0.f;
+#pragma unroll 8
+      for (int64_t i = 0; i < slots; ++i) v += p[i * next + e];
+      dst[e] = v;
+    }
+  }
 }
 
 // ---- grouping: a stable counting sort of the nodes by group ----------------------
@@ -691,100 +828,163 @@ struct RowsShape {
 };
 template <bool ONE>
 struct RowsShape<0, ONE> {
-  using type = Shape<32, 32, 32, 32, 4, 128>;
+  using type = Shape<32, 32, 32, 32, 4, 128, ONE ? 4 : 2>;
 };
 
-template <int BN, typename TI, typename TW, typename TO, bool WT>
+template <int BN, typename TI, typename TW, typename TO>
 hipError_t launch_rows_typed(const LinRowsArgs& a, hipStream_t s) {
   using S = typename RowsShape<BN, Planes<TI>::count == 1 && Planes<TW>::count == 1>::type;
-  hipLaunchKernelGGL((lin_rows_kernel<S, TI, TW, TO, WT>), dim3(xcd_grid(a.tiles)), dim3(kThreads), 0, s, a);
+  hipLaunchKernelGGL((lin_rows_kernel<S, TI, TW, TO, false>), dim3(xcd_grid(a.tiles)), dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
-
 template <int BN>
-hipError_t launch_rows_shape(const LinRowsArgs& a, hipStream_t s) {
+hipError_t launch_rows_types(const LinRowsArgs& a, hipStream_t s) {
   using H = uint16_t;
-  if (a.wt)
-    return a.w_bf16 ? launch_rows_typed<BN, float, H, float, true>(a, s) : launch_rows_typed<BN, float, float, float, true>(a, s);
   switch ((a.in_bf16 ? 4 : 0) + (a.w_bf16 ? 2 : 0) + (a.out_bf16 ? 1 : 0)) {
-    case 0: return launch_rows_typed<BN, float, float, float, false>(a, s);
-    case 1: return launch_rows_typed<BN, float, float, H, false>(a, s);
-    case 2: return launch_rows_typed<BN, float, H, float, false>(a, s);
-    case 3: return launch_rows_typed<BN, float, H, H, false>(a, s);
-    case 4: return launch_rows_typed<BN, H, float, float, false>(a, s);
-    case 5: return launch_rows_typed<BN, H, float, H, false>(a, s);
-    case 6: return launch_rows_typed<BN, H, H, float, false>(a, s);
-    default: return launch_rows_typed<BN, H, H, H, false>(a, s);
+    case 0: return launch_rows_typed<BN, float, float, float>(a, s);
+    case 1: return launch_rows_typed<BN, float, float, H>(a, s);
+    case 2: return launch_rows_typed<BN, float, H, float>(a, s);
+    case 3: return launch_rows_typed<BN, float, H, H>(a, s);
+    case 4: return launch_rows_typed<BN, H, float, float>(a, s);
+    case 5: return launch_rows_typed<BN, H, float, H>(a, s);
+    case 6: return launch_rows_typed<BN, H, H, float>(a, s);
+    default: return launch_rows_typed<BN, H, H, H>(a, s);
   }
 }
 
-// Column tile of an output block: the padded columns, wider tiles preferred
-// (they re-read the rows less often).
-int rows_width(int cols) {
-  const int p128 = (cols + 127) / 128 * 128, p64 = (cols + 63) / 64 * 64, p32 = (cols + 31) / 32 * 32;
-  if (p128 * 4 <= p64 * 5) return 128;
-  return p64 * 4 <= p32 * 5 ? 64 : 32;
+// Weight-gradient shapes of the same widths (0: of launches of few rows).
+template <int BN>
+struct GwShape {
+  using type = Shape<128, 128, 64, 64, 1, 32>;
+};
+template <>
+struct GwShape<64> {
+  using type = Shape<64, 64, 32, 32, 1, 64>;
+};
+template <>
+struct GwShape<32> {
+  using type = Shape<32, 32, 32, 32, 4, 64>;
+};
+template <>
+struct GwShape<0> {
+  using type = Shape<32, 32, 32, 32, 4, 64>;
+};
+
+template <int BN, int BG, typename TX, typename TW>
+hipError_t launch_backward_typed(LinBackwardArgs& a, hipStream_t s) {
+  using S = typename RowsShape<BN, false>::type;
+  a.rows_first = (a.gw.tiles + 7) / 8 * 8;
+  const int64_t grid = a.rows_first + (a.rows.tiles + 7) / 8 * 8;
+  if (grid >= INT32_MAX) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((lin_backward_kernel<S, typename GwShape<BG>::type, TX, TW>), dim3((unsigned)grid), dim3(kThreads), 0, s, a);
+  return hipGetLastError();
+}
+template <int BN, int BG>
+hipError_t launch_backward_types(LinBackwardArgs& a, hipStream_t s) {
+  using H = uint16_t;
+  if (a.gw.x_bf16)
+    return a.rows.w_bf16 ? launch_backward_typed<BN, BG, H, H>(a, s) : launch_backward_typed<BN, BG, H, float>(a, s);
+  return a.rows.w_bf16 ? launch_backward_typed<BN, BG, float, H>(a, s) : launch_backward_typed<BN, BG, float, float>(a, s);
+}
+template <int BN>
+hipError_t launch_backward_shapes(int gw_width, LinBackwardArgs& a, hipStream_t s) {
+  return gw_width == 128  ? launch_backward_types<BN, 128>(a, s)
+         : gw_width == 64 ? launch_backward_types<BN, 64>(a, s)
+                          : launch_backward_types<BN, 32>(a, s);
 }
 
-// Weight-gradient tile of a block: the padded area, larger tiles preferred.
-int gw_width(int mi, int mo) {
-  auto area = [&](int64_t t) { return ((mi + t - 1) / t * t) * ((mo + t - 1) / t * t); };
-  if (area(128) * 2 <= area(64) * 3) return 128;
-  return area(64) <= area(32) * 2 ? 64 : 32;
+// Row tiles (or slots) of 1 << shift rows that cover every split of N n rows over G groups.
+int64_t row_tiles(int64_t rows, int G, int shift, int32_t& by_row) {
+  const int64_t tiles = (rows >> shift) + G;
+  by_row = rows < tiles;
+  return by_row ? rows : tiles;
+}
+
+// Tiles of the rows jobs of a launch, all of one shape (a launch per shape would
+// run one after the other: the ragged training step took 91 us in seven
+// launches).  The width is the one with the least padded work; narrow tiles
+// count more per column because they re-read the rows and share less (factors
+// 5/4 per halving); 0: the 32 x 32 shape of launches of few rows.
+int plan_rows(LinRowsArgs& a) {
+  int width = 128;
+  double best = 0.0;
+  int64_t big = 0;
+  for (int w : {128, 64, 32}) {
+    double cost = 0.0;
+    int64_t blocks = 0;
+    for (int j = 0; j < a.njobs; ++j) {
+      const int64_t tiles = (a.job[j].cols + w - 1) / w;
+      cost += (double)a.N * a.job[j].n * tiles * w * (w == 128 ? 1.0 : w == 64 ? 1.25 : 1.5625);
+      blocks += ((a.N * a.job[j].n + 127) / 128) * tiles;
+    }
+    if (w == 128 || cost < best) {
+      best = cost;
+      width = w;
+      big = blocks;
+    }
+  }
+  if (big < 64) width = 0;
+  const int bn = width ? width : 32, shift = width ? 7 : 5;
+  a.tiles = 0;
+  for (int j = 0; j < a.njobs; ++j) {
+    LinJob& J = a.job[j];
+    J.tiles_n = (J.cols + bn - 1) / bn;
+    J.first_tile = a.tiles;
+    a.tiles += row_tiles(a.N * J.n, a.offsets ? a.G : 1, shift, J.by_row) * J.tiles_n;
+  }
+  return width;
+}
+
+// The same for the weight gradient's tiles of W x W; smaller tiles read both operands more often.
+int gw_width(const LinGwArgs& a) {
+  int width = 128;
+  double best = 0.0;
+  for (int w : {128, 64, 32}) {
+    double cost = 0.0;
+    for (int j = 0; j < a.njobs; ++j) {
+      const double ti = (a.job[j].mi + w - 1) / w, to = (a.job[j].mo + w - 1) / w;
+      cost += (double)a.job[j].n * ti * to * w * w * (w == 128 ? 1.0 : w == 64 ? 1.5 : 3.0);
+    }
+    if (w == 128 || cost < best) {
+      best = cost;
+      width = w;
+    }
+  }
+  return width;
 }
 
 }  // namespace
 
 hipError_t launch_lin_rows(LinRowsArgs& a, hipStream_t s) {
   TimingScope ts(kcLinear, s);
-  for (int width : {128, 64, 32}) {
-    LinRowsArgs k = a;
-    k.njobs = 0;
-    int64_t big = 0;
-    for (int j = 0; j < a.njobs; ++j)
-      if (rows_width(a.job[j].cols) == width) {
-        LinJob& J = k.job[k.njobs++];
-        J = a.job[j];
-        J.tiles_n = (J.cols + width - 1) / width;
-        big += ((a.N * J.n + 127) / 128) * J.tiles_n;
-      }
-    if (k.njobs == 0) continue;
-    const bool few = big < 64;
-    const int bm = few ? 32 : 128, bn = few ? 32 : width;
-    k.tiles = 0;
-    for (int j = 0; j < k.njobs; ++j) {
-      LinJob& J = k.job[j];
-      J.tiles_n = (J.cols + bn - 1) / bn;
-      J.first_tile = k.tiles;
-      k.tiles += ((a.N * J.n) / bm + a.G) * J.tiles_n;
-    }
-    if (k.tiles >= INT32_MAX - 8) return hipErrorInvalidValue;
-    const hipError_t e = few            ? launch_rows_shape<0>(k, s)
-                         : width == 128 ? launch_rows_shape<128>(k, s)
-                         : width == 64  ? launch_rows_shape<64>(k, s)
-                                        : launch_rows_shape<32>(k, s);
-    if (e != hipSuccess) return e;
-  }
-  return hipSuccess;
+  const int width = plan_rows(a);
+  if (a.tiles >= INT32_MAX - 8) return hipErrorInvalidValue;
+  return width == 128  ? launch_rows_types<128>(a, s)
+         : width == 64 ? launch_rows_types<64>(a, s)
+         : width == 32 ? launch_rows_types<32>(a, s)
+                       : launch_rows_types<0>(a, s);
 }
 
 int64_t lin_gw_plan(LinGwArgs& a) {
   // rows per slot: about 512 blocks over all jobs, at least 128 rows each
+  a.width = gw_width(a);
   int64_t work = 0;
   for (int j = 0; j < a.njobs; ++j) {
     LinGwJob& J = a.job[j];
-    J.width = gw_width(J.mi, J.mo);
-    J.tiles_i = (J.mi + J.width - 1) / J.width;
-    J.tiles_o = (J.mo + J.width - 1) / J.width;
+    J.tiles_i = (J.mi + a.width - 1) / a.width;
+    J.tiles_o = (J.mo + a.width - 1) / a.width;
     work += a.N * J.n * J.tiles_i * J.tiles_o;
   }
   int shift = 7;
   while (shift < 30 && (work >> shift) > 512) ++shift;
   int64_t part = 0, elems = 0;
+  a.tiles = 0;
   for (int j = 0; j < a.njobs; ++j) {
     LinGwJob& J = a.job[j];
     J.rshift = shift;
-    J.slots = ((a.N * J.n) >> shift) + a.G;
+    J.slots = row_tiles(a.N * J.n, a.G, shift, J.by_row);
+    J.first_tile = a.tiles;
+    a.tiles += J.slots * J.tiles_i * J.tiles_o;
     J.part_off = part;
     part += J.slots * J.mi * J.mo;
     J.first_elem = elems;
@@ -794,43 +994,23 @@ int64_t lin_gw_plan(LinGwArgs& a) {
   return part;
 }
 
-hipError_t launch_lin_gw(LinGwArgs& a, hipStream_t s) {
+hipError_t launch_lin_backward(LinBackwardArgs& a, hipStream_t s) {
   TimingScope ts(kcLinear, s);
-  lin_gw_plan(a);
-  if (a.elems >= (int64_t)INT32_MAX * kThreads) return hipErrorInvalidValue;
-  const dim3 b(kThreads);
-  for (int width : {128, 64, 32}) {
-    LinGwArgs k = a;
-    k.njobs = 0;
-    k.tiles = 0;
-    for (int j = 0; j < a.njobs; ++j)
-      if (a.job[j].width == width) {
-        LinGwJob& J = k.job[k.njobs++];
-        J = a.job[j];
-        J.first_tile = k.tiles;
-        k.tiles += J.slots * J.tiles_i * J.tiles_o;
-      }
-    if (k.njobs == 0) continue;
-    if (k.tiles >= INT32_MAX - 8) return hipErrorInvalidValue;
-    const dim3 g(xcd_grid(k.tiles));
-#define TP_GW(...)                                                                        \
-  do {                                                                                    \
-    if (a.x_bf16)                                                                         \
-      hipLaunchKernelGGL((lin_gw_kernel<Shape<__VA_ARGS__>, uint16_t>), g, b, 0, s, k);   \
-    else                                                                                  \
-      hipLaunchKernelGGL((lin_gw_kernel<Shape<__VA_ARGS__>, float>), g, b, 0, s, k);      \
-  } while (0)
-    if (width == 128)
-      TP_GW(128, 128, 64, 64, 1, 32);
-    else if (width == 64)
-      TP_GW(64, 64, 32, 32, 1, 64);
-    else
-      TP_GW(32, 32, 32, 32, 4, 128);
-#undef TP_GW
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  hipLaunchKernelGGL(lin_gw_reduce_kernel, dim3(blocks(a.elems, kThreads), (unsigned)a.G), b, 0, s, a);
+  int width = 0;
+  a.rows.tiles = a.gw.tiles = 0;
+  if (a.rows.njobs > 0) width = plan_rows(a.rows);
+  if (a.gw.njobs > 0) lin_gw_plan(a.gw);
+  if (a.gw.elems >= (int64_t)INT32_MAX * kThreads) return hipErrorInvalidValue;
+  const hipError_t e = width == 128  ? launch_backward_shapes<128>(a.gw.width, a, s)
+                       : width == 64 ? launch_backward_shapes<64>(a.gw.width, a, s)
+                       : width == 32 ? launch_backward_shapes<32>(a.gw.width, a, s)
+                                     : launch_backward_shapes<0>(a.gw.width, a, s);
+  if (e != hipSuccess || a.gw.njobs == 0) return e;
+  // (49152 x 16 elements over two slots each: 10.6 us with one per thread, 22 with eight;
+  // 2 M x 8 of groups with one slot: 25 us with one, 5.8 with eight)
+  const int run = a.gw.elems * a.gw.G < (int64_t(1) << 22) ? 1 : 8;
+  hipLaunchKernelGGL(lin_gw_reduce_kernel, dim3(blocks(a.gw.elems, kThreads * run), (unsigned)a.gw.G), dim3(kThreads), 0, s,
+                     a.gw, run);
   return hipGetLastError();
 }
 

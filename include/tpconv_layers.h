@@ -19,8 +19,7 @@
  * calls must not share a workspace, nothing allocates, no exception crosses
  * the ABI.  Inputs and outputs must not overlap unless a call allows it.
  * All results are deterministic: every sum has a fixed order, nothing is added
- * with atomics.  Pointers need the alignment of their element type; 16-byte
- * alignment (and multiplicities divisible by 4 or 8) selects wide loads.
+ * with atomics.  Pointers need the alignment of their element type.
  * All sums and statistics are fp32 whatever the input types.
  */
 #ifndef TPCONV_LAYERS_H_
