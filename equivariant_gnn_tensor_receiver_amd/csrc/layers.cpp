@@ -107,8 +107,7 @@ void rows_args(const tpconv_linear_s& h, bool grad, int64_t N, const int32_t* of
       LinSeg& S = a.seg[ns++];
       S.off = grad ? b.yoff : b.xoff;
       S.len = grad ? b.mo : b.mi;
-      S.ldw = b.mo;
-      S.woff = b.woff;
+      S.woff = (int32_t)b.woff;
       J.nseg++;
     }
   }
@@ -136,7 +135,7 @@ void gw_args(const tpconv_linear_s& h, int64_t N, const int32_t* offsets, const 
     J.mo = b.mo;
     J.xoff = b.xoff;
     J.yoff = b.yoff;
-    J.woff = b.woff;
+    J.woff = (int32_t)b.woff;
   }
 }
 
@@ -312,7 +311,7 @@ tpconv_status tpconv_linear_create(tpconv_linear* out, const tpconv_linear_desc*
           h->w_numel += (int64_t)b.mi * b.mo;
           h->blocks.push_back(b);
         }
-      if ((int)h->blocks.size() > kMaxLinBlocks) st = TPCONV_ERROR_UNSUPPORTED;
+      if ((int)h->blocks.size() > kMaxLinBlocks || h->w_numel > INT32_MAX) st = TPCONV_ERROR_UNSUPPORTED;
     }
     if (st != TPCONV_SUCCESS) return st;
     h->groups = desc->num_groups;

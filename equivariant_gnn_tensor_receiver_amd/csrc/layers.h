@@ -61,11 +61,12 @@ struct LinBlock {
 
 // Rows kernel (forward, input gradient): out[(v, m), c'] = sum over segments
 // sum_c in[(v, m), c] B(c, c').
+// (32-bit throughout: the argument blocks are copied at every launch, at about
+// a microsecond per KiB; a group's weights and a launch's tiles stay below 2^31.)
 struct LinSeg {
   int32_t off;   // feature offset of the input block
   int32_t len;   // reduction length
-  int32_t ldw;   // row length of the weight block
-  int64_t woff;
+  int32_t woff;  // weight block within the group's weights
 };
 struct LinJob {
   int32_t n;           // rows per node
@@ -73,7 +74,7 @@ struct LinJob {
   int32_t seg0, nseg;
   int32_t tiles_n;     // column tiles
   int32_t by_row;      // row tiles numbered by their first row (fewer rows than groups)
-  int64_t first_tile;  // first block of the job in the launch
+  int32_t first_tile;  // first block of the job in the launch
 };
 struct LinRowsArgs {
   int32_t njobs, G;
@@ -91,19 +92,16 @@ struct LinRowsArgs {
 // Weight-gradient kernel: W_g[c][c'] = sum over the rows (v, m) of group g in[(v, m), c] gy[(v, m), c'].
 struct LinGwJob {
   int32_t n, mi, mo, xoff, yoff;
-  int32_t tiles_i, tiles_o;
-  int32_t rshift;       // rows per slot = 1 << rshift
+  int32_t woff;         // weight block within a group's weights: also its first element of the reduction launch
   int32_t by_row;       // slots numbered by their first row (fewer rows than groups)
-  int64_t woff;
-  int64_t first_tile;   // first block of the job
-  int64_t slots;        // row slots: (N n >> rshift) + G, or N n
+  int32_t first_tile;   // first block of the job
   int64_t part_off;     // [slots][mi][mo] partial sums
-  int64_t first_elem;   // first element of the job in the reduction launch
 };
 struct LinGwArgs {
   int32_t njobs, G, x_bf16;
-  int32_t width;  // tile width
-  int64_t N, F_in, F_out, w_per_group, tiles, elems;
+  int32_t width;   // tile width
+  int32_t rshift;  // rows per slot = 1 << rshift
+  int64_t N, F_in, F_out, w_per_group, tiles;
   const int32_t* offsets;
   const int32_t* order;
   const void* x;

@@ -427,7 +427,7 @@ __device__ __forceinline__ void lin_rows(const LinRowsArgs& a, int64_t block, ch
     const LinSeg& G = a.seg[J.seg0 + i];
     const bool tail = G.len % 8 != 0;
     odd = odd || tail;
-    if constexpr (WT) near_end = near_end || (tail && Wg + G.woff + (int64_t)min(n0 + BN, J.cols) * G.ldw + 8 > w_end);
+    if constexpr (WT) near_end = near_end || (tail && Wg + G.woff + (int64_t)min(n0 + BN, J.cols) * G.len + 8 > w_end);
   }
   if constexpr (!WT) near_end = !wide_pairs(n0, BN, J.cols);
 #pragma unroll
@@ -460,14 +460,14 @@ __device__ __forceinline__ void lin_rows(const LinRowsArgs& a, int64_t block, ch
         if constexpr (WT) {  // B(k, c') = W[c'][k]
 #pragma unroll
           for (int p = 0; p < PartB::kPasses; ++p)
-            load_run8<WIDE>(Wg + G.woff + (int64_t)min(n0 + PartB::row(p), J.cols - 1) * G.ldw, k0 + PartB::k(), G.len, w_end,
+            load_run8<WIDE>(Wg + G.woff + (int64_t)min(n0 + PartB::row(p), J.cols - 1) * G.len, k0 + PartB::k(), G.len, w_end,
                             pb[d].raw[p].v);
         } else {  // B(k, c') = W[k][c']
 #pragma unroll
           for (int p = 0; p < PartB::kPasses; ++p)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-              pb[d].template load<WIDE>(p, j, Wg + G.woff + (int64_t)min(k0 + PartB::k(p) + j, G.len - 1) * G.ldw, n0 + PartB::col(), J.cols);
+              pb[d].template load<WIDE>(p, j, Wg + G.woff + (int64_t)min(k0 + PartB::k(p) + j, G.len - 1) * J.cols, n0 + PartB::col(), J.cols);
         }
       }
     };
@@ -537,14 +537,14 @@ __device__ __forceinline__ void lin_gw(const LinGwArgs& a, int64_t tile, char* s
   // XCD taking a run of them: the tiles of one or two column tiles of gy
   const LinGwJob& J = a.job[find_job(a.job, a.njobs, tile)];
   const int64_t lt = tile - J.first_tile;
-  const int tiles = J.tiles_i * J.tiles_o;
+  const int tiles_i = (J.mi + BM - 1) / BM, tiles = tiles_i * ((J.mo + BN - 1) / BN);
   const int64_t slot = lt / tiles;
   int ti = (int)(lt - slot * tiles);
   if (tiles % 8 == 0) ti = (ti & 7) * (tiles >> 3) + (ti >> 3);
-  const int i0 = (ti % J.tiles_i) * BM, o0 = (ti / J.tiles_i) * BN;
+  const int i0 = (ti % tiles_i) * BM, o0 = (ti / tiles_i) * BN;
   Slot s;
-  if (!find_slot(a.offsets, a.G, a.N, J.n, J.rshift, J.by_row, slot, s)) return;
-  const int rows = (int)min(s.rows - s.row0, int64_t(1) << J.rshift);
+  if (!find_slot(a.offsets, a.G, a.N, J.n, a.rshift, J.by_row, slot, s)) return;
+  const int rows = (int)min(s.rows - s.row0, int64_t(1) << a.rshift);
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   floatx16 acc[S::MT][S::NT];
 #pragma unroll
@@ -631,7 +631,7 @@ __device__ __forceinline__ void lin_gw(const LinGwArgs& a, int64_t tile, char* s
   if (S::KS > 1 && wave > 0) return;
   constexpr int kCols = S::KS > 1 ? 1 : BN / S::WN;
   const int mw = (wave / kCols) * S::WM, nw = (wave % kCols) * S::WN;
-  const bool whole = s.rows <= (int64_t(1) << J.rshift);
+  const bool whole = s.rows <= (int64_t(1) << a.rshift);
   float* dst = whole ? a.gW + s.g * a.w_per_group + J.woff : a.part + J.part_off + slot * ((int64_t)J.mi * J.mo);
 #pragma unroll
   for (int i = 0; i < S::MT; ++i)
@@ -671,19 +671,19 @@ __global__ __launch_bounds__(kThreads) void lin_gw_reduce_kernel(const LinGwArgs
   const LinGwArgs& a = *(const LinGwArgs*)__builtin_amdgcn_kernarg_segment_ptr();
   const int g = blockIdx.y;
   const int64_t o0 = a.offsets ? a.offsets[g] : 0, o1 = a.offsets ? a.offsets[g + 1] : a.N;
-  const int64_t first = (int64_t)blockIdx.x * (kThreads * run), last = min(a.elems, first + kThreads * run);
+  const int64_t first = (int64_t)blockIdx.x * (kThreads * run), last = min(a.w_per_group, first + kThreads * run);
   int ji = 0;
-  while (ji + 1 < a.njobs && first >= a.job[ji + 1].first_elem) ++ji;
-  for (; ji < a.njobs && a.job[ji].first_elem < last; ++ji) {  // the jobs this block's run of elements meets
+  while (ji + 1 < a.njobs && first >= a.job[ji + 1].woff) ++ji;
+  for (; ji < a.njobs && a.job[ji].woff < last; ++ji) {  // the jobs this block's run of elements meets
     const LinGwJob& J = a.job[ji];
-    const int64_t slots = ((o1 - o0) * J.n + (int64_t(1) << J.rshift) - 1) >> J.rshift;
+    const int64_t slots = ((o1 - o0) * J.n + (int64_t(1) << a.rshift) - 1) >> a.rshift;
     if (slots == 1) continue;
     const int64_t size = (int64_t)J.mi * J.mo;
-    const float* p = a.part + J.part_off + (J.by_row ? o0 * J.n : ((o0 * J.n) >> J.rshift) + g) * size;
-    const int64_t next = J.by_row ? size << J.rshift : size;
+    const float* p = a.part + J.part_off + (J.by_row ? o0 * J.n : ((o0 * J.n) >> a.rshift) + g) * size;
+    const int64_t next = J.by_row ? size << a.rshift : size;
     float* dst = a.gW + g * a.w_per_group + J.woff;
-    const int64_t e1 = min(last - J.first_elem, size);
-    for (int64_t e = max(first - J.first_elem, int64_t(0)) + threadIdx.x; e < e1; e += kThreads) {
+    const int64_t e1 = min(last - J.woff, size);
+    for (int64_t e = max(first - J.woff, int64_t(0)) + threadIdx.x; e < e1; e += kThreads) {
       float v = 0.f;
 #pragma unroll 8
       for (int64_t i = 0; i < slots; ++i) v += p[i * next + e];
@@ -929,7 +929,7 @@ int plan_rows(LinRowsArgs& a) {
   for (int j = 0; j < a.njobs; ++j) {
     LinJob& J = a.job[j];
     J.tiles_n = (J.cols + bn - 1) / bn;
-    J.first_tile = a.tiles;
+    J.first_tile = (int32_t)(a.tiles < INT32_MAX ? a.tiles : INT32_MAX);  // (the launch refuses more)
     a.tiles += row_tiles(a.N * J.n, a.offsets ? a.G : 1, shift, J.by_row) * J.tiles_n;
   }
   return width;
@@ -968,29 +968,24 @@ hipError_t launch_lin_rows(LinRowsArgs& a, hipStream_t s) {
 int64_t lin_gw_plan(LinGwArgs& a) {
   // rows per slot: about 512 blocks over all jobs, at least 128 rows each
   a.width = gw_width(a);
+  auto tiles = [&](const LinGwJob& J) {
+    return (int64_t)((J.mi + a.width - 1) / a.width) * ((J.mo + a.width - 1) / a.width);
+  };
   int64_t work = 0;
-  for (int j = 0; j < a.njobs; ++j) {
-    LinGwJob& J = a.job[j];
-    J.tiles_i = (J.mi + a.width - 1) / a.width;
-    J.tiles_o = (J.mo + a.width - 1) / a.width;
-    work += a.N * J.n * J.tiles_i * J.tiles_o;
-  }
+  for (int j = 0; j < a.njobs; ++j) work += a.N * a.job[j].n * tiles(a.job[j]);
   int shift = 7;
   while (shift < 30 && (work >> shift) > 512) ++shift;
-  int64_t part = 0, elems = 0;
+  a.rshift = shift;
+  int64_t part = 0;
   a.tiles = 0;
   for (int j = 0; j < a.njobs; ++j) {
     LinGwJob& J = a.job[j];
-    J.rshift = shift;
-    J.slots = row_tiles(a.N * J.n, a.G, shift, J.by_row);
-    J.first_tile = a.tiles;
-    a.tiles += J.slots * J.tiles_i * J.tiles_o;
+    const int64_t slots = row_tiles(a.N * J.n, a.G, shift, J.by_row);
+    J.first_tile = (int32_t)(a.tiles < INT32_MAX ? a.tiles : INT32_MAX);  // (the launch refuses more)
+    a.tiles += slots * tiles(J);
     J.part_off = part;
-    part += J.slots * J.mi * J.mo;
-    J.first_elem = elems;
-    elems += (int64_t)J.mi * J.mo;
+    part += slots * J.mi * J.mo;
   }
-  a.elems = elems;
   return part;
 }
 
@@ -1000,7 +995,6 @@ hipError_t launch_lin_backward(LinBackwardArgs& a, hipStream_t s) {
   a.rows.tiles = a.gw.tiles = 0;
   if (a.rows.njobs > 0) width = plan_rows(a.rows);
   if (a.gw.njobs > 0) lin_gw_plan(a.gw);
-  if (a.gw.elems >= (int64_t)INT32_MAX * kThreads) return hipErrorInvalidValue;
   const hipError_t e = width == 128  ? launch_backward_shapes<128>(a.gw.width, a, s)
                        : width == 64 ? launch_backward_shapes<64>(a.gw.width, a, s)
                        : width == 32 ? launch_backward_shapes<32>(a.gw.width, a, s)
@@ -1008,8 +1002,8 @@ hipError_t launch_lin_backward(LinBackwardArgs& a, hipStream_t s) {
   if (e != hipSuccess || a.gw.njobs == 0) return e;
   // (49152 x 16 elements over two slots each: 10.6 us with one per thread, 22 with eight;
   // 2 M x 8 of groups with one slot: 25 us with one, 5.8 with eight)
-  const int run = a.gw.elems * a.gw.G < (int64_t(1) << 22) ? 1 : 8;
-  hipLaunchKernelGGL(lin_gw_reduce_kernel, dim3(blocks(a.gw.elems, kThreads * run), (unsigned)a.gw.G), dim3(kThreads), 0, s,
+  const int run = a.gw.w_per_group * a.gw.G < (int64_t(1) << 22) ? 1 : 8;
+  hipLaunchKernelGGL(lin_gw_reduce_kernel, dim3(blocks(a.gw.w_per_group, kThreads * run), (unsigned)a.gw.G), dim3(kThreads), 0, s,
                      a.gw, run);
   return hipGetLastError();
 }

@@ -113,17 +113,31 @@ def _device(t, name):
     return t.device
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle without a Stream object
+
+
 def _call(fn, device, stream, *args):
     """fn(*args, stream) on the tensors' device, on `stream` or that device's current stream."""
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    if torch.cuda.current_device() != device.index:
-        with torch.cuda.device(device):
-            st = getattr(_LIB, fn)(*args, stream.cuda_stream)
+    index = device.index
+    handle = _raw_stream(index) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == index:
+        st = getattr(_LIB, fn)(*args, handle)
     else:
-        st = getattr(_LIB, fn)(*args, stream.cuda_stream)
+        with torch.cuda.device(device):
+            st = getattr(_LIB, fn)(*args, handle)
     if st != 0:
         raise tp.TpconvError(st, fn)
+
+
+def _new(shape, dtype, device, stream, like=None):
+    """An uninitialised result; one used on another stream is not reused before that stream is done with it."""
+    if like is not None and like.dtype == dtype:
+        t = torch.empty_like(like)
+    else:
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        tp._keep_for_stream(stream, t)
+    return t
 
 
 def _ptr(t):
@@ -143,11 +157,10 @@ def _scratch(workspace, need, device, stream):
     if workspace is None:
         if need == 0:
             return None, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        tp._keep_for_stream(stream, workspace)
-    else:
+        workspace = _new(need, torch.uint8, device, stream)
+    elif workspace.device != device or not workspace.is_contiguous():
         tp._require(workspace, "workspace", None, None, device)
-    return workspace, workspace.numel() * workspace.element_size()
+    return workspace, workspace.nbytes
 
 
 # ---- layer norm ---------------------------------------------------------------------
@@ -195,8 +208,7 @@ def tpconv_norm_forward(norm: Norm, x, weight=None, bias=None, out=None, stats=N
     n = _norm_nodes(norm, x)
     _need(x, "x", norm.x_dtype, n * norm.features, dev)
     if out is None:
-        out = torch.empty(x.shape, dtype=norm.y_dtype, device=dev)
-        tp._keep_for_stream(stream, out)
+        out = _new(x.shape, norm.y_dtype, dev, stream, x)
     else:
         _need(out, "out", norm.y_dtype, n * norm.features, dev)
     if weight is not None:
@@ -218,12 +230,11 @@ def tpconv_norm_backward(norm: Norm, x, weight, grad_y, stats=None, want=("x", "
     _need(x, "x", norm.x_dtype, n * norm.features, dev)
     _need(grad_y, "grad_y", torch.float32, n * norm.features, dev)
     if grad_x is None and "x" in want:
-        grad_x = torch.empty(x.shape, dtype=torch.float32, device=dev)
+        grad_x = _new(x.shape, torch.float32, dev, stream, x)
     if grad_weight is None and "weight" in want:
-        grad_weight = torch.empty(norm.num_weights, dtype=torch.float32, device=dev)
+        grad_weight = _new(norm.num_weights, torch.float32, dev, stream)
     if grad_bias is None and "bias" in want:
-        grad_bias = torch.empty(norm.num_biases, dtype=torch.float32, device=dev)
-    tp._keep_for_stream(stream, grad_x, grad_weight, grad_bias)
+        grad_bias = _new(norm.num_biases, torch.float32, dev, stream)
     if weight is not None:
         _need(weight, "weight", torch.float32, norm.num_weights, dev)
     if stats is not None:
@@ -294,12 +305,11 @@ def tpconv_linear_groups(linear: Linear, group, validate: bool = True, workspace
     dev = _device(group, "group")
     n = group.numel()
     _need(group, "group", torch.int32, n, dev)
-    offsets = torch.empty(linear.num_groups + 1, dtype=torch.int32, device=dev)
-    order = torch.empty(max(n, 1), dtype=torch.int32, device=dev)
+    offsets = _new(linear.num_groups + 1, torch.int32, dev, stream)
+    order = _new(max(n, 1), torch.int32, dev, stream)
     b = c_size_t()
     tp._check(_LIB.tpconv_linear_groups_workspace_size(linear.handle, n, ctypes.byref(b)),
               "tpconv_linear_groups_workspace_size")
-    tp._keep_for_stream(stream, offsets, order)
     workspace, nbytes = _scratch(workspace, b.value, dev, stream)
     _call("tpconv_linear_groups", dev, stream, linear.handle, n, group.data_ptr(), offsets.data_ptr(),
           order.data_ptr(), int(validate), _ptr(workspace), nbytes)
@@ -321,8 +331,7 @@ def tpconv_linear_forward(linear: Linear, groups: Groups, x, W, out=None, worksp
     _need(x, "x", linear.x_dtype, n * linear.feat_in, dev)
     _need(W, "W", linear.w_dtype, linear.num_groups * linear.w_per_group, dev)
     if out is None:
-        out = torch.empty((n, linear.feat_out), dtype=linear.y_dtype, device=dev)
-        tp._keep_for_stream(stream, out)
+        out = _new((n, linear.feat_out), linear.y_dtype, dev, stream)
     else:
         _need(out, "out", linear.y_dtype, n * linear.feat_out, dev)
     workspace, nbytes = _scratch(workspace, linear.workspace_size(n, OP_FORWARD), dev, stream)
@@ -340,10 +349,9 @@ def tpconv_linear_backward(linear: Linear, groups: Groups, x, W, grad_y, want=("
     _need(x, "x", linear.x_dtype, n * linear.feat_in, dev)
     _need(W, "W", linear.w_dtype, linear.num_groups * linear.w_per_group, dev)
     if grad_x is None and "x" in want:
-        grad_x = torch.empty(x.shape, dtype=torch.float32, device=dev)
+        grad_x = _new(x.shape, torch.float32, dev, stream, x)
     if grad_W is None and "W" in want:
-        grad_W = torch.empty(linear.w_shape, dtype=torch.float32, device=dev)
-    tp._keep_for_stream(stream, grad_x, grad_W)
+        grad_W = _new(linear.w_shape, torch.float32, dev, stream)
     if grad_x is not None:
         _need(grad_x, "grad_x", torch.float32, n * linear.feat_in, dev)
     if grad_W is not None:
@@ -412,8 +420,7 @@ def tpconv_muon_orthogonalize(muon: Muon, u, out=None, workspace=None, stream=No
     _muon_tensor(muon, u, "u", torch.float32, u)
     if out is None:
         if u.numel() == muon.dense:
-            out = torch.empty_like(u)
-            tp._keep_for_stream(stream, out)
+            out = _new(u.shape, torch.float32, dev, stream, u)
         else:
             out = _filled(lambda: torch.zeros_like(u), stream)
     else:
@@ -434,13 +441,11 @@ def tpconv_muon_step(muon: Muon, W, grad, momentum, lr: float, beta: float = 0.9
     _muon_tensor(muon, momentum, "momentum", torch.float32, W)
     dense = W.numel() == muon.dense
     if W_out is None:
-        W_out = torch.empty_like(W) if dense else _filled(W.clone, stream)
-        tp._keep_for_stream(stream, W_out)
+        W_out = _new(W.shape, torch.float32, dev, stream, W) if dense else _filled(W.clone, stream)
     else:
         _muon_tensor(muon, W_out, "W_out", torch.float32, W)
     if momentum_out is None:
-        momentum_out = torch.empty_like(momentum) if dense else _filled(momentum.clone, stream)
-        tp._keep_for_stream(stream, momentum_out)
+        momentum_out = _new(W.shape, torch.float32, dev, stream, momentum) if dense else _filled(momentum.clone, stream)
     else:
         _muon_tensor(muon, momentum_out, "momentum_out", torch.float32, W)
     if W_bf16 is not None:

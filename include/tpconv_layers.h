@@ -77,7 +77,8 @@ tpconv_status tpconv_norm_backward(tpconv_norm norm, int64_t num_nodes, const vo
  *   y[v, o, m, c'] = sum_{i ~ o} sum_c x[v, i, m, c] W[group(v)][(i, o)][c, c']
  * over the input irreps i of the same degree and parity as the output irrep o
  * (an output irrep without such an input is zero).  W is [num_groups][w_numel],
- * per group the blocks [mul_i][mul_o] in the order of i, then o.
+ * per group the blocks [mul_i][mul_o] in the order of i, then o (at most 64
+ * blocks and 2^31 - 1 weights per group, or UNSUPPORTED).
  * Products of fp32 operands are exact to fp32: each operand is the sum of three
  * bf16 values and the six products that matter are added in fp32.  A value
  * that is not finite makes the results that it takes part in not finite. */
