@@ -378,9 +378,9 @@ __global__ __launch_bounds__(kGemmThreads) void muon_gemm_kernel(const Bank /*ar
 
 // ---- small matrices: all steps of one matrix in one block of threads ---------------
 // Padded shapes RP x CP that fit the registers and the 160 KB of LDS of one CU.
-// X stays in fp32 accumulator registers over all steps; LDS holds its planes
-// (row-major for X X^T, then transposed for B X) and those of A, later B.  The
-// only global traffic is the update's own.
+// X stays in fp32 accumulator registers over all steps; LDS holds the planes of
+// X^T (read along rows for B X, turned on the way for X X^T) and those of A,
+// later B.  The only global traffic is the update's own.
 
 struct SmallBlock {
   int32_t rows, cols;
@@ -396,75 +396,120 @@ struct SmallArgs {
   SmallBlock block[kMaxMuonBlocks];
 };
 
-template <int RP_, int CP_, int NW_, int TPW_>
+// Tiles of T x T: 32 (v_mfma_f32_32x32x16_f16), or 16 (16x16x32) where a matrix
+// has so few tiles that more, smaller ones are needed to keep the SIMDs busy.
+template <int RP_, int CP_, int T_, int NW_, int TPW_>
 struct Small {
-  static constexpr int RP = RP_, CP = CP_, NW = NW_, TPW = TPW_;
-  static constexpr int RT = RP / 32, CT = CP / 32;
-  static constexpr int APW = RT == 4 ? 2 : 1;               // tiles of A per wave
-  static constexpr int AW = RT * RT / APW;                  // waves that hold tiles of A
-  static constexpr int KS = NW / AW;                        // waves that share the reduction of X X^T
-  static constexpr int LX = CP + 8, LT = RP + 8;            // LDS rows, padded by 16 bytes
-  static constexpr int kX = RP * LX > CP * LT ? RP * LX : CP * LT;
-  static constexpr int kBytes = 2 * (2 * kX + 2 * RP * LT) + (KS - 1) * AW * APW * 1024 * 4;
-  static_assert(RT * CT == NW * TPW && AW * KS == NW, "tiles per wave");
+  static constexpr int RP = RP_, CP = CP_, T = T_, NW = NW_, TPW = TPW_;
+  static constexpr int RT = RP / T, CT = CP / T;
+  static constexpr int APW = RT * RT > NW ? RT * RT / NW : 1;  // tiles of A per wave
+  static constexpr int AW = RT * RT / APW;                     // waves that hold tiles of A
+  static constexpr int KS = NW / AW;                           // waves that share the reduction of X X^T
+  static constexpr int kStep = T == 32 ? 16 : 32;              // reductions of one product
+  // LDS rows of X^T and of A: paddings that keep both the 16-byte reads of 16
+  // rows and the transposing reads of 4 rows x 32 bytes free of bank conflicts
+  static constexpr int LT = RP == 128 ? 152 : RP == 64 ? 72 : 56;
+  static constexpr int LA = RP + 8;
+  static constexpr int kX = CP * LT, kA = RP * LA;
+  static constexpr int kBytes = 2 * 2 * (kX + kA) + (KS - 1) * AW * APW * T * T * 4;
+  static_assert(RT * CT == NW * TPW && AW * KS == NW && CP % (KS * kStep) == 0, "tiles per wave");
   static_assert(kBytes <= 160 * 1024, "LDS");
 };
 
-template <int TILES>
-__device__ __forceinline__ void mul_tiles(const _Float16* p, int lp, int plane_p, const _Float16* q, int lq, int plane_q,
-                                          int k0, int steps, floatx16 (&acc)[TILES]) {
-  // p: rows of TILES stacked 32-row tiles, q: rows of one 32-column tile
-  const int lane = threadIdx.x & 63, i = lane & 31, h = lane >> 5;
+template <int T>
+struct Acc;
+template <>
+struct Acc<32> {
+  typedef floatx16 type;
+  static constexpr int regs = 16;
+  static __device__ __forceinline__ floatx16 mul(half8 a, half8 b, floatx16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+  }
+};
+template <>
+struct Acc<16> {
+  typedef float type __attribute__((ext_vector_type(4)));
+  static constexpr int regs = 4;
+  static __device__ __forceinline__ type mul(half8 a, half8 b, type c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+  }
+};
+// Row of accumulator register r within a tile (columns run along the lanes).
+template <int T>
+__device__ __forceinline__ int tile_row(int r) {
+  const int lane = threadIdx.x & 63;
+  return T == 32 ? 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3) : 4 * (lane >> 4) + r;
+}
+
+// An operand's run of eight reductions from rows of the reduction: row i of the tile at s.
+template <int T>
+__device__ __forceinline__ half8 run_of_rows(const _Float16* s, int ld, int k) {
+  const int lane = threadIdx.x & 63;
+  return *reinterpret_cast<const half8*>(s + (lane & (T - 1)) * ld + k + 8 * (lane / T));
+}
+// The same from the transposed matrix (its rows are the reductions), by LDS
+// reads that turn 4 x 16 blocks: in each group of 16 lanes, lane l supplies the
+// address of four values of row l / 4 and receives column l of the four rows.
+template <int T>
+__device__ __forceinline__ half8 run_of_columns(const _Float16* s, int ld, int i0, int k) {
+  typedef __fp16 fp16x4 __attribute__((ext_vector_type(4)));
+  typedef __attribute__((address_space(3))) fp16x4* lds_ptr;
+  const int lane = threadIdx.x & 63, l = lane & 15;
+  const int row = k + 8 * (lane / T) + (l >> 2), col = i0 + (T == 32 ? 16 * ((lane >> 4) & 1) : 0) + 4 * (l & 3);
+  const _Float16* p = s + row * ld + col;
+  const fp16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_ptr)p);
+  const fp16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_ptr)(p + 4 * ld));
+  const half4 x = __builtin_bit_cast(half4, a), y = __builtin_bit_cast(half4, b);
+  return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// acc[t] += P Q^T for TILES stacked tiles of P's rows from row i0 and one tile
+// of Q's rows from row j0, over `steps` products from reduction k0.
+// COLS: the planes hold the transposed operands.
+template <int T, int TILES, bool COLS>
+__device__ __forceinline__ void mul_tiles(const _Float16* p, int lp, int plane_p, int i0, const _Float16* q, int lq,
+                                          int plane_q, int j0, int k0, int steps, typename Acc<T>::type (&acc)[TILES]) {
+  constexpr int kStep = T == 32 ? 16 : 32;
+  auto get = [&](const _Float16* s, int ld, int row, int k) {
+    if constexpr (COLS)
+      return run_of_columns<T>(s, ld, row, k);
+    else
+      return run_of_rows<T>(s + row * ld, ld, k);
+  };
 #pragma unroll 2
   for (int s = 0; s < steps; ++s) {
-    const int k = k0 + 16 * s + 8 * h;
-    const half8 qh = *reinterpret_cast<const half8*>(q + i * lq + k);
-    const half8 ql = *reinterpret_cast<const half8*>(q + plane_q + i * lq + k);
+    const int k = k0 + kStep * s;
+    const half8 qh = get(q, lq, j0, k), ql = get(q + plane_q, lq, j0, k);
     half8 ph[TILES], pl[TILES];
 #pragma unroll
     for (int t = 0; t < TILES; ++t) {
-      ph[t] = *reinterpret_cast<const half8*>(p + (32 * t + i) * lp + k);
-      pl[t] = *reinterpret_cast<const half8*>(p + plane_p + (32 * t + i) * lp + k);
+      ph[t] = get(p, lp, i0 + T * t, k);
+      pl[t] = get(p + plane_p, lp, i0 + T * t, k);
     }
 #pragma unroll
-    for (int t = 0; t < TILES; ++t) acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph[t], ql, acc[t], 0, 0, 0);
+    for (int t = 0; t < TILES; ++t) acc[t] = Acc<T>::mul(ph[t], ql, acc[t]);
 #pragma unroll
-    for (int t = 0; t < TILES; ++t) acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(pl[t], qh, acc[t], 0, 0, 0);
+    for (int t = 0; t < TILES; ++t) acc[t] = Acc<T>::mul(pl[t], qh, acc[t]);
 #pragma unroll
-    for (int t = 0; t < TILES; ++t) acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph[t], qh, acc[t], 0, 0, 0);
+    for (int t = 0; t < TILES; ++t) acc[t] = Acc<T>::mul(ph[t], qh, acc[t]);
   }
 }
 
-// The tile (rows i0.., columns j0..) of v * 2^e into planes whose rows are the
+// The tile (rows i0.., columns j0..) of v f into planes whose rows are the
 // tile's columns: four consecutive rows of a column are one 8-byte write.
-__device__ __forceinline__ void put_columns(_Float16* s, int ld, int plane, int i0, int j0, const floatx16& v, float f) {
-  const int lane = threadIdx.x & 63, j = j0 + (lane & 31), h = lane >> 5;
+template <int T>
+__device__ __forceinline__ void put_columns(_Float16* s, int ld, int plane, int i0, int j0,
+                                            const typename Acc<T>::type& v, float f) {
+  typedef float floatx4 __attribute__((ext_vector_type(4)));
+  const int j = j0 + (threadIdx.x & (T - 1));
 #pragma unroll
-  for (int rq = 0; rq < 4; ++rq) {
-    half4 hi, lo;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      _Float16 a, b;
-      split2(v[4 * rq + e] * f, a, b);
-      hi[e] = a;
-      lo[e] = b;
-    }
-    _Float16* at = s + j * ld + i0 + 8 * rq + 4 * h;
+  for (int q = 0; q < Acc<T>::regs / 4; ++q) {
+    const floatx4 x = {v[4 * q] * f, v[4 * q + 1] * f, v[4 * q + 2] * f, v[4 * q + 3] * f};
+    const half4 hi = __builtin_convertvector(x, half4);
+    const half4 lo = __builtin_convertvector(x - __builtin_convertvector(hi, floatx4), half4);
+    _Float16* at = s + j * ld + i0 + tile_row<T>(4 * q);
     *reinterpret_cast<half4*>(at) = hi;
     *reinterpret_cast<half4*>(at + plane) = lo;
-  }
-}
-
-// The same into planes whose rows are the tile's rows.
-__device__ __forceinline__ void put_rows(_Float16* s, int ld, int plane, int i0, int j0, const floatx16& v, float f) {
-  const int lane = threadIdx.x & 63, j = j0 + (lane & 31), h = lane >> 5;
-#pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    _Float16 a, b;
-    split2(v[r] * f, a, b);
-    _Float16* at = s + (i0 + 8 * (r >> 2) + 4 * h + (r & 3)) * ld + j;
-    at[0] = a;
-    at[plane] = b;
   }
 }
 
@@ -473,11 +518,12 @@ __global__ __launch_bounds__(64 * S::NW) void muon_small_kernel(const SmallArgs 
   const SmallArgs& a = *(const SmallArgs*)__builtin_amdgcn_kernarg_segment_ptr();
   __shared__ __align__(16) char smem[S::kBytes];
   __shared__ float s_norm[S::NW];
-  constexpr int RP = S::RP, RT = S::RT, TPW = S::TPW, APW = S::APW, AW = S::AW, KS = S::KS, LX = S::LX, LT = S::LT;
-  constexpr int kXPlane = S::kX, kAPlane = RP * LT;
+  constexpr int RP = S::RP, RT = S::RT, T = S::T, TPW = S::TPW, APW = S::APW, AW = S::AW, KS = S::KS, LT = S::LT, LA = S::LA;
+  constexpr int R = Acc<T>::regs;
+  typedef typename Acc<T>::type acc_t;
   _Float16* sx = reinterpret_cast<_Float16*>(smem);
-  _Float16* sq = sx + 2 * kXPlane;
-  float* sr = reinterpret_cast<float*>(sq + 2 * kAPlane);
+  _Float16* sq = sx + 2 * S::kX;
+  float* sr = reinterpret_cast<float*>(sq + 2 * S::kA);
   int bi = 0;
   while (bi + 1 < a.nblocks && (int64_t)blockIdx.x >= a.block[bi + 1].first) ++bi;
   const SmallBlock& m = a.block[bi];
@@ -485,17 +531,17 @@ __global__ __launch_bounds__(64 * S::NW) void muon_small_kernel(const SmallArgs 
   const bool transposed = m.rows > m.cols;
   const int nr = transposed ? m.cols : m.rows, nc = transposed ? m.rows : m.cols;
   const int si = transposed ? 1 : m.cols, sj = transposed ? m.cols : 1;  // X[i][j] is U at i * si + j * sj
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, lj = lane & 31, lh = lane >> 5;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, lj = lane & (T - 1);
 
-  // X in registers: tile t of the wave covers rows 32 (tile % RT), columns 32 (tile / RT)
-  floatx16 x[TPW];
+  // X in registers: tile t of the wave covers rows T (tile % RT), columns T (tile / RT)
+  acc_t x[TPW];
   float q = 0.f;
 #pragma unroll
   for (int t = 0; t < TPW; ++t) {
-    const int tile = wave * TPW + t, i0 = 32 * (tile % RT) + 4 * lh, j = 32 * (tile / RT) + lj;
+    const int tile = wave * TPW + t, j = T * (tile / RT) + lj;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int i = i0 + 8 * (r >> 2) + (r & 3);
+    for (int r = 0; r < R; ++r) {
+      const int i = T * (tile % RT) + tile_row<T>(r);
       float v = 0.f;
       if (i < nr && j < nc) {
         const int64_t e = base + (int64_t)i * si + (int64_t)j * sj;
@@ -520,58 +566,53 @@ __global__ __launch_bounds__(64 * S::NW) void muon_small_kernel(const SmallArgs 
 #pragma unroll
   for (int t = 0; t < TPW; ++t)
 #pragma unroll
-    for (int r = 0; r < 16; ++r) x[t][r] *= inv;
+    for (int r = 0; r < R; ++r) x[t][r] *= inv;
 
   for (int k = 0; k < a.nsteps; ++k) {
     const MuonStep st = a.step[k];
 #pragma unroll
     for (int t = 0; t < TPW; ++t) {
       const int tile = wave * TPW + t;
-      put_rows(sx, LX, kXPlane, 32 * (tile % RT), 32 * (tile / RT), x[t], pow2(st.ex));
+      put_columns<T>(sx, LT, S::kX, T * (tile % RT), T * (tile / RT), x[t], pow2(st.ex));  // X^T
     }
     __syncthreads();
-    // A = X X^T: KS waves per tile group take a part of the columns each
+    // A = X X^T: KS waves per tile take a part of the columns each
     const int aw = wave % AW, ks = wave / AW;
-    const int ai = 32 * ((aw * APW) % RT), aj = 32 * ((aw * APW) / RT);
-    floatx16 acc[APW];
+    const int ai = T * ((aw * APW) % RT), aj = T * ((aw * APW) / RT);
+    acc_t acc[APW];
 #pragma unroll
     for (int t = 0; t < APW; ++t)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) acc[t][r] = 0.f;
-    mul_tiles<APW>(sx + ai * LX, LX, kXPlane, sx + aj * LX, LX, kXPlane, ks * (S::CP / KS), S::CP / (16 * KS), acc);
+      for (int r = 0; r < R; ++r) acc[t][r] = 0.f;
+    mul_tiles<T, APW, true>(sx, LT, S::kX, ai, sx, LT, S::kX, aj, ks * (S::CP / KS), S::CP / (S::kStep * KS), acc);
     if constexpr (KS > 1) {
       if (ks > 0)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) sr[((ks - 1) * AW + aw) * 1024 + r * 64 + lane] = acc[0][r];
+        for (int r = 0; r < R; ++r) sr[((ks - 1) * AW + aw) * T * T + r * 64 + lane] = acc[0][r];
+      __syncthreads();
     }
-    __syncthreads();
     const float fa = pow2(-2 * st.ex);
     if (ks == 0) {
 #pragma unroll
       for (int t = 0; t < APW; ++t) {
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
+        for (int r = 0; r < R; ++r) {
           if constexpr (KS > 1)
-            for (int w = 0; w < KS - 1; ++w) acc[t][r] += sr[(w * AW + aw) * 1024 + r * 64 + lane];
+            for (int w = 0; w < KS - 1; ++w) acc[t][r] += sr[(w * AW + aw) * T * T + r * 64 + lane];
           acc[t][r] *= fa;
         }
-        put_columns(sq, LT, kAPlane, ai + 32 * t, aj, acc[t], pow2(st.ea));  // A is symmetric
+        put_columns<T>(sq, LA, S::kA, ai + T * t, aj, acc[t], pow2(st.ea));  // A is symmetric
       }
-    }
-#pragma unroll
-    for (int t = 0; t < TPW; ++t) {
-      const int tile = wave * TPW + t;
-      put_columns(sx, LT, kXPlane, 32 * (tile % RT), 32 * (tile / RT), x[t], pow2(st.ex));  // X^T
     }
     __syncthreads();
     // B = b A + c A A, over A
-    floatx16 sqr[APW];
+    acc_t sqr[APW];
     if (ks == 0) {
 #pragma unroll
       for (int t = 0; t < APW; ++t)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) sqr[t][r] = 0.f;
-      mul_tiles<APW>(sq + ai * LT, LT, kAPlane, sq + aj * LT, LT, kAPlane, 0, RP / 16, sqr);
+        for (int r = 0; r < R; ++r) sqr[t][r] = 0.f;
+      mul_tiles<T, APW, false>(sq, LA, S::kA, ai, sq, LA, S::kA, aj, 0, RP / S::kStep, sqr);
     }
     __syncthreads();
     if (ks == 0) {
@@ -579,36 +620,34 @@ __global__ __launch_bounds__(64 * S::NW) void muon_small_kernel(const SmallArgs 
 #pragma unroll
       for (int t = 0; t < APW; ++t) {
 #pragma unroll
-        for (int r = 0; r < 16; ++r) sqr[t][r] = st.b * acc[t][r] + fc * sqr[t][r];
-        put_columns(sq, LT, kAPlane, ai + 32 * t, aj, sqr[t], pow2(st.eb));
+        for (int r = 0; r < R; ++r) sqr[t][r] = st.b * acc[t][r] + fc * sqr[t][r];
+        put_columns<T>(sq, LA, S::kA, ai + T * t, aj, sqr[t], pow2(st.eb));
       }
     }
     __syncthreads();
-    // X <- a X + B X, the wave's own tiles (all in one column of tiles, or single)
+    // X <- a X + B X, the wave's own tiles
     const float fx = pow2(-st.ex - st.eb);
-    if constexpr (RT > 1 || TPW == 1) {
-      floatx16 bx[TPW];
+    acc_t bx[TPW];
 #pragma unroll
-      for (int t = 0; t < TPW; ++t)
+    for (int t = 0; t < TPW; ++t)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) bx[t][r] = 0.f;
+      for (int r = 0; r < R; ++r) bx[t][r] = 0.f;
+    if constexpr (RT % TPW == 0) {  // (all in one column of tiles)
       const int tile = wave * TPW;
-      mul_tiles<TPW>(sq + 32 * (tile % RT) * LT, LT, kAPlane, sx + 32 * (tile / RT) * LT, LT, kXPlane, 0, RP / 16, bx);
-#pragma unroll
-      for (int t = 0; t < TPW; ++t)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) x[t][r] = st.a * x[t][r] + fx * bx[t][r];
+      mul_tiles<T, TPW, false>(sq, LA, S::kA, T * (tile % RT), sx, LT, S::kX, T * (tile / RT), 0, RP / S::kStep, bx);
     } else {
 #pragma unroll
       for (int t = 0; t < TPW; ++t) {
-        floatx16 bx[1];
-#pragma unroll
-        for (int r = 0; r < 16; ++r) bx[0][r] = 0.f;
-        mul_tiles<1>(sq, LT, kAPlane, sx + 32 * (wave * TPW + t) * LT, LT, kXPlane, 0, RP / 16, bx);
-#pragma unroll
-        for (int r = 0; r < 16; ++r) x[t][r] = st.a * x[t][r] + fx * bx[0][r];
+        const int tile = wave * TPW + t;
+        acc_t one[1] = {bx[t]};
+        mul_tiles<T, 1, false>(sq, LA, S::kA, T * (tile % RT), sx, LT, S::kX, T * (tile / RT), 0, RP / S::kStep, one);
+        bx[t] = one[0];
       }
     }
+#pragma unroll
+    for (int t = 0; t < TPW; ++t)
+#pragma unroll
+      for (int r = 0; r < R; ++r) x[t][r] = st.a * x[t][r] + fx * bx[t][r];
     __syncthreads();
   }
 
@@ -616,10 +655,10 @@ __global__ __launch_bounds__(64 * S::NW) void muon_small_kernel(const SmallArgs 
   const float rate = a.u.lr * (m.cols > m.rows ? sqrtf((float)m.cols / (float)m.rows) : 1.f);
 #pragma unroll
   for (int t = 0; t < TPW; ++t) {
-    const int tile = wave * TPW + t, i0 = 32 * (tile % RT) + 4 * lh, j = 32 * (tile / RT) + lj;
+    const int tile = wave * TPW + t, j = T * (tile / RT) + lj;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int i = i0 + 8 * (r >> 2) + (r & 3);
+    for (int r = 0; r < R; ++r) {
+      const int i = T * (tile % RT) + tile_row<T>(r);
       if (i >= nr || j >= nc) continue;
       const int64_t e = base + (int64_t)i * si + (int64_t)j * sj;
       float v = x[t][r];
@@ -669,15 +708,15 @@ hipError_t launch_small_kinds(const MuonPlan& p, const MuonUpdate& u, hipStream_
     std::copy(p.step, p.step + kMaxMuonSteps + 1, k.step);
     hipError_t e = hipSuccess;
     switch (kind) {
-      case kS32x32: e = launch_small<Small<32, 32, 1, 1>>(k, n, s); break;
-      case kS32x64: e = launch_small<Small<32, 64, 2, 1>>(k, n, s); break;
-      case kS32x128: e = launch_small<Small<32, 128, 4, 1>>(k, n, s); break;
-      case kS32x256: e = launch_small<Small<32, 256, 8, 1>>(k, n, s); break;
-      case kS32x512: e = launch_small<Small<32, 512, 8, 2>>(k, n, s); break;
-      case kS64x64: e = launch_small<Small<64, 64, 4, 1>>(k, n, s); break;
-      case kS64x128: e = launch_small<Small<64, 128, 8, 1>>(k, n, s); break;
-      case kS64x256: e = launch_small<Small<64, 256, 8, 2>>(k, n, s); break;
-      default: e = launch_small<Small<128, 128, 8, 2>>(k, n, s); break;
+      case kS32x32: e = launch_small<Small<32, 32, 16, 4, 1>>(k, n, s); break;
+      case kS32x64: e = launch_small<Small<32, 64, 16, 8, 1>>(k, n, s); break;
+      case kS32x128: e = launch_small<Small<32, 128, 16, 16, 1>>(k, n, s); break;
+      case kS32x256: e = launch_small<Small<32, 256, 32, 8, 1>>(k, n, s); break;
+      case kS32x512: e = launch_small<Small<32, 512, 32, 8, 2>>(k, n, s); break;
+      case kS64x64: e = launch_small<Small<64, 64, 16, 16, 1>>(k, n, s); break;
+      case kS64x128: e = launch_small<Small<64, 128, 32, 8, 1>>(k, n, s); break;
+      case kS64x256: e = launch_small<Small<64, 256, 32, 8, 2>>(k, n, s); break;
+      default: e = launch_small<Small<128, 128, 32, 16, 1>>(k, n, s); break;
     }
     if (e != hipSuccess) return e;
   }
