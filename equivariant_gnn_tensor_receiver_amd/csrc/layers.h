@@ -17,7 +17,7 @@ struct NormIrrep {
   int32_t scalar;        // 1: 0e (mean and bias)
   int32_t off;           // feature offset of the block within a node
   int32_t w_off, b_off;  // offsets in weight and bias
-  int32_t vec, lanes;    // wide accesses; lanes per (node, irrep) of narrow blocks
+  int32_t lanes;         // lanes per (node, irrep) of narrow blocks
   int32_t first_block, blocks;  // the irrep's blocks of the launch
   int64_t part_off;      // backward: the irrep's partial sums, [blocks][mul] (scalar irreps: [blocks][2][mul])
 };

@@ -476,7 +476,7 @@ __device__ __forceinline__ void mul_tiles(const _Float16* p, int lp, int plane_p
     else
       return run_of_rows<T>(s + row * ld, ld, k);
   };
-#pragma unroll 2
+#pragma unroll  // (176 x 128 x 128: 51.8 us by two, 47.7 in full)
   for (int s = 0; s < steps; ++s) {
     const int k = k0 + kStep * s;
     const half8 qh = get(q, lq, j0, k), ql = get(q + plane_q, lq, j0, k);
