@@ -32,14 +32,16 @@ namespace {
 
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kThreads = 256;
 
-// Eight fp32 values as three planes of packed bf16 (exact: truncation leaves
-// 8 bits per piece); bf16 values are one plane already.
-__device__ __forceinline__ void split3(const float (&v)[8], u32x4 (&p)[3]) {
+// N fp32 values as three planes of packed bf16 (exact: truncation leaves 8 bits
+// per piece); bf16 values are one plane already.
+template <int N, typename V>
+__device__ __forceinline__ void split3(const float (&v)[N], V (&p)[3]) {
 #pragma unroll
-  for (int t = 0; t < 4; ++t) {
+  for (int t = 0; t < N / 2; ++t) {
     const uint32_t x0 = __float_as_uint(v[2 * t]), x1 = __float_as_uint(v[2 * t + 1]);
     const float r0 = v[2 * t] - __uint_as_float(x0 & 0xffff0000u);
     const float r1 = v[2 * t + 1] - __uint_as_float(x1 & 0xffff0000u);
@@ -107,9 +109,7 @@ __device__ __forceinline__ int64_t div_rows(int64_t r, int n) {
 
 // Wide accesses at any element's address (the hardware needs no more alignment).
 typedef float floatx4_any __attribute__((ext_vector_type(4), aligned(4)));
-typedef float floatx2_any __attribute__((ext_vector_type(2), aligned(4)));
 typedef unsigned int u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
-typedef unsigned int u32_any __attribute__((aligned(2)));
 
 // Eight values along the reduction of one row: p[k..k+8), as loaded.  Runs past
 // `len` read on into the memory behind the row (a run wholly past it reads the
@@ -156,27 +156,6 @@ __device__ __forceinline__ void mask_run8(u32x4& v, int left) {
     v[j] = 2 * j + 1 < left ? v[j] : 2 * j < left ? v[j] & 0xffffu : 0u;
 }
 
-// Two neighbouring columns c, c + 1 of one row; columns past `cols` take a
-// value from inside the row (they are never stored).  WIDE: see wide_pairs.
-template <bool WIDE>
-__device__ __forceinline__ void load_pair(const float* p, int c, int cols, float& a, float& b) {
-  if constexpr (WIDE) {
-    const floatx2_any x = *reinterpret_cast<const floatx2_any*>(p + min(c, cols - 2));
-    a = x.x;
-    b = x.y;
-  } else {
-    a = p[min(c, cols - 1)];
-    b = p[min(c + 1, cols - 1)];
-  }
-}
-template <bool WIDE>
-__device__ __forceinline__ uint32_t load_pair(const uint16_t* p, int c, int cols) {
-  if constexpr (WIDE) return *reinterpret_cast<const u32_any*>(p + min(c, cols - 2));
-  return (uint32_t)p[min(c, cols - 1)] | ((uint32_t)p[min(c + 1, cols - 1)] << 16);
-}
-// Whether the columns [c0, c0 + width) of rows of `cols` can be loaded in pairs: none straddles the row's end.
-__device__ __forceinline__ bool wide_pairs(int c0, int width, int cols) { return cols % 2 == 0 || c0 + width < cols; }
-
 template <typename T>
 struct Planes;
 template <>
@@ -188,21 +167,20 @@ struct Planes<uint16_t> {
   static constexpr int count = 1;
 };
 
-// Eight values of one row to its place in every plane.
-template <int LD, int ROWS>
-__device__ __forceinline__ void put_run8(uint16_t (*s)[ROWS][LD], int row, int k, const float (&v)[8]) {
-  u32x4 p[3];
-  split3(v, p);
-#pragma unroll
-  for (int i = 0; i < 3; ++i) *reinterpret_cast<u32x4*>(&s[i][row][k]) = p[i];
-}
-template <int LD, int ROWS>
-__device__ __forceinline__ void put_run8(uint16_t (*s)[ROWS][LD], int row, int k, const u32x4& v) {
-  *reinterpret_cast<u32x4*>(&s[0][row][k]) = v;
-}
+// Operands in LDS, one plane after the other, in the layout they come in:
+//   by rows:    [row][reduction], for operands whose reduction is contiguous in
+//               memory; rows padded by 16 bytes, so that 16-byte reads of 16
+//               rows touch every bank once;
+//   by columns: [reduction][row], for operands whose rows are contiguous; they
+//               are turned by the LDS reads (run_of_columns), and padded so
+//               that the four rows of 32 bytes of such a read do not meet.
+template <bool COLS, int ROWS, int KC>
+struct Layout {
+  static constexpr int LD = !COLS ? KC + 8 : ROWS == 128 ? 144 : ROWS == 64 ? 72 : 48;
+  static constexpr int plane = (COLS ? KC : ROWS) * LD;
+};
 
 // The values one thread loads of an operand for one chunk.
-// RunPart: rows of the operand, eight reductions each, contiguous in memory.
 template <typename T>
 struct Raw8;
 template <>
@@ -214,8 +192,11 @@ struct Raw8<uint16_t> {
   u32x4 v;
 };
 
+// RunPart: operands by rows; eight reductions of a row at a time.
 template <typename T, int ROWS, int KC>
 struct RunPart {
+  using L = Layout<false, ROWS, KC>;
+  static constexpr bool kCols = false;
   static constexpr int kPer = KC / 8;                        // threads per row
   static constexpr int kPasses = (ROWS * kPer + kThreads - 1) / kThreads;
   static constexpr bool kWhole = ROWS * kPer >= kThreads;    // else the first threads alone
@@ -223,86 +204,115 @@ struct RunPart {
   static __device__ __forceinline__ bool mine() { return kWhole || (int)threadIdx.x < ROWS * kPer; }
   static __device__ __forceinline__ int row(int p) { return p * (kThreads / kPer) + (int)threadIdx.x / kPer; }
   static __device__ __forceinline__ int k() { return ((int)threadIdx.x % kPer) * 8; }
-  template <int LD>
-  __device__ __forceinline__ void put(uint16_t (*s)[ROWS][LD], int left) {
+  __device__ __forceinline__ void put(uint16_t* s, int left) {
     if (!mine()) return;
 #pragma unroll
     for (int p = 0; p < kPasses; ++p) {
       if (left < KC) mask_run8(raw[p].v, left - k());  // `left` is uniform
-      put_run8<LD, ROWS>(s, row(p), k(), raw[p].v);
-    }
-  }
-};
-
-// PairPart: rows of the operand are columns of the memory; a thread takes two
-// neighbouring columns and eight reductions, and turns them in registers.
-template <typename T, int ROWS, int KC>
-struct PairPart {
-  static constexpr int kPer = ROWS / 2;  // threads per reduction group
-  static constexpr int kPasses = (kPer * (KC / 8) + kThreads - 1) / kThreads;
-  static constexpr bool kWhole = kPer * (KC / 8) >= kThreads;
-  float f[sizeof(T) == 4 ? kPasses : 1][2][8];
-  uint32_t h[sizeof(T) == 2 ? kPasses : 1][8];
-  static __device__ __forceinline__ bool mine() { return kWhole || (int)threadIdx.x < kPer * (KC / 8); }
-  static __device__ __forceinline__ int col() { return 2 * ((int)threadIdx.x % kPer); }
-  // (64 or more threads per group: the group is uniform over the wave, and said so)
-  static __device__ __forceinline__ int k(int p) {
-    const int g = (int)threadIdx.x / kPer;
-    return (p * (kThreads / kPer) + (kPer >= 64 ? __builtin_amdgcn_readfirstlane(g) : g)) * 8;
-  }
-  static constexpr bool kUniform = kPer >= 64;
-  template <bool WIDE>
-  __device__ __forceinline__ void load(int p, int j, const float* at, int c, int cols) {
-    load_pair<WIDE>(at, c, cols, f[p][0][j], f[p][1][j]);
-  }
-  template <bool WIDE>
-  __device__ __forceinline__ void load(int p, int j, const uint16_t* at, int c, int cols) {
-    h[p][j] = load_pair<WIDE>(at, c, cols);
-  }
-  template <int LD>
-  __device__ __forceinline__ void put(uint16_t (*s)[ROWS][LD], int left) {
-    if (!mine()) return;
-#pragma unroll
-    for (int p = 0; p < kPasses; ++p) {
+      uint16_t* at = s + row(p) * L::LD + k();
       if constexpr (sizeof(T) == 4) {
+        u32x4 pl[3];
+        split3(raw[p].v, pl);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          if (left < KC) mask_run8(f[p][e], left - k(p));
-          put_run8<LD, ROWS>(s, col() + e, k(p), f[p][e]);
-        }
+        for (int i = 0; i < 3; ++i) *reinterpret_cast<u32x4*>(at + i * L::plane) = pl[i];
       } else {
-        u32x4 v[2];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[0][j] = __builtin_amdgcn_perm(h[p][2 * j + 1], h[p][2 * j], 0x05040100);
-          v[1][j] = __builtin_amdgcn_perm(h[p][2 * j + 1], h[p][2 * j], 0x07060302);
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          if (left < KC) mask_run8(v[e], left - k(p));
-          put_run8<LD, ROWS>(s, col() + e, k(p), v[e]);
-        }
+        *reinterpret_cast<u32x4*>(at) = raw[p].v;
       }
     }
   }
 };
 
+// ColPart: operands by columns; 16 bytes of neighbouring columns of one reduction at a time.
+template <typename T, int ROWS, int KC>
+struct ColPart {
+  using L = Layout<true, ROWS, KC>;
+  static constexpr bool kCols = true;
+  static constexpr int kUnit = 16 / sizeof(T);
+  static constexpr int kPer = ROWS / kUnit;          // threads per reduction
+  static constexpr int kStep = kThreads / kPer;      // reductions per pass
+  static constexpr bool kWhole = KC >= kStep;        // else the first threads alone
+  static constexpr int kPasses = kWhole ? KC / kStep : 1;
+  static_assert(!kWhole || KC % kStep == 0, "whole passes");
+  u32x4 raw[kPasses];
+  static __device__ __forceinline__ bool mine() { return kWhole || (int)threadIdx.x < KC * kPer; }
+  static __device__ __forceinline__ int col() { return ((int)threadIdx.x % kPer) * kUnit; }
+  static __device__ __forceinline__ int k(int p) { return p * kStep + (int)threadIdx.x / kPer; }
+  // The columns c.. of the row at p of `cols` columns: those past it are never
+  // stored and take what follows in memory (or the row's start).
+  template <bool WIDE>
+  __device__ __forceinline__ void load(int pass, const T* p, int c, int cols, const T* end) {
+    const T* q = p + (c < cols ? c : 0);
+    if (WIDE || q + kUnit <= end) {
+      raw[pass] = *reinterpret_cast<const u32x4_any*>(q);
+    } else {
+      u32x4 v = {0, 0, 0, 0};
+#pragma unroll
+      for (int e = 0; e < kUnit; ++e) {
+        const T x = p[min(c + e, cols - 1)];
+        if constexpr (sizeof(T) == 4)
+          v[e] = __builtin_bit_cast(uint32_t, x);
+        else
+          v[e >> 1] |= (uint32_t)x << (16 * (e & 1));
+      }
+      raw[pass] = v;
+    }
+  }
+  __device__ __forceinline__ void put(uint16_t* s, int left) {
+    if (!mine()) return;
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+      u32x4 v = raw[p];
+      if (left < KC && k(p) >= left) v = (u32x4){0, 0, 0, 0};
+      uint16_t* at = s + k(p) * L::LD + col();
+      if constexpr (sizeof(T) == 4) {
+        float f[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = __uint_as_float(v[e]);
+        u32x2 pl[3];
+        split3(f, pl);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) *reinterpret_cast<u32x2*>(at + i * L::plane) = pl[i];
+      } else {
+        *reinterpret_cast<u32x4*>(at) = v;
+      }
+    }
+  }
+};
+
+// A lane's eight reductions k.. of its row of the 32-row tile at `row`.
+template <typename L, bool COLS>
+__device__ __forceinline__ bf16x8 fragment(const uint16_t* s, int row, int k) {
+  const int lane = threadIdx.x & 63, h = lane >> 5;
+  if constexpr (!COLS) {
+    return *reinterpret_cast<const bf16x8*>(s + (row + (lane & 31)) * L::LD + k + 8 * h);
+  } else {
+    // each group of 16 lanes turns 4 reductions x 16 rows: lane l supplies the address of four
+    // rows of reduction l / 4 and receives row l of the four
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) s16x4* lds_ptr;
+    const int l = lane & 15;
+    const uint16_t* p = s + (k + 8 * h + (l >> 2)) * L::LD + row + 16 * ((lane >> 4) & 1) + 4 * (l & 3);
+    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)p);
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + 4 * L::LD));
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+  }
+}
+
 // acc += A B over the k16 steps of this wave from the staged planes.
-template <int PA, int PB, int MT, int NT, int BM, int BN, int LD>
-__device__ __forceinline__ void multiply(const uint16_t (*sa)[BM][LD], const uint16_t (*sb)[BN][LD], int m0, int n0,
-                                         int k0, int steps, floatx16 (&acc)[MT][NT]) {
-  const int lane = threadIdx.x & 63, i = lane & 31, h = lane >> 5;
+template <int PA, int PB, int MT, int NT, typename A, typename B>
+__device__ __forceinline__ void multiply(const uint16_t* sa, const uint16_t* sb, int m0, int n0, int k0, int steps,
+                                         floatx16 (&acc)[MT][NT]) {
   for (int st = 0; st < steps; ++st) {
-    const int k = k0 + 16 * st + 8 * h;
+    const int k = k0 + 16 * st;
     bf16x8 fa[PA][MT], fb[PB][NT];
 #pragma unroll
     for (int p = 0; p < PA; ++p)
 #pragma unroll
-      for (int t = 0; t < MT; ++t) fa[p][t] = *reinterpret_cast<const bf16x8*>(&sa[p][m0 + 32 * t + i][k]);
+      for (int t = 0; t < MT; ++t) fa[p][t] = fragment<typename A::L, A::kCols>(sa + p * A::L::plane, m0 + 32 * t, k);
 #pragma unroll
     for (int p = 0; p < PB; ++p)
 #pragma unroll
-      for (int t = 0; t < NT; ++t) fb[p][t] = *reinterpret_cast<const bf16x8*>(&sb[p][n0 + 32 * t + i][k]);
+      for (int t = 0; t < NT; ++t) fb[p][t] = fragment<typename B::L, B::kCols>(sb + p * B::L::plane, n0 + 32 * t, k);
 #pragma unroll
     for (int rank = 2; rank >= 0; --rank)
 #pragma unroll
@@ -328,13 +338,12 @@ __device__ __forceinline__ void store_out(uint16_t* p, int64_t i, float v) {
 
 // Tile shapes.  A block of four waves computes BM x BN; with KS = 1 its waves
 // take WM x WN each, with KS = 4 every wave takes a quarter of the reduction of
-// the whole tile and the sums are added in order through LDS.  LDS rows are
-// padded by 16 bytes, so 16-byte reads of 16 rows touch every bank once.
+// the whole tile and the sums are added in order through LDS.
 // AHEAD chunks of loads are in flight (more than one pays where few blocks wait
 // for memory: four rows over 64 experts took 16.3 us with one, see RowsShape).
 template <int BM_, int BN_, int WM_, int WN_, int KS_, int KC_, int AHEAD_ = 1>
 struct Shape {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, KS = KS_, KC = KC_, LD = KC_ + 8, kAhead = AHEAD_;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, KS = KS_, KC = KC_, kAhead = AHEAD_;
   static constexpr int MT = WM / 32, NT = WN / 32;
   static_assert((BM / WM) * (BN / WN) * KS == kThreads / 64, "four waves");
 };
@@ -343,19 +352,26 @@ constexpr int max_int(int a, int b) { return a > b ? a : b; }
 
 // LDS bytes: the operands' planes (later the partial sums of KS > 1) and the
 // tables of row addresses.
-template <typename S, int PA, int PB>
+template <typename S, int PA, int PB, typename A, typename B>
 constexpr int plane_bytes() {
-  return max_int((PA * S::BM + PB * S::BN) * S::LD * 2, (S::KS - 1) * S::BM * S::BN * 4);
+  return max_int((PA * A::L::plane + PB * B::L::plane) * 2, (S::KS - 1) * S::BM * S::BN * 4);
 }
 constexpr int kRowTable = 256;  // weight gradient: rows of a slot whose addresses are in LDS at a time
-template <typename S, int PA, int PB>
-constexpr int rows_lds() {
-  return plane_bytes<S, PA, PB>() + 2 * S::BM * 4;
-}
-template <typename S, int PA>
-constexpr int gw_lds() {
-  return plane_bytes<S, PA, 3>() + 2 * kRowTable * 8;
-}
+// The operands' parts: x or gy by rows, W by rows or columns; both by columns in the weight gradient.
+template <typename S, typename TI, typename TW, bool WT>
+struct RowsParts {
+  using A = RunPart<TI, S::BM, S::KC>;
+  using B = std::conditional_t<WT, RunPart<TW, S::BN, S::KC>, ColPart<TW, S::BN, S::KC>>;
+  static constexpr int planes = plane_bytes<S, Planes<TI>::count, Planes<TW>::count, A, B>();
+  static constexpr int lds = planes + 2 * S::BM * 4;
+};
+template <typename S, typename TX>
+struct GwParts {
+  using A = ColPart<TX, S::BM, S::KC>;
+  using B = ColPart<float, S::BN, S::KC>;
+  static constexpr int planes = plane_bytes<S, Planes<TX>::count, 3, A, B>();
+  static constexpr int lds = planes + 2 * kRowTable * 8;
+};
 
 // Adds the waves' sums of KS > 1 in order; the result is wave 0's.
 template <typename S>
@@ -377,11 +393,14 @@ __device__ __forceinline__ void join_waves(floatx16 (&acc)[S::MT][S::NT], char* 
 
 template <typename S, typename TI, typename TW, typename TO, bool WT>
 __device__ __forceinline__ void lin_rows(const LinRowsArgs& a, int64_t block, char* smem) {
-  constexpr int PA = Planes<TI>::count, PB = Planes<TW>::count, BM = S::BM, BN = S::BN, KC = S::KC, LD = S::LD;
-  int32_t* s_node = reinterpret_cast<int32_t*>(smem + plane_bytes<S, PA, PB>());
+  using Parts = RowsParts<S, TI, TW, WT>;
+  using PartA = typename Parts::A;
+  using PartB = typename Parts::B;
+  constexpr int PA = Planes<TI>::count, PB = Planes<TW>::count, BM = S::BM, BN = S::BN, KC = S::KC;
+  int32_t* s_node = reinterpret_cast<int32_t*>(smem + Parts::planes);
   int32_t* s_m = s_node + BM;
-  uint16_t(*sa)[BM][LD] = reinterpret_cast<uint16_t(*)[BM][LD]>(smem);
-  uint16_t(*sb)[BN][LD] = reinterpret_cast<uint16_t(*)[BN][LD]>(smem + PA * BM * LD * 2);
+  uint16_t* sa = reinterpret_cast<uint16_t*>(smem);
+  uint16_t* sb = sa + PA * PartA::L::plane;
   // consecutive tiles (the column tiles of one row tile, then its group's next
   // rows) run on one XCD and share its L2
   const int64_t tile = xcd_item(block, (a.tiles + 7) / 8 * 8);
@@ -416,8 +435,6 @@ __device__ __forceinline__ void lin_rows(const LinRowsArgs& a, int64_t block, ch
   const TI* in_end = in + a.N * a.F_in;
   const TW* w_end = static_cast<const TW*>(a.W) + a.G * a.w_per_group;
 
-  using PartA = RunPart<TI, BM, KC>;
-  using PartB = std::conditional_t<WT, RunPart<TW, BN, KC>, PairPart<TW, BN, KC>>;
   constexpr int kAhead = S::kAhead;
   const TI* row_ptr[PartA::kPasses];
   int row_m[PartA::kPasses];
@@ -427,9 +444,11 @@ __device__ __forceinline__ void lin_rows(const LinRowsArgs& a, int64_t block, ch
     const LinSeg& G = a.seg[J.seg0 + i];
     const bool tail = G.len % 8 != 0;
     odd = odd || tail;
-    if constexpr (WT) near_end = near_end || (tail && Wg + G.woff + (int64_t)min(n0 + BN, J.cols) * G.len + 8 > w_end);
+    if constexpr (WT)
+      near_end = near_end || (tail && Wg + G.woff + (int64_t)min(n0 + BN, J.cols) * G.len + 8 > w_end);
+    else
+      near_end = near_end || (J.cols % 8 != 0 && n0 + BN > J.cols - 8 && Wg + G.woff + (int64_t)G.len * J.cols + 8 > w_end);
   }
-  if constexpr (!WT) near_end = !wide_pairs(n0, BN, J.cols);
 #pragma unroll
   for (int p = 0; p < PartA::kPasses; ++p) {
     const int m = s_m[PartA::row(p) % BM];
@@ -456,19 +475,18 @@ __device__ __forceinline__ void lin_rows(const LinRowsArgs& a, int64_t block, ch
       for (int p = 0; p < PartA::kPasses; ++p)
         if (PartA::mine())
           load_run8<WIDE>(row_ptr[p] + G.off + row_m[p] * G.len, k0 + PartA::k(), G.len, in_end, pa[d].raw[p].v);
-      if (PartB::mine()) {
-        if constexpr (WT) {  // B(k, c') = W[c'][k]
+      if constexpr (WT) {  // B(k, c') = W[c'][k]
+        if (PartB::mine())
 #pragma unroll
           for (int p = 0; p < PartB::kPasses; ++p)
-            load_run8<WIDE>(Wg + G.woff + (int64_t)min(n0 + PartB::row(p), J.cols - 1) * G.len, k0 + PartB::k(), G.len, w_end,
-                            pb[d].raw[p].v);
-        } else {  // B(k, c') = W[k][c']
+            load_run8<WIDE>(Wg + G.woff + (int64_t)min(n0 + PartB::row(p), J.cols - 1) * G.len, k0 + PartB::k(), G.len,
+                            w_end, pb[d].raw[p].v);
+      } else {  // B(k, c') = W[k][c']
+        if (PartB::mine())
 #pragma unroll
           for (int p = 0; p < PartB::kPasses; ++p)
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              pb[d].template load<WIDE>(p, j, Wg + G.woff + (int64_t)min(k0 + PartB::k(p) + j, G.len - 1) * J.cols, n0 + PartB::col(), J.cols);
-        }
+            pb[d].template load<WIDE>(p, Wg + G.woff + (int64_t)min(k0 + PartB::k(p), G.len - 1) * J.cols,
+                                    n0 + PartB::col(), J.cols, w_end);
       }
     };
 #pragma unroll
@@ -478,8 +496,8 @@ __device__ __forceinline__ void lin_rows(const LinRowsArgs& a, int64_t block, ch
       for (int d = 0; d < kAhead; ++d) {
         if (si >= J.nseg) break;
         const int left = a.seg[J.seg0 + si].len - k0;
-        pa[d].template put<LD>(sa, left);
-        pb[d].template put<LD>(sb, left);
+        pa[d].put(sa, left);
+        pb[d].put(sb, left);
         __syncthreads();
         k0 += KC;
         if (left <= KC) {
@@ -490,11 +508,11 @@ __device__ __forceinline__ void lin_rows(const LinRowsArgs& a, int64_t block, ch
         __builtin_amdgcn_sched_barrier(0);  // the loads stay ahead of the products
         if constexpr (S::KS > 1) {
           const int kw = wave * (KC / S::KS);  // a wave without reductions left skips its products
-          if (kw < left) multiply<PA, PB, S::MT, S::NT, BM, BN, LD>(sa, sb, 0, 0, kw, KC / (16 * S::KS), acc);
+          if (kw < left) multiply<PA, PB, S::MT, S::NT, PartA, PartB>(sa, sb, 0, 0, kw, KC / (16 * S::KS), acc);
         } else {
           constexpr int kCols = BN / S::WN;
-          multiply<PA, PB, S::MT, S::NT, BM, BN, LD>(sa, sb, (wave / kCols) * S::WM, (wave % kCols) * S::WN, 0, KC / 16,
-                                                     acc);
+          multiply<PA, PB, S::MT, S::NT, PartA, PartB>(sa, sb, (wave / kCols) * S::WM, (wave % kCols) * S::WN, 0, KC / 16,
+                                                       acc);
         }
         __syncthreads();
       }
@@ -527,11 +545,14 @@ __device__ __forceinline__ void lin_rows(const LinRowsArgs& a, int64_t block, ch
 // lin_gw_reduce_kernel adds in order.
 template <typename S, typename TX>
 __device__ __forceinline__ void lin_gw(const LinGwArgs& a, int64_t tile, char* smem) {
-  constexpr int PA = Planes<TX>::count, PB = 3, BM = S::BM, BN = S::BN, KC = S::KC, LD = S::LD;
-  int64_t* s_x = reinterpret_cast<int64_t*>(smem + plane_bytes<S, PA, PB>());
+  using Parts = GwParts<S, TX>;
+  using PartA = typename Parts::A;
+  using PartB = typename Parts::B;
+  constexpr int PA = Planes<TX>::count, PB = 3, BM = S::BM, BN = S::BN, KC = S::KC;
+  int64_t* s_x = reinterpret_cast<int64_t*>(smem + Parts::planes);
   int64_t* s_y = s_x + kRowTable;
-  uint16_t(*sa)[BM][LD] = reinterpret_cast<uint16_t(*)[BM][LD]>(smem);
-  uint16_t(*sb)[BN][LD] = reinterpret_cast<uint16_t(*)[BN][LD]>(smem + PA * BM * LD * 2);
+  uint16_t* sa = reinterpret_cast<uint16_t*>(smem);
+  uint16_t* sb = sa + PA * PartA::L::plane;
   // every slot's tiles are shared out evenly over the XCDs (groups differ in
   // size, so whole slots per XCD would leave most of them waiting), each
   // XCD taking a run of them: the tiles of one or two column tiles of gy
@@ -555,16 +576,16 @@ __device__ __forceinline__ void lin_gw(const LinGwArgs& a, int64_t tile, char* s
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
   const TX* x = static_cast<const TX*>(a.x) + J.xoff;
   const float* gy = a.gy + J.yoff;
-  using PartA = PairPart<TX, BM, KC>;
-  using PartB = PairPart<float, BN, KC>;
+  const TX* x_end = static_cast<const TX*>(a.x) + a.N * a.F_in;
+  const float* y_end = a.gy + a.N * a.F_out;
   constexpr int kAhead = S::kAhead;
-  // a row's offset from the table, moved to scalar registers where the wave reads one row
-  auto row_at = [&](const int64_t* table, int i, auto uniform) -> int64_t {
-    const int64_t v = table[i];
-    if constexpr (!decltype(uniform)::value) return v;
-    return (int64_t)(((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32) |
-                     (uint32_t)__builtin_amdgcn_readfirstlane((int)v));
-  };
+  // reads past a row could leave the tensors: multiplicities that are not a multiple of a unit and the
+  // last nodes (a group's nodes ascend, so the slot's last row tells)
+  bool near_end = false;
+  if (J.mi % PartA::kUnit != 0 || J.mo % PartB::kUnit != 0) {
+    const int64_t p = div_rows(s.row0 + rows - 1, J.n), left = a.N - 1 - (a.order ? a.order[s.node0 + p] : p);
+    near_end = left * min(a.F_in, a.F_out) < 8;
+  }
   auto main_loop = [&](auto wide) {
     constexpr bool WIDE = decltype(wide)::value;
     PartA pa[kAhead];
@@ -587,17 +608,11 @@ __device__ __forceinline__ void lin_gw(const LinGwArgs& a, int64_t tile, char* s
       if (PartA::mine())
 #pragma unroll
         for (int p = 0; p < PartA::kPasses; ++p)
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            pa[d].template load<WIDE>(p, j, x + row_at(s_x, t0 + PartA::k(p) + j, std::bool_constant<PartA::kUniform>{}), i0 + PartA::col(),
-                    J.mi);
+          pa[d].template load<WIDE>(p, x + s_x[t0 + PartA::k(p)], i0 + PartA::col(), J.mi, x_end);
       if (PartB::mine())
 #pragma unroll
         for (int p = 0; p < PartB::kPasses; ++p)
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            pb[d].template load<WIDE>(p, j, gy + row_at(s_y, t0 + PartB::k(p) + j, std::bool_constant<PartB::kUniform>{}), o0 + PartB::col(),
-                    J.mo);
+          pb[d].template load<WIDE>(p, gy + s_y[t0 + PartB::k(p)], o0 + PartB::col(), J.mo, y_end);
     };
 #pragma unroll
     for (int d = 0; d < kAhead; ++d) load(d, d * KC);
@@ -606,27 +621,27 @@ __device__ __forceinline__ void lin_gw(const LinGwArgs& a, int64_t tile, char* s
       for (int d = 0; d < kAhead; ++d) {
         const int r0 = r + d * KC, left = rows - r0;
         if (left <= 0) break;
-        pa[d].template put<LD>(sa, left);
-        pb[d].template put<LD>(sb, left);
+        pa[d].put(sa, left);
+        pb[d].put(sb, left);
         __syncthreads();
         load(d, r0 + kAhead * KC);
         __builtin_amdgcn_sched_barrier(0);  // the loads stay ahead of the products
         if constexpr (S::KS > 1) {
           const int kw = wave * (KC / S::KS);
-          if (kw < left) multiply<PA, PB, S::MT, S::NT, BM, BN, LD>(sa, sb, 0, 0, kw, KC / (16 * S::KS), acc);
+          if (kw < left) multiply<PA, PB, S::MT, S::NT, PartA, PartB>(sa, sb, 0, 0, kw, KC / (16 * S::KS), acc);
         } else {
           constexpr int kCols = BN / S::WN;
-          multiply<PA, PB, S::MT, S::NT, BM, BN, LD>(sa, sb, (wave / kCols) * S::WM, (wave % kCols) * S::WN, 0, KC / 16,
-                                                     acc);
+          multiply<PA, PB, S::MT, S::NT, PartA, PartB>(sa, sb, (wave / kCols) * S::WM, (wave % kCols) * S::WN, 0, KC / 16,
+                                                       acc);
         }
         __syncthreads();
       }
     }
   };
-  if (wide_pairs(i0, BM, J.mi) && wide_pairs(o0, BN, J.mo))
-    main_loop(std::true_type{});
-  else
+  if (near_end)
     main_loop(std::false_type{});
+  else
+    main_loop(std::true_type{});
   join_waves<S>(acc, smem);
   if (S::KS > 1 && wave > 0) return;
   constexpr int kCols = S::KS > 1 ? 1 : BN / S::WN;
@@ -648,16 +663,17 @@ __device__ __forceinline__ void lin_gw(const LinGwArgs& a, int64_t tile, char* s
 
 template <typename S, typename TI, typename TW, typename TO, bool WT>
 __global__ __launch_bounds__(kThreads, 2) void lin_rows_kernel(const LinRowsArgs /*args*/) {
-  __shared__ __align__(16) char smem[rows_lds<S, Planes<TI>::count, Planes<TW>::count>()];
+  __shared__ __align__(16) char smem[RowsParts<S, TI, TW, WT>::lds];
   lin_rows<S, TI, TW, TO, WT>(*(const LinRowsArgs*)__builtin_amdgcn_kernarg_segment_ptr(), blockIdx.x, smem);
 }
 
 // Both gradients in one launch: the weight gradient's tiles, then the input
 // gradient's.  They read the same gy and wait for memory at different times.
+// (bf16 x and W: three waves per SIMD fit, two registers short of it without the bound)
 template <typename S, typename SG, typename TX, typename TW>
-__global__ __launch_bounds__(kThreads, 2) void lin_backward_kernel(const LinBackwardArgs /*args*/) {
+__global__ __launch_bounds__(kThreads, Planes<TX>::count + Planes<TW>::count == 2 ? 3 : 2) void lin_backward_kernel(const LinBackwardArgs /*args*/) {
   const LinBackwardArgs& a = *(const LinBackwardArgs*)__builtin_amdgcn_kernarg_segment_ptr();
-  __shared__ __align__(16) char smem[max_int(rows_lds<S, 3, Planes<TW>::count>(), gw_lds<SG, Planes<TX>::count>())];
+  __shared__ __align__(16) char smem[max_int(RowsParts<S, float, TW, true>::lds, GwParts<SG, TX>::lds)];
   if ((int64_t)blockIdx.x < a.rows_first) {
     if ((int64_t)blockIdx.x < a.gw.tiles) lin_gw<SG, TX>(a.gw, blockIdx.x, smem);
   } else {
@@ -828,7 +844,7 @@ struct RowsShape {
 };
 template <bool ONE>
 struct RowsShape<0, ONE> {
-  using type = Shape<32, 32, 32, 32, 4, 128, ONE ? 4 : 2>;
+  using type = Shape<32, 32, 32, 32, 4, ONE ? 256 : 128, ONE ? 4 : 2>;
 };
 
 template <int BN, typename TI, typename TW, typename TO>
