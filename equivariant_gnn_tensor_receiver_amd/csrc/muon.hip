@@ -392,7 +392,7 @@ struct SmallArgs {
   MuonUpdate u;
   int32_t update, nsteps, nblocks;
   float eps;
-  MuonStep step[kMaxMuonSteps + 1];
+  MuonStep step[kMaxMuonSteps];
   SmallBlock block[kMaxMuonBlocks];
 };
 
@@ -691,21 +691,26 @@ hipError_t launch_small(const SmallArgs& k, int64_t matrices, hipStream_t s) {
 }
 
 hipError_t launch_small_kinds(const MuonPlan& p, const MuonUpdate& u, hipStream_t s) {
+  uint32_t kinds = 0;
+  for (int i = 0; i < p.nblocks; ++i)
+    if (p.block[i].count > 0 && small_kind(p.block[i]) >= 0) kinds |= 1u << small_kind(p.block[i]);
+  if (kinds == 0) return hipSuccess;
+  SmallArgs k;
+  k.u = u;
+  k.update = u.W != nullptr;
+  k.nsteps = p.nsteps;
+  k.eps = p.eps;
+  std::copy(p.step, p.step + p.nsteps, k.step);
   for (int kind = 0; kind < kSmallKinds; ++kind) {
-    SmallArgs k{};
+    if (!(kinds >> kind & 1)) continue;
     int64_t n = 0;
+    k.nblocks = 0;
     for (int i = 0; i < p.nblocks; ++i) {
       const MuonBlock& b = p.block[i];
       if (b.count == 0 || small_kind(b) != kind) continue;
       k.block[k.nblocks++] = {b.rows, b.cols, b.offset, b.stride, n};
       n += b.count;
     }
-    if (n == 0) continue;
-    k.u = u;
-    k.update = u.W != nullptr;
-    k.nsteps = p.nsteps;
-    k.eps = p.eps;
-    std::copy(p.step, p.step + kMaxMuonSteps + 1, k.step);
     hipError_t e = hipSuccess;
     switch (kind) {
       case kS32x32: e = launch_small<Small<32, 32, 16, 4, 1>>(k, n, s); break;
@@ -748,13 +753,15 @@ void set_bank(const MuonPlan& p, int i, Bank& b) {
 }
 
 template <int PHASE>
-void launch_phase(const Bank& b, int tile, const MuonStep& st, int ex_next, hipStream_t s) {
+hipError_t launch_phase(const Bank& b, int tile, const MuonStep& st, int ex_next, hipStream_t s) {
   const int R = b.rp / tile, C = b.cp / tile, tiles = PHASE == kGram || PHASE == kPoly ? R * (R + 1) / 2 : R * C;
+  if (tiles * b.m.count >= INT32_MAX - 8) return hipErrorInvalidValue;
   const dim3 g((unsigned)((tiles * b.m.count + 7) / 8 * 8));
   if (tile == 128)
     hipLaunchKernelGGL((muon_gemm_kernel<PHASE, 128>), g, dim3(kGemmThreads), 0, s, b, st, ex_next, tiles);
   else
     hipLaunchKernelGGL((muon_gemm_kernel<PHASE, 64>), g, dim3(kGemmThreads), 0, s, b, st, ex_next, tiles);
+  return hipGetLastError();
 }
 
 // X in two planes, X^T in two buffers of two planes, A and B.
@@ -808,12 +815,12 @@ hipError_t launch_muon(const MuonPlan& p, const MuonUpdate& u, void* ws, hipStre
     hipLaunchKernelGGL(muon_init_kernel, dim3(b.cp / 64, b.rp / 64, n), dim3(kThreads), 0, s, b, p.step[0].ex);
     for (int k = 0; k < p.nsteps; ++k) {
       const int ex_next = p.step[k + 1].ex;
-      launch_phase<kGram>(b, b.square_tile, p.step[k], ex_next, s);
-      launch_phase<kPoly>(b, b.square_tile, p.step[k], ex_next, s);
-      if (k + 1 < p.nsteps)
-        launch_phase<kApply>(b, b.apply_tile, p.step[k], ex_next, s);
-      else
-        launch_phase<kLast>(b, b.apply_tile, p.step[k], ex_next, s);
+      hipError_t e = launch_phase<kGram>(b, b.square_tile, p.step[k], ex_next, s);
+      if (e == hipSuccess) e = launch_phase<kPoly>(b, b.square_tile, p.step[k], ex_next, s);
+      if (e == hipSuccess)
+        e = k + 1 < p.nsteps ? launch_phase<kApply>(b, b.apply_tile, p.step[k], ex_next, s)
+                             : launch_phase<kLast>(b, b.apply_tile, p.step[k], ex_next, s);
+      if (e != hipSuccess) return e;
       std::swap(b.th, b.nh);
       std::swap(b.tl, b.nl);
     }

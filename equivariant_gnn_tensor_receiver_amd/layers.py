@@ -408,23 +408,24 @@ class Muon(_Handle):
         return self._ws
 
 
-def _muon_tensor(muon, t, name, dtype, like):
-    if t.numel() < muon.numel:
-        raise ValueError(f"{name}: {t.numel()} elements, at least {muon.numel} needed")
-    _need(t, name, dtype, like.numel(), like.device)
+def _muon_tensor(muon, t, name, dtype, numel, device):
+    if numel < muon.numel:
+        raise ValueError(f"{name}: {numel} elements, at least {muon.numel} needed")
+    _need(t, name, dtype, numel, device)
 
 
 def tpconv_muon_orthogonalize(muon: Muon, u, out=None, workspace=None, stream=None):
     """The matrices of u (fp32) orthogonalised, in u's shape; elements outside the blocks are zero in a new `out`."""
     dev = _device(u, "u")
-    _muon_tensor(muon, u, "u", torch.float32, u)
+    n = u.numel()
+    _muon_tensor(muon, u, "u", torch.float32, n, dev)
     if out is None:
-        if u.numel() == muon.dense:
+        if n == muon.dense:
             out = _new(u.shape, torch.float32, dev, stream, u)
         else:
             out = _filled(lambda: torch.zeros_like(u), stream)
     else:
-        _muon_tensor(muon, out, "out", torch.float32, u)
+        _muon_tensor(muon, out, "out", torch.float32, n, dev)
     workspace, nbytes = _scratch(workspace, muon.workspace_size(), dev, stream)
     _call("tpconv_muon_orthogonalize", dev, stream, muon.handle, u.data_ptr(), out.data_ptr(), _ptr(workspace), nbytes)
     return out
@@ -436,20 +437,21 @@ def tpconv_muon_step(muon: Muon, W, grad, momentum, lr: float, beta: float = 0.9
     """(new W, new momentum): new tensors, or W_out / momentum_out, which may be W / momentum themselves.  W_bf16
     receives the new weights in bf16 as well.  Elements outside the blocks keep their values in new tensors."""
     dev = _device(W, "W")
-    _muon_tensor(muon, W, "W", torch.float32, W)
-    _muon_tensor(muon, grad, "grad", torch.float32, W)
-    _muon_tensor(muon, momentum, "momentum", torch.float32, W)
-    dense = W.numel() == muon.dense
+    n = W.numel()
+    _muon_tensor(muon, W, "W", torch.float32, n, dev)
+    _muon_tensor(muon, grad, "grad", torch.float32, n, dev)
+    _muon_tensor(muon, momentum, "momentum", torch.float32, n, dev)
+    dense = n == muon.dense
     if W_out is None:
         W_out = _new(W.shape, torch.float32, dev, stream, W) if dense else _filled(W.clone, stream)
     else:
-        _muon_tensor(muon, W_out, "W_out", torch.float32, W)
+        _muon_tensor(muon, W_out, "W_out", torch.float32, n, dev)
     if momentum_out is None:
         momentum_out = _new(W.shape, torch.float32, dev, stream, momentum) if dense else _filled(momentum.clone, stream)
     else:
-        _muon_tensor(muon, momentum_out, "momentum_out", torch.float32, W)
+        _muon_tensor(muon, momentum_out, "momentum_out", torch.float32, n, dev)
     if W_bf16 is not None:
-        _muon_tensor(muon, W_bf16, "W_bf16", torch.bfloat16, W)
+        _muon_tensor(muon, W_bf16, "W_bf16", torch.bfloat16, n, dev)
     workspace, nbytes = _scratch(workspace, muon.workspace_size(), dev, stream)
     args = MuonStepArgs(lr, beta, int(nesterov), weight_decay)
     _call("tpconv_muon_step", dev, stream, muon.handle, ctypes.byref(args), W.data_ptr(), grad.data_ptr(),
