@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstdint>
 #include <cstring>
 #include <memory>
 #include <string>
@@ -38,6 +39,10 @@ namespace {
 
 tpconv_status dev(hipError_t e) { return e == hipSuccess ? TPCONV_SUCCESS : TPCONV_ERROR_DEVICE; }
 bool bad_dtype(int t) { return t != TPCONV_F32 && t != TPCONV_BF16; }
+// Too small, or not aligned for the 16-byte accesses of the kernels.
+bool bad_workspace(const void* ws, size_t bytes, size_t need) {
+  return need > 0 && (!ws || bytes < need || reinterpret_cast<uintptr_t>(ws) % 16 != 0);
+}
 bool bad_count(int64_t n) { return n < 0 || n >= INT32_MAX; }
 
 // Irreps of one side and their feature offsets.
@@ -270,7 +275,7 @@ tpconv_status tpconv_norm_backward(tpconv_norm norm, int64_t num_nodes, const vo
   NormArgs a = norm_args(*norm, num_nodes);
   const size_t need = (size_t)norm_backward_blocks(a) * sizeof(float);
   const bool params = grad_weight || grad_bias;
-  if (params && (!workspace || workspace_bytes < need)) return TPCONV_ERROR_WORKSPACE;
+  if (params && bad_workspace(workspace, workspace_bytes, need)) return TPCONV_ERROR_WORKSPACE;
   if (!params && !grad_x) return TPCONV_SUCCESS;
   a.x = x;
   a.w = weight;
@@ -367,7 +372,8 @@ tpconv_status tpconv_linear_groups(tpconv_linear linear, int64_t num_nodes, cons
                                    void* stream) {
   if (!linear || bad_count(num_nodes) || !offsets || (num_nodes > 0 && (!group || !order)))
     return TPCONV_ERROR_INVALID_VALUE;
-  if (!workspace || workspace_bytes < lin_groups_workspace(num_nodes, linear->groups)) return TPCONV_ERROR_WORKSPACE;
+  if (bad_workspace(workspace, workspace_bytes, lin_groups_workspace(num_nodes, linear->groups)))
+    return TPCONV_ERROR_WORKSPACE;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (validate && num_nodes > 0) {
     int32_t* flag = static_cast<int32_t*>(workspace);
@@ -397,7 +403,7 @@ tpconv_status tpconv_linear_forward(tpconv_linear linear, int64_t num_nodes, con
   if (num_nodes == 0) return TPCONV_SUCCESS;
   if (!x || !y || (!W && linear->w_numel > 0)) return TPCONV_ERROR_INVALID_VALUE;
   const size_t need = linear_workspace(*linear, TPCONV_OP_FORWARD, num_nodes);
-  if (need > 0 && (!workspace || workspace_bytes < need)) return TPCONV_ERROR_WORKSPACE;
+  if (bad_workspace(workspace, workspace_bytes, need)) return TPCONV_ERROR_WORKSPACE;
   LinRowsArgs a;
   rows_args(*linear, false, num_nodes, offsets, order, x, W, y, a);
   return dev(launch_lin_rows(a, static_cast<hipStream_t>(stream)));
@@ -415,7 +421,7 @@ tpconv_status tpconv_linear_backward(tpconv_linear linear, int64_t num_nodes, co
     return grad_W ? dev(launch_fill(grad_W, linear->w_numel * linear->groups, 0.f, s)) : TPCONV_SUCCESS;
   if (!grad_y || (grad_x && !W && linear->w_numel > 0) || (grad_W && !x)) return TPCONV_ERROR_INVALID_VALUE;
   const size_t need = grad_W ? linear_workspace(*linear, TPCONV_OP_BACKWARD, num_nodes) : 0;
-  if (need > 0 && (!workspace || workspace_bytes < need)) return TPCONV_ERROR_WORKSPACE;
+  if (bad_workspace(workspace, workspace_bytes, need)) return TPCONV_ERROR_WORKSPACE;
   LinBackwardArgs a;
   std::memset(&a, 0, sizeof(a));
   if (grad_x) rows_args(*linear, true, num_nodes, offsets, order, grad_y, W, grad_x, a.rows);
@@ -520,7 +526,7 @@ tpconv_status tpconv_muon_orthogonalize(tpconv_muon muon, const float* u, float*
                                         size_t workspace_bytes, void* stream) {
   if (!muon || !u || !out) return TPCONV_ERROR_INVALID_VALUE;
   const size_t need = muon_workspace(muon->plan);
-  if (need > 0 && (!workspace || workspace_bytes < need)) return TPCONV_ERROR_WORKSPACE;
+  if (bad_workspace(workspace, workspace_bytes, need)) return TPCONV_ERROR_WORKSPACE;
   MuonUpdate a{};
   a.u = u;
   a.out = out;
@@ -535,7 +541,7 @@ tpconv_status tpconv_muon_step(tpconv_muon muon, const tpconv_muon_step_args* ar
       (args->nesterov != 0 && args->nesterov != 1))
     return TPCONV_ERROR_INVALID_VALUE;
   const size_t need = muon_workspace(muon->plan);
-  if (need > 0 && (!workspace || workspace_bytes < need)) return TPCONV_ERROR_WORKSPACE;
+  if (bad_workspace(workspace, workspace_bytes, need)) return TPCONV_ERROR_WORKSPACE;
   MuonUpdate a{};
   a.W = W;
   a.grad = grad;

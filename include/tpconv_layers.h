@@ -19,7 +19,8 @@
  * calls must not share a workspace, nothing allocates, no exception crosses
  * the ABI.  Inputs and outputs must not overlap unless a call allows it.
  * All results are deterministic: every sum has a fixed order, nothing is added
- * with atomics.  Pointers need the alignment of their element type.
+ * with atomics.  Pointers need the alignment of their element type, workspaces
+ * one of 16 bytes (TPCONV_ERROR_WORKSPACE otherwise).
  * All sums and statistics are fp32 whatever the input types.
  */
 #ifndef TPCONV_LAYERS_H_

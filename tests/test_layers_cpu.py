@@ -126,3 +126,15 @@ def test_binding_refuses_tensors_the_kernels_would_misread():
         ly.tpconv_norm_forward(norm, torch.zeros(3, 8))
     with pytest.raises(ValueError, match="GPU"):
         ly.tpconv_muon_orthogonalize(ly.Muon([(4, 4)]), torch.zeros(4, 4))
+
+
+def test_a_workspace_that_is_not_16_byte_aligned_is_refused():
+    L = ly._lib()
+    norm, lin, muon = ly.Norm("8x0e+8x1o"), ly.Linear("8x0e", "8x0e", 3), ly.Muon([(160, 160)])
+    assert muon.workspace_size() > 0
+    for by in (1, 4, 8):
+        off = FAKE.value + by if hasattr(FAKE, "value") else FAKE + by
+        assert L.tpconv_norm_backward(norm.handle, 4, FAKE, None, FAKE, None, None, FAKE, None, off, BIG, None) == 4
+        assert L.tpconv_linear_groups(lin.handle, 4, FAKE, FAKE, FAKE, 1, off, BIG, None) == 4
+        assert L.tpconv_linear_backward(lin.handle, 4, FAKE, FAKE, FAKE, FAKE, FAKE, None, FAKE, off, BIG, None) == 4
+        assert L.tpconv_muon_orthogonalize(muon.handle, FAKE, FAKE, off, BIG, None) == 4
