@@ -12,6 +12,12 @@
 // Bound by HBM: the forward reads x and writes y, the backward reads x and g
 // and writes gx; the parameter gradients are summed per block of threads over
 // the nodes it takes, and the blocks' sums are added in a fixed order.
+//
+// Measured (kernel times; a plain copy of the sizes runs at 5.4 to 8.5 TB/s on
+// this chip): 32768 nodes of 288 fp32 values forward 14.4 us (5.2 TB/s),
+// backward 20.8 (5.5) and 4.3 for the sums of the parameters; 8192 rows of 4096
+// bf16 values forward 28.7 us (4.7 TB/s), backward 65.6 (fp32 gradients, 5.1)
+// and 4.9; 64 nodes of 32 values 3.1 us (a launch).
 #include "device_common.h"
 #include "layers.h"
 #include "timing.h"
@@ -143,7 +149,9 @@ struct Quad {
 // ---- narrow blocks (at most 256 channels) -------------------------------------------
 // A group of `lanes` lanes (a power of two, four channels per lane) takes one
 // (node, irrep) and keeps its N rows in registers: one read, statistics by lane
-// swaps, one write.
+// swaps, one write.  (A block of threads per node and irrep with the values read
+// again for each sum, the general path below, takes 437 us for the 32768 x 288
+// training step against 39.)
 
 template <int N, typename TX, typename TY>
 __device__ __forceinline__ void forward_narrow(const NormArgs& a, const NormIrrep& ir) {
@@ -302,6 +310,8 @@ __global__ __launch_bounds__(kThreads) void norm_backward_narrow_kernel(const No
 // ---- wide scalar rows (one row of 257 to 8192 channels) ------------------------------
 // A block of threads per node; a thread keeps its 4 V channels of the row, of
 // the weights and of the parameter gradients in registers over all its nodes.
+// (8192 x 4096 bf16 training step: 699 us on the general path, 142 with a row's
+// values in registers, 99 with the weights kept and the next row prefetched.)
 
 __device__ __forceinline__ void block_sum2(float& u, float& v, float2* tmp) {
   u = group_sum(u, 64);

@@ -20,6 +20,16 @@
 // the pieces whose ranks add up to at most 2 are added in fp32, smallest
 // first: what is left out is below 2^-22 of a term.  bf16 operands are one
 // piece, so bf16 x bf16 takes one product, mixed types three, fp32 six.
+//
+// Measured (kernel times): 8192 nodes of 128x0e+128x1o+128x2e in fp32, 16
+// groups: forward 37 us (2.4 GFLOP x 6 products: 390 TFLOP/s of the matrix
+// cores, 2.1 TB/s), both gradients 49, their join 9.  The wave slots start
+// together, so address setup, loads, splitting, products and stores follow one
+// another over the whole chip, and no single one of them is the limit (leaving
+// any one out saves 6 to 8 us).  8192 nodes of 1024x0e in bf16 to 2048x0e, 8
+// groups: forward 75 us (34 GFLOP, 460 TFLOP/s), both gradients 285 (69 GFLOP
+// x 3 products, 720 TFLOP/s; three waves per SIMD), bound by the splitting of
+// the fp32 gradients into pieces beside the products.
 #include "device_common.h"
 #include "layers.h"
 #include "timing.h"
@@ -35,6 +45,7 @@ typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kThreads = 256;
+constexpr int kCUs = 256;
 
 // N fp32 values as three planes of packed bf16 (exact: truncation leaves 8 bits
 // per piece); bf16 values are one plane already.
@@ -339,8 +350,10 @@ __device__ __forceinline__ void store_out(uint16_t* p, int64_t i, float v) {
 // Tile shapes.  A block of four waves computes BM x BN; with KS = 1 its waves
 // take WM x WN each, with KS = 4 every wave takes a quarter of the reduction of
 // the whole tile and the sums are added in order through LDS.
-// AHEAD chunks of loads are in flight (more than one pays where few blocks wait
-// for memory: four rows over 64 experts took 16.3 us with one, see RowsShape).
+// AHEAD chunks of loads are in flight: one in the wide shapes (two or three
+// changed nothing for fp32 and slowed the bf16 experts), more where few blocks
+// wait for memory: four bf16 rows over 64 matrices of 1024 x 2048 took 16.3 us
+// with one and take 10.0 with the chunks of the shape for few rows.
 template <int BM_, int BN_, int WM_, int WN_, int KS_, int KC_, int AHEAD_ = 1>
 struct Shape {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, KS = KS_, KC = KC_, kAhead = AHEAD_;
@@ -668,8 +681,11 @@ __global__ __launch_bounds__(kThreads, 2) void lin_rows_kernel(const LinRowsArgs
 }
 
 // Both gradients in one launch: the weight gradient's tiles, then the input
-// gradient's.  They read the same gy and wait for memory at different times.
-// (bf16 x and W: three waves per SIMD fit, two registers short of it without the bound)
+// gradient's.  They read the same gy and wait for memory at different times
+// (8192 nodes of 128x0e+128x1o+128x2e, fp32: 130 us of kernels for the training
+// step with a launch each, 104 with one).  bf16 x and W: three waves per SIMD
+// fit, two registers short of it without the bound (416 -> 358 us for the
+// experts above).
 template <typename S, typename SG, typename TX, typename TW>
 __global__ __launch_bounds__(kThreads, Planes<TX>::count + Planes<TW>::count == 2 ? 3 : 2) void lin_backward_kernel(const LinBackwardArgs /*args*/) {
   const LinBackwardArgs& a = *(const LinBackwardArgs*)__builtin_amdgcn_kernarg_segment_ptr();
@@ -868,7 +884,7 @@ hipError_t launch_rows_types(const LinRowsArgs& a, hipStream_t s) {
   }
 }
 
-// Weight-gradient shapes of the same widths (0: of launches of few rows).
+// Weight-gradient shapes of the same widths.
 template <int BN>
 struct GwShape {
   using type = Shape<128, 128, 64, 64, 1, 32>;
@@ -879,10 +895,6 @@ struct GwShape<64> {
 };
 template <>
 struct GwShape<32> {
-  using type = Shape<32, 32, 32, 32, 4, 64>;
-};
-template <>
-struct GwShape<0> {
   using type = Shape<32, 32, 32, 32, 4, 64>;
 };
 
@@ -917,14 +929,21 @@ int64_t row_tiles(int64_t rows, int G, int shift, int32_t& by_row) {
 }
 
 // Tiles of the rows jobs of a launch, all of one shape (a launch per shape would
-// run one after the other: the ragged training step took 91 us in seven
-// launches).  The width is the one with the least padded work; narrow tiles
-// count more per column because they re-read the rows and share less (factors
-// 5/4 per halving); 0: the 32 x 32 shape of launches of few rows.
+// run one after the other: the training step of 5003 nodes, 65x0e+33x1o+20x1o+
+// 17x2e, 89 groups took 91 us in seven launches and takes 53 in three).  The
+// width is the one of least padded work (narrow tiles count more per column
+// because they re-read the rows and share less: 5/4 per halving), of which
+// launches of fewer blocks than CUs reach only their share: 1024 rows x 1024 x
+// 1024 in fp32 take 63 us in 64 blocks of 128 columns, 43.5 in 256 of 32; 2048
+// rows 64.5 in 128 blocks, 57.5 in 256 of 64; 4000 x 256 x 256 21.5 against
+// 13.9; 20000 nodes of 48x0e+48x1o 23.9 at 128, 14.9 at 64.
+// 0: the 32 x 32 shape, its reduction split over the waves, below 64 blocks of
+// 128 x 128: 512 rows of 1024 channels 33.2 us against 36.9, 256 rows 19.8
+// against 36.9; at 1024 rows (64 blocks) it takes 47.4 against 43.5.
 int plan_rows(LinRowsArgs& a) {
   int width = 128;
   double best = 0.0;
-  int64_t big = 0;
+  int64_t wide = 0;
   for (int w : {128, 64, 32}) {
     double cost = 0.0;
     int64_t blocks = 0;
@@ -933,13 +952,14 @@ int plan_rows(LinRowsArgs& a) {
       cost += (double)a.N * a.job[j].n * tiles * w * (w == 128 ? 1.0 : w == 64 ? 1.25 : 1.5625);
       blocks += ((a.N * a.job[j].n + 127) / 128) * tiles;
     }
+    if (w == 128) wide = blocks;
+    if (blocks < kCUs) cost *= (double)kCUs / blocks;
     if (w == 128 || cost < best) {
       best = cost;
       width = w;
-      big = blocks;
     }
   }
-  if (big < 64) width = 0;
+  if (wide < 64) width = 0;
   const int bn = width ? width : 32, shift = width ? 7 : 5;
   a.tiles = 0;
   for (int j = 0; j < a.njobs; ++j) {
@@ -951,7 +971,9 @@ int plan_rows(LinRowsArgs& a) {
   return width;
 }
 
-// The same for the weight gradient's tiles of W x W; smaller tiles read both operands more often.
+// The same for the weight gradient's tiles of W x W; smaller tiles read both
+// operands more often (20000 nodes of 48x0e+48x1o, backward: 41.0 us at 128,
+// 29.4 at 64; of 96x0e+96x1o: 47.2 at 128, 56.6 at 64).
 int gw_width(const LinGwArgs& a) {
   int width = 128;
   double best = 0.0;

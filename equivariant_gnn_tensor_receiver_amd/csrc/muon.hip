@@ -12,7 +12,21 @@
 // operands' magnitudes, and what X, A and B can reach is known: |X|_2 <= s_t
 // with s_0 = 1 and s_{t+1} the largest |a s + b s^3 + c s^5| on [0, s_t]; so
 // powers of two fixed by the host per step keep them inside the fp16 range
-// with their lo parts normal).  X lives in these two planes between the steps.
+// with their lo parts normal).
+//
+// Matrices up to 128 x 128 (or 64 x 256, 32 x 512) run all their steps in one
+// block of threads; larger ones run one launch per product (norm, init, then
+// three per step), with X, X^T, A and B as hi and lo planes in the workspace.
+//
+// Measured (kernel times, five steps): 88 matrices of 32 x 32 9.0 us, 184 of
+// 64 x 64 17.8 and 176 of 128 x 128 47 (one block per CU, each a chain of 15
+// dependent products through LDS: bound by that latency, not by the matrix
+// cores, which see 11 GFLOP x 3 = 0.7 PFLOP/s at 128).  Two of 1024 x 2048:
+// X X^T 39 us (half of it: 13.7 GFLOP of fp16 products), A A 25, B X 40 (25.8
+// GFLOP, 0.65 PFLOP/s), the last B X with the update 55, init 19, norm 13.
+// There 272 blocks share 256 CUs in the r x r products: the doubled-up CUs set
+// the time (256 blocks of the same size take 60% of it); cutting the reduction
+// into equal parts instead gave 25 + 8 us (the join) and 18 + 8, no gain.
 #include "device_common.h"
 #include "layers.h"
 #include "timing.h"
@@ -735,9 +749,13 @@ void set_bank(const MuonPlan& p, int i, Bank& b) {
   b.transposed = b.m.rows > b.m.cols;
   b.r = b.transposed ? b.m.cols : b.m.rows;
   b.c = b.transposed ? b.m.rows : b.m.cols;
-  // 128-wide tiles where they are enough for the 256 CUs
+  // 128-wide tiles, which read LDS six times for six products instead of four for
+  // three, where there are enough of them: r x r products of 144 such tiles
+  // (4 x 1024 x 1024, whole call) 502 us against 522 at 64, of 160 (16 x 512 x
+  // 512) 335 against 355, of 72 to 96 slower (32 x 256 x 256: 224 against 205);
+  // B X in 256 tiles (16 x 512 x 512) 355 against 385
   const int64_t R = (b.r + 127) / 128, C = (b.c + 127) / 128;
-  b.square_tile = R * (R + 1) / 2 * b.m.count >= 256 ? 128 : 64;
+  b.square_tile = R * (R + 1) / 2 * b.m.count >= 128 ? 128 : 64;
   b.apply_tile = R * C * b.m.count >= 192 ? 128 : 64;
   const int pad = b.square_tile > b.apply_tile ? b.square_tile : b.apply_tile;
   b.rp = (b.r + pad - 1) / pad * pad;
