@@ -62,7 +62,7 @@ struct Bank {
   int32_t chunks;          // blocks per matrix of the norm
   float eps, scale;        // scale: sqrt(max(1, cols / rows))
   int32_t update;          // 0: orthogonalize, 1: optimiser step
-  float* norm;             // [count][chunks] sums of squares
+  float2* norm;            // [count][chunks] sums of squares (Squares)
   int64_t xsize, tsize, asize;  // halfs per matrix of the planes of X, X^T, and A or B
   _Float16 *xh, *xl;       // [count][rp][cl]
   _Float16 *th, *tl;       // [count][cp][rl]: X^T
@@ -82,6 +82,26 @@ __device__ __forceinline__ float u_at(const Bank& b, int64_t e) {
   if (!b.update) return b.u.u[e];
   const float m = b.u.mom_out[e];
   return b.u.nesterov ? (1.f - b.u.beta) * b.u.grad[e] + b.u.beta * m : m;
+}
+
+// |U|^2 as s 4^e.  e is 0 where the plain sum is in range (`plain_sum`); else the values are taken
+// times 2^-e, with e the exponent of the largest of them, so that any finite matrix has its norm:
+// X = (U 2^-e) / max(sqrt(s), eps 2^-e).
+constexpr int kLeastExponent = -100;  // of the smallest value, 2^-149, the square still has room at 2^(2 (100 - 149))
+struct Squares {
+  float s;
+  int e;
+};
+__device__ __forceinline__ Squares add(const Squares& a, const Squares& b) {
+  const int e = max(a.e, b.e);
+  return {ldexpf(a.s, 2 * (a.e - e)) + ldexpf(b.s, 2 * (b.e - e)), e};
+}
+// Neither overflown (of up to 2^18 such sums either) nor made of squares that underflow, unless eps decides anyway.
+__device__ __forceinline__ bool plain_sum(float s, float eps) {
+  return s <= 0x1p100f && (s >= 0x1p-90f || eps >= 0x1p-44f);
+}
+__device__ __forceinline__ int scale_exponent(float largest) {
+  return largest > 0.f ? max(__builtin_amdgcn_frexp_expf(largest) - 1, kLeastExponent) : kLeastExponent;
 }
 
 __global__ __launch_bounds__(kThreads) void muon_norm_kernel(const Bank /*args*/) {
@@ -112,13 +132,31 @@ __global__ __launch_bounds__(kThreads) void muon_norm_kernel(const Bank /*args*/
       q = __builtin_fmaf(v, v, q);
     }
   }
-  tmp[threadIdx.x] = q;
-  __syncthreads();
-  for (int s = kThreads / 2; s > 0; s >>= 1) {
-    if ((int)threadIdx.x < s) tmp[threadIdx.x] += tmp[threadIdx.x + s];
+  auto reduce = [&](float v, auto join) {  // over the block, the result in every thread
+    tmp[threadIdx.x] = v;
     __syncthreads();
+    for (int s = kThreads / 2; s > 0; s >>= 1) {
+      if ((int)threadIdx.x < s) tmp[threadIdx.x] = join(tmp[threadIdx.x], tmp[threadIdx.x + s]);
+      __syncthreads();
+    }
+    v = tmp[0];
+    __syncthreads();
+    return v;
+  };
+  auto sum = [](float x, float y) { return x + y; };
+  Squares all = {reduce(q, sum), 0};
+  if (!plain_sum(all.s, b.eps)) {  // (uniform over the block; every thread reads the elements that it wrote)
+    float largest = 0.f;
+    for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) largest = fmaxf(largest, fabsf(u_at(b, base + i)));
+    all.e = scale_exponent(reduce(largest, [](float x, float y) { return fmaxf(x, y); }));
+    q = 0.f;
+    for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) {
+      const float v = ldexpf(u_at(b, base + i), -all.e);
+      q = __builtin_fmaf(v, v, q);
+    }
+    all.s = reduce(q, sum);
   }
-  if (threadIdx.x == 0) b.norm[(int64_t)blockIdx.y * b.chunks + blockIdx.x] = tmp[0];
+  if (threadIdx.x == 0) b.norm[(int64_t)blockIdx.y * b.chunks + blockIdx.x] = {all.s, __int_as_float(all.e)};
 }
 
 // X = U / max(|U|, eps) into the planes of X and X^T (zero in the padding), by
@@ -126,24 +164,29 @@ __global__ __launch_bounds__(kThreads) void muon_norm_kernel(const Bank /*args*/
 __global__ __launch_bounds__(kThreads) void muon_init_kernel(const Bank /*args*/, int ex) {
   const Bank& b = *(const Bank*)__builtin_amdgcn_kernarg_segment_ptr();
   __shared__ float tile[64][65];
-  __shared__ float tmp[kThreads];
+  __shared__ Squares tmp[kThreads];
   const int64_t bz = blockIdx.z;
-  float q = 0.f;
-  for (int i = threadIdx.x; i < b.chunks; i += kThreads) q += b.norm[bz * b.chunks + i];
+  Squares q = {0.f, kLeastExponent};
+  for (int i = threadIdx.x; i < b.chunks; i += kThreads) {
+    const float2 n = b.norm[bz * b.chunks + i];
+    q = add(q, {n.x, __float_as_int(n.y)});
+  }
   tmp[threadIdx.x] = q;
   __syncthreads();
   for (int s = kThreads / 2; s > 0; s >>= 1) {
-    if ((int)threadIdx.x < s) tmp[threadIdx.x] += tmp[threadIdx.x + s];
+    if ((int)threadIdx.x < s) tmp[threadIdx.x] = add(tmp[threadIdx.x], tmp[threadIdx.x + s]);
     __syncthreads();
   }
-  const float f = pow2(ex) / fmaxf(sqrtf(tmp[0]), b.eps);
+  q = tmp[0];
+  const float f = pow2(ex) / fmaxf(sqrtf(q.s), ldexpf(b.eps, -q.e));
   const int i0 = blockIdx.y * 64, j0 = blockIdx.x * 64, lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int64_t base = b.m.offset + bz * b.m.stride;
   // rows of U: rows of X, or its columns when X = U^T
   const int u0 = b.transposed ? j0 : i0, v0 = b.transposed ? i0 : j0;
   for (int k = w; k < 64; k += 4) {
     float v = 0.f;
-    if (u0 + k < b.m.rows && v0 + lane < b.m.cols) v = u_at(b, base + (int64_t)(u0 + k) * b.m.cols + v0 + lane) * f;
+    if (u0 + k < b.m.rows && v0 + lane < b.m.cols)
+      v = ldexpf(u_at(b, base + (int64_t)(u0 + k) * b.m.cols + v0 + lane), -q.e) * f;
     tile[k][lane] = v;
   }
   __syncthreads();
@@ -571,12 +614,38 @@ __global__ __launch_bounds__(64 * S::NW) void muon_small_kernel(const SmallArgs 
       q = __builtin_fmaf(v, v, q);
     }
   }
-  for (int d = 32; d > 0; d >>= 1) q += __shfl_xor(q, d);
-  if (lane == 0) s_norm[wave] = q;
-  __syncthreads();
-  q = 0.f;
-  for (int w = 0; w < S::NW; ++w) q += s_norm[w];
-  const float inv = 1.f / fmaxf(sqrtf(q), a.eps);
+  auto reduce = [&](float v, auto join) {  // over the block, the result in every thread
+    for (int d = 32; d > 0; d >>= 1) v = join(v, __shfl_xor(v, d));
+    if (lane == 0) s_norm[wave] = v;
+    __syncthreads();
+    v = 0.f;
+    for (int w = 0; w < S::NW; ++w) v = join(v, s_norm[w]);
+    return v;
+  };
+  auto sum = [](float u, float v) { return u + v; };
+  q = reduce(q, sum);
+  float least = a.eps;
+  if (!plain_sum(q, a.eps)) {  // uniform over the block
+    float largest = 0.f;
+#pragma unroll
+    for (int t = 0; t < TPW; ++t)
+#pragma unroll
+      for (int r = 0; r < R; ++r) largest = fmaxf(largest, fabsf(x[t][r]));
+    __syncthreads();
+    const int e = scale_exponent(reduce(largest, [](float u, float v) { return fmaxf(u, v); }));
+    q = 0.f;
+#pragma unroll
+    for (int t = 0; t < TPW; ++t)
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        x[t][r] = ldexpf(x[t][r], -e);
+        q = __builtin_fmaf(x[t][r], x[t][r], q);
+      }
+    __syncthreads();
+    q = reduce(q, sum);
+    least = ldexpf(a.eps, -e);
+  }
+  const float inv = 1.f / fmaxf(sqrtf(q), least);
 #pragma unroll
   for (int t = 0; t < TPW; ++t)
 #pragma unroll
@@ -785,7 +854,7 @@ hipError_t launch_phase(const Bank& b, int tile, const MuonStep& st, int ex_next
 // X in two planes, X^T in two buffers of two planes, A and B.
 size_t bank_bytes(const Bank& b) {
   const size_t n = (size_t)b.m.count * 2;
-  return align_up((size_t)b.m.count * b.chunks * 4) + n * (2 * b.xsize + 4 * b.tsize + 4 * b.asize);
+  return align_up((size_t)b.m.count * b.chunks * sizeof(float2)) + n * (2 * b.xsize + 4 * b.tsize + 4 * b.asize);
 }
 
 }  // namespace
@@ -811,8 +880,9 @@ hipError_t launch_muon(const MuonPlan& p, const MuonUpdate& u, void* ws, hipStre
     if (b.m.count == 0 || small_kind(b.m) >= 0) continue;
     b.u = u;
     b.update = u.W != nullptr;
-    b.norm = static_cast<float*>(ws);
-    _Float16* at = reinterpret_cast<_Float16*>(static_cast<char*>(ws) + align_up((size_t)b.m.count * b.chunks * 4));
+    b.norm = static_cast<float2*>(ws);
+    _Float16* at =
+        reinterpret_cast<_Float16*>(static_cast<char*>(ws) + align_up((size_t)b.m.count * b.chunks * sizeof(float2)));
     auto take = [&](int64_t size) {
       _Float16* p = at;
       at += b.m.count * size;

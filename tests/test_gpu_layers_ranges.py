@@ -1,0 +1,78 @@
+"""The node layers at the ends of the range of fp32 and on empty tensors, against their fp64 definitions.
+
+The orthogonalisation's tolerances are those of test_gpu_layers.py: a matrix's scale takes no part in them.
+"""
+import numpy as np
+import pytest
+
+from gpu_cases import say
+from oracle import layers as ol
+from test_gpu_layers import MUON_TOL, QUINTIC, U, cuda, f64, frob, ly, matrices  # noqa: F401  (ly: the fixture)
+
+pytestmark = pytest.mark.gpu
+
+# one block of threads per matrix (both tile sizes, transposed), and the tiled path (T = 64, transposed)
+MUON_SHAPES = [(32, 32), (12, 40), (100, 90), (140, 131), (131, 300), (300, 131)]
+
+
+def scaled(count, rows, cols, seed, largest):
+    """Matrices whose largest entry is `largest` in magnitude."""
+    u = matrices(count, rows, cols, seed).astype(np.float64)
+    return (u / np.abs(u).max((1, 2), keepdims=True) * largest).astype(np.float32)
+
+
+@pytest.mark.parametrize("rows,cols", MUON_SHAPES)
+def test_orthogonalize_any_finite_matrix(ly, rows, cols):
+    """Entries whose squares leave fp32 on either side: the singular values are those of the scaled matrix."""
+    for largest in (9e17, 1e19, 1e30, 3.4e38):
+        say(f"[case] orthogonalize {rows} x {cols} with entries of {largest:g}")
+        u = scaled(2, rows, cols, 31, largest)
+        o = ly.tpconv_muon_orthogonalize(ly.Muon([(rows, cols, 2)]), cuda(u))
+        assert frob(f64(o) - ol.orthogonalize(u, [QUINTIC] * 5)).max() <= MUON_TOL
+    for largest, eps in ((1e-20, 1e-30), (1e-30, 1e-40), (1e-38, 1e-45), (1e-30, 1e-7), (1e30, 1e-45)):
+        say(f"[case] orthogonalize {rows} x {cols} with entries of {largest:g} and eps {eps:g}")
+        u = scaled(2, rows, cols, 32, largest)
+        u[1] = 0.0
+        o = ly.tpconv_muon_orthogonalize(ly.Muon([(rows, cols, 2)], eps=eps), cuda(u))
+        least = float(np.float32(eps))
+        assert frob(f64(o) - ol.orthogonalize(u, [QUINTIC] * 5, least)).max() <= MUON_TOL
+        assert not o[1].any()
+
+
+def test_orthogonalize_parts_of_very_different_size(ly):
+    """Rows of zeros, tiny and huge entries in one matrix: the chunks of its norm have different scales."""
+    for eps in (1e-7, 1e-45):
+        say(f"[case] orthogonalize 400 x 150 with rows of different scales, eps {eps:g}")
+        u = matrices(2, 400, 150, 33)
+        u[:, :30] = 0.0
+        u[:, 30:60] *= np.float32(1e-30)
+        u[0, 390:] *= np.float32(1e33)
+        u[1, 390:] *= np.float32(1e22)
+        o = ly.tpconv_muon_orthogonalize(ly.Muon([(400, 150, 2)], eps=eps), cuda(u))
+        assert frob(f64(o) - ol.orthogonalize(u, [QUINTIC] * 5, eps)).max() <= MUON_TOL
+
+
+@pytest.mark.parametrize("rows,cols", [(32, 32), (140, 131)])
+@pytest.mark.parametrize("nesterov", [True, False])
+def test_muon_step_with_huge_gradients(ly, rows, cols, nesterov):
+    say(f"[case] muon step {rows} x {cols} with gradients of 1e30")
+    W = np.random.default_rng(34).standard_normal((2, rows, cols)).astype(np.float32)
+    g, m = scaled(2, rows, cols, 35, 1e30), scaled(2, rows, cols, 36, 3e29)
+    W1, m1 = ly.tpconv_muon_step(ly.Muon([(rows, cols, 2)]), cuda(W), cuda(g), cuda(m), lr=0.05, beta=0.9,
+                                 nesterov=nesterov, weight_decay=0.1)
+    rW, rm = ol.muon_step(W, g, m, [QUINTIC] * 5, 0.05, 0.9, nesterov, 0.1)
+    scale = np.sqrt(max(1.0, cols / rows))
+    assert frob(f64(W1) - rW).max() <= 0.05 * scale * MUON_TOL + 4 * U * frob(W).max()
+    assert np.abs(f64(m1) - rm).max() <= 4 * U * np.abs(rm).max()
+    assert not np.array_equal(f64(W1), np.float64(np.float32(1 - 0.005)) * W)  # more than the decay
+
+
+def test_orthogonalize_infinite_entry_is_not_hidden(ly):
+    import torch
+
+    for rows, cols in ((12, 40), (140, 131)):
+        say(f"[case] orthogonalize {rows} x {cols} with an infinite entry")
+        u = matrices(2, rows, cols, 37)
+        u[1, 3, 4] = np.inf
+        o = ly.tpconv_muon_orthogonalize(ly.Muon([(rows, cols, 2)]), cuda(u))
+        assert torch.isfinite(o[0]).all() and torch.isnan(o[1]).all()
