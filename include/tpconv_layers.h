@@ -141,7 +141,9 @@ tpconv_status tpconv_linear_backward(tpconv_linear linear, int64_t num_nodes, co
  *   X = U / max(|U|_F, eps);  per step  A = X X^T,  X <- a X + (b A + c A A) X
  * (X^T X form for matrices with more rows than columns, the same result), which
  * takes the singular values s of X to a s + b s^3 + c s^5 and leaves the
- * singular vectors alone.  Entries of U below 1e18 in magnitude. */
+ * singular vectors alone.  U may hold any finite values (its norm is scaled by
+ * a power of two where the squares would leave fp32); a matrix with a value that
+ * is not finite comes out as NaN. */
 typedef struct tpconv_muon_s* tpconv_muon;
 
 /* `count` row-major matrices of rows x cols at element offset + i * stride. */
