@@ -144,6 +144,12 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _nothing_to_compute(*outs):
+    """Whether every wanted result is empty (an empty tensor has no address, which C reads as one that is not wanted)."""
+    wanted = [t for t in outs if t is not None]
+    return bool(wanted) and all(t.numel() == 0 for t in wanted)
+
+
 def _filled(make, stream):
     """make() with its kernels on the stream of the call they come before."""
     if stream is None:
@@ -245,6 +251,8 @@ def tpconv_norm_backward(norm: Norm, x, weight, grad_y, stats=None, want=("x", "
         _need(grad_weight, "grad_weight", torch.float32, norm.num_weights, dev)
     if grad_bias is not None:
         _need(grad_bias, "grad_bias", torch.float32, norm.num_biases, dev)
+    if _nothing_to_compute(grad_x, grad_weight, grad_bias):
+        return grad_x, grad_weight, grad_bias
     need = norm.workspace_size(n) if grad_weight is not None or grad_bias is not None else 0
     workspace, nbytes = _scratch(workspace, need, dev, stream)
     _call("tpconv_norm_backward", dev, stream, norm.handle, n, x.data_ptr(), _ptr(weight), grad_y.data_ptr(),
@@ -356,6 +364,8 @@ def tpconv_linear_backward(linear: Linear, groups: Groups, x, W, grad_y, want=("
         _need(grad_x, "grad_x", torch.float32, n * linear.feat_in, dev)
     if grad_W is not None:
         _need(grad_W, "grad_W", torch.float32, linear.num_groups * linear.w_per_group, dev)
+    if _nothing_to_compute(grad_x, grad_W):
+        return grad_x, grad_W
     workspace, nbytes = _scratch(workspace, linear.workspace_size(n) if grad_W is not None else 0, dev, stream)
     _call("tpconv_linear_backward", dev, stream, linear.handle, n, _ptr(groups.offsets), _ptr(groups.order),
           x.data_ptr(), W.data_ptr(), grad_y.data_ptr(), _ptr(grad_x), _ptr(grad_W), _ptr(workspace), nbytes)
@@ -426,6 +436,8 @@ def tpconv_muon_orthogonalize(muon: Muon, u, out=None, workspace=None, stream=No
             out = _filled(lambda: torch.zeros_like(u), stream)
     else:
         _muon_tensor(muon, out, "out", torch.float32, n, dev)
+    if _nothing_to_compute(out):
+        return out
     workspace, nbytes = _scratch(workspace, muon.workspace_size(), dev, stream)
     _call("tpconv_muon_orthogonalize", dev, stream, muon.handle, u.data_ptr(), out.data_ptr(), _ptr(workspace), nbytes)
     return out
@@ -452,6 +464,8 @@ def tpconv_muon_step(muon: Muon, W, grad, momentum, lr: float, beta: float = 0.9
         _muon_tensor(muon, momentum_out, "momentum_out", torch.float32, n, dev)
     if W_bf16 is not None:
         _muon_tensor(muon, W_bf16, "W_bf16", torch.bfloat16, n, dev)
+    if _nothing_to_compute(W_out, momentum_out):
+        return W_out, momentum_out
     workspace, nbytes = _scratch(workspace, muon.workspace_size(), dev, stream)
     args = MuonStepArgs(lr, beta, int(nesterov), weight_decay)
     _call("tpconv_muon_step", dev, stream, muon.handle, ctypes.byref(args), W.data_ptr(), grad.data_ptr(),

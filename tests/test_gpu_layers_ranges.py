@@ -76,3 +76,30 @@ def test_orthogonalize_infinite_entry_is_not_hidden(ly):
         u[1, 3, 4] = np.inf
         o = ly.tpconv_muon_orthogonalize(ly.Muon([(rows, cols, 2)]), cuda(u))
         assert torch.isfinite(o[0]).all() and torch.isnan(o[1]).all()
+
+
+def test_gradients_of_empty_tensors(ly):
+    """Gradients asked for one at a time where there is nothing to compute: no nodes, no 0e block, no pair of irreps."""
+    import torch
+
+    say("[case] empty gradients, one at a time")
+    dev = torch.device("cuda")
+    norm, odd = ly.Norm("8x0e+8x1o"), ly.Norm("4x1o")
+    x, three = torch.zeros(0, 32, device=dev), torch.ones(3, 12, device=dev)
+    for name in ("x", "weight", "bias"):
+        got = dict(zip(("x", "weight", "bias"), ly.tpconv_norm_backward(norm, x, None, x, want=(name,))))
+        assert [k for k, v in got.items() if v is not None] == [name] and not got[name].any()
+    assert ly.tpconv_norm_backward(odd, three, None, three, want=("bias",))[2].numel() == 0
+    lin, none = ly.Linear("4x0e", "3x0e", 2), ly.Linear("4x0e", "3x1o", 2)
+    nobody = ly.tpconv_linear_groups(lin, torch.zeros(0, dtype=torch.int32, device=dev))
+    W = torch.ones(lin.w_shape, device=dev)
+    gx, gW = ly.tpconv_linear_backward(lin, nobody, x.view(0, 4), W, x.view(0, 3), want=("x",))
+    assert gx.shape == (0, 4) and gW is None
+    gx, gW = ly.tpconv_linear_backward(lin, nobody, x.view(0, 4), W, x.view(0, 3), want=("W",))
+    assert gx is None and not gW.any()
+    groups = ly.tpconv_linear_groups(none, torch.zeros(3, dtype=torch.int32, device=dev))
+    gx, gW = ly.tpconv_linear_backward(none, groups, torch.ones(3, 4, device=dev), torch.zeros(none.w_shape, device=dev),
+                                       torch.ones(3, 9, device=dev), want=("W",))
+    assert gx is None and gW.shape == (2, 0)
+    u = torch.zeros(0, 4, 4, device=dev)
+    assert ly.tpconv_muon_orthogonalize(ly.Muon([(4, 4, 0)]), u).shape == (0, 4, 4)

@@ -1,0 +1,49 @@
+"""The node layers' binding on its own: empty tensors, threads that share a handle, the pools that results come from (no GPU)."""
+import os
+import sys
+import threading
+
+import pytest
+import torch
+
+from equivariant_gnn_tensor_receiver_amd import tpconv as tp
+
+pytestmark = pytest.mark.skipif(not os.path.exists(tp.LIB_PATH), reason="libtpconv.so not built")
+if os.path.exists(tp.LIB_PATH):
+    from equivariant_gnn_tensor_receiver_amd import layers as ly
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """CPU tensors in place of device tensors; the names of the library calls that would be made."""
+    made = []
+    monkeypatch.setattr(ly, "_device", lambda t, name: t.device)
+    monkeypatch.setattr(ly, "_call", lambda fn, device, stream, *args: made.append(fn))
+    return made
+
+
+def test_empty_wanted_gradients_need_no_call(calls):
+    """An empty tensor has no address, which the C side reads as a gradient that is not wanted."""
+    norm, odd = ly.Norm("8x0e+8x1o"), ly.Norm("4x1o")
+    x = torch.zeros(0, 32)
+    gx, gw, gb = ly.tpconv_norm_backward(norm, x, None, x, want=("x",))
+    assert gx.shape == (0, 32) and gw is None and gb is None
+    ones = torch.ones(3, 12)
+    assert ly.tpconv_norm_backward(odd, ones, None, ones, want=("bias",))[2].shape == (0,)
+    lin, none = ly.Linear("4x0e", "3x0e", 2), ly.Linear("4x0e", "3x1o", 2)
+    gx, gW = ly.tpconv_linear_backward(lin, ly.Groups(0), x.view(0, 4), torch.zeros(lin.w_shape), x.view(0, 3),
+                                       want=("x",))
+    assert gx.shape == (0, 4) and gW is None
+    gx, gW = ly.tpconv_linear_backward(none, ly.Groups(3), torch.ones(3, 4), torch.zeros(none.w_shape),
+                                       torch.ones(3, 9), want=("W",))
+    assert gx is None and gW.shape == (2, 0)
+    bank = ly.Muon([(4, 4, 0)])  # no matrices
+    u = torch.zeros(0, 4, 4)
+    assert ly.tpconv_muon_orthogonalize(bank, u).shape == (0, 4, 4)
+    assert [t.shape for t in ly.tpconv_muon_step(bank, u, u, u, lr=0.1)] == [(0, 4, 4)] * 2
+    assert calls == []
+    # one that holds something is still computed, and no wish at all is still refused by the C side
+    ly.tpconv_norm_backward(norm, x, None, x, want=("x", "weight"))
+    ly.tpconv_linear_backward(lin, ly.Groups(0), x.view(0, 4), torch.zeros(lin.w_shape), x.view(0, 3))
+    ly.tpconv_norm_backward(norm, x, None, x, want=())
+    assert calls == ["tpconv_norm_backward", "tpconv_linear_backward", "tpconv_norm_backward"]
