@@ -186,19 +186,21 @@ class Norm(_Handle):
         tp._check(L.tpconv_norm_info(h, *(ctypes.byref(v) for v in (f, n, w, b))), "tpconv_norm_info")
         self.features, self.num_irreps, self.num_weights, self.num_biases = f.value, n.value, w.value, b.value
         self.x_dtype, self.y_dtype = _dtype(x_dtype), _dtype(y_dtype)
-        self._ws = {}
+        self._ws = (None, 0)
 
     def stats_shape(self, num_nodes: int):
         """Shape of the statistics a forward can save: (mean, 1 / deviation) per node and irrep."""
         return (num_nodes, self.num_irreps, 2)
 
     def workspace_size(self, num_nodes: int) -> int:
-        if num_nodes not in self._ws:
+        last, size = self._ws  # one read and one store: other threads may ask the same handle
+        if last != num_nodes:
             b = c_size_t()
             tp._check(_LIB.tpconv_norm_workspace_size(self.handle, num_nodes, ctypes.byref(b)),
                       "tpconv_norm_workspace_size")
-            self._ws = {num_nodes: b.value}
-        return self._ws[num_nodes]
+            size = b.value
+            self._ws = (num_nodes, size)
+        return size
 
 
 def _norm_nodes(norm, x):
@@ -291,14 +293,16 @@ class Linear(_Handle):
     def workspace_size(self, num_nodes: int, op: int = OP_BACKWARD) -> int:
         """Bytes for `op`; the backward's cover the forward too."""
         key = (num_nodes, op)
-        if key not in self._ws:
+        size = self._ws.get(key)  # other threads may ask the same handle, and replace the dict
+        if size is None:
             b = c_size_t()
             tp._check(_LIB.tpconv_linear_workspace_size(self.handle, op, num_nodes, ctypes.byref(b)),
                       "tpconv_linear_workspace_size")
+            size = b.value
             if len(self._ws) > 16:
                 self._ws = {}
-            self._ws[key] = b.value
-        return self._ws[key]
+            self._ws[key] = size
+        return size
 
 
 class Groups:

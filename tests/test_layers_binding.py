@@ -1,7 +1,6 @@
-"""The node layers' binding on its own: empty tensors, threads that share a handle, the pools that results come from (no GPU)."""
+"""The node layers' binding on its own: empty tensors, calls that share a handle, the pools that results come from (no GPU)."""
 import os
 import sys
-import threading
 
 import pytest
 import torch
@@ -47,3 +46,27 @@ def test_empty_wanted_gradients_need_no_call(calls):
     ly.tpconv_linear_backward(lin, ly.Groups(0), x.view(0, 4), torch.zeros(lin.w_shape), x.view(0, 3))
     ly.tpconv_norm_backward(norm, x, None, x, want=())
     assert calls == ["tpconv_norm_backward", "tpconv_linear_backward", "tpconv_norm_backward"]
+
+
+@pytest.mark.parametrize("make", [lambda: ly.Norm("8x0e+8x1o"), lambda: ly.Linear("8x0e", "8x0e", 3)])
+def test_workspace_size_while_another_thread_asks_the_same_handle(make):
+    """Between any two operations of the call another one runs through, with other node counts."""
+    alone = {n: make().workspace_size(n) for n in range(1, 40)}
+    handle, others = make(), iter(range(1000, 10 ** 6))
+    code = type(handle).workspace_size.__code__
+
+    def trace(frame, event, arg):
+        if frame.f_code is not code:
+            return None
+        frame.f_trace_opcodes = True
+        handle.workspace_size(next(others))  # (untraced: a trace function does not trace itself)
+        return trace
+
+    before = sys.gettrace()
+    sys.settrace(trace)
+    try:
+        got = {n: handle.workspace_size(n) for n in alone}
+        again = {n: handle.workspace_size(n) for n in alone}
+    finally:
+        sys.settrace(before)
+    assert got == alone and again == alone and next(others) > 1100
