@@ -129,15 +129,25 @@ def _call(fn, device, stream, *args):
         raise tp.TpconvError(st, fn)
 
 
-def _new(shape, dtype, device, stream, like=None):
-    """An uninitialised result; one used on another stream is not reused before that stream is done with it."""
-    if like is not None and like.dtype == dtype:
-        t = torch.empty_like(like)
-    else:
-        t = torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None:
-        tp._keep_for_stream(stream, t)
+def _on(stream, device, make):
+    """make(): a new tensor (and what fills it) for a call on `stream`.  Its memory comes from that stream's pool, since
+    pending work of the current stream may still use what the current one's holds, and stays until the current stream,
+    on which a result is used as well, is done with it."""
+    if stream is None:
+        return make()
+    with torch.cuda.stream(stream):
+        t = make()
+    t.record_stream(torch.cuda.current_stream(device))
     return t
+
+
+def _new(shape, dtype, device, stream, like=None):
+    """An uninitialised result."""
+    if stream is not None:
+        return _on(stream, device, lambda: _new(shape, dtype, device, None, like))
+    if like is not None and like.dtype == dtype:
+        return torch.empty_like(like)
+    return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _ptr(t):
@@ -148,14 +158,6 @@ def _nothing_to_compute(*outs):
     """Whether every wanted result is empty (an empty tensor has no address, which C reads as one that is not wanted)."""
     wanted = [t for t in outs if t is not None]
     return bool(wanted) and all(t.numel() == 0 for t in wanted)
-
-
-def _filled(make, stream):
-    """make() with its kernels on the stream of the call they come before."""
-    if stream is None:
-        return make()
-    with torch.cuda.stream(stream):
-        return make()
 
 
 def _scratch(workspace, need, device, stream):
@@ -437,7 +439,7 @@ def tpconv_muon_orthogonalize(muon: Muon, u, out=None, workspace=None, stream=No
         if n == muon.dense:
             out = _new(u.shape, torch.float32, dev, stream, u)
         else:
-            out = _filled(lambda: torch.zeros_like(u), stream)
+            out = _on(stream, dev, lambda: torch.zeros_like(u))
     else:
         _muon_tensor(muon, out, "out", torch.float32, n, dev)
     if _nothing_to_compute(out):
@@ -459,11 +461,11 @@ def tpconv_muon_step(muon: Muon, W, grad, momentum, lr: float, beta: float = 0.9
     _muon_tensor(muon, momentum, "momentum", torch.float32, n, dev)
     dense = n == muon.dense
     if W_out is None:
-        W_out = _new(W.shape, torch.float32, dev, stream, W) if dense else _filled(W.clone, stream)
+        W_out = _new(W.shape, torch.float32, dev, stream, W) if dense else _on(stream, dev, W.clone)
     else:
         _muon_tensor(muon, W_out, "W_out", torch.float32, n, dev)
     if momentum_out is None:
-        momentum_out = _new(W.shape, torch.float32, dev, stream, momentum) if dense else _filled(momentum.clone, stream)
+        momentum_out = _new(W.shape, torch.float32, dev, stream, momentum) if dense else _on(stream, dev, momentum.clone)
     else:
         _muon_tensor(muon, momentum_out, "momentum_out", torch.float32, n, dev)
     if W_bf16 is not None:

@@ -103,3 +103,27 @@ def test_gradients_of_empty_tensors(ly):
     assert gx is None and gW.shape == (2, 0)
     u = torch.zeros(0, 4, 4, device=dev)
     assert ly.tpconv_muon_orthogonalize(ly.Muon([(4, 4, 0)]), u).shape == (0, 4, 4)
+
+
+def test_results_on_another_stream_have_memory_of_their_own(ly):
+    """A block that the current stream has just given back is not handed to a call on another stream."""
+    import torch
+
+    say("[case] results of calls on a side stream")
+    side = torch.cuda.Stream()
+    norm, lin = ly.Norm("40x0e+8x1o"), ly.Linear("40x0e+8x1o", "40x0e+8x1o", 2)
+    x = torch.randn(50000, 64, device="cuda")
+    W = torch.randn(lin.w_shape, device="cuda")
+    groups = ly.tpconv_linear_groups(lin, torch.zeros(50000, dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    want = ly.tpconv_norm_forward(norm, x), ly.tpconv_linear_forward(lin, groups, x, W)
+    torch.cuda.synchronize()
+    for call, ref in ((lambda: ly.tpconv_norm_forward(norm, x, stream=side), want[0]),
+                      (lambda: ly.tpconv_linear_forward(lin, groups, x, W, stream=side), want[1])):
+        given_back = torch.empty_like(x)
+        address = given_back.data_ptr()
+        del given_back
+        y = call()
+        assert y.data_ptr() != address and torch.empty_like(x).data_ptr() == address
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(y, ref)

@@ -70,3 +70,53 @@ def test_workspace_size_while_another_thread_asks_the_same_handle(make):
     finally:
         sys.settrace(before)
     assert got == alone and again == alone and next(others) > 1100
+
+
+def test_memory_of_a_call_on_another_stream_comes_from_that_streams_pool(calls, monkeypatch):
+    """A block of the current stream's pool may still be in use by that stream's pending work, which the other stream
+    does not wait for; and a result must outlive its use on the current stream."""
+    import contextlib
+
+    side, pool, made, kept = object(), [None], [], []
+
+    @contextlib.contextmanager
+    def on(stream):
+        pool.append(stream)
+        try:
+            yield
+        finally:
+            pool.pop()
+
+    def noting(fn):
+        def make(*args, **kwargs):
+            t = fn(*args, **kwargs)
+            made.append((t.data_ptr(), pool[-1]))
+            return t
+        return make
+
+    for name in ("empty", "empty_like", "zeros_like"):
+        monkeypatch.setattr(torch, name, noting(getattr(torch, name)))
+    monkeypatch.setattr(torch.Tensor, "clone", noting(torch.Tensor.clone))
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: kept.append((t.data_ptr(), s)))
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: "current")
+    norm, lin = ly.Norm("8x0e+8x1o"), ly.Linear("8x0e+8x1o", "4x0e+4x1o", 2)
+    muon, gaps = ly.Muon([(160, 8), (4, 300, 2, 2000)]), ly.Muon([(4, 4, 1, 3)])
+    x, W, w, b = torch.ones(5, 32), torch.ones(lin.w_shape), torch.ones(3320 + 1280), torch.ones(40)
+
+    def results(stream):
+        groups = ly.tpconv_linear_groups(lin, torch.zeros(5, dtype=torch.int32), stream=stream)
+        y = ly.tpconv_linear_forward(lin, groups, x, W, stream=stream)
+        return [groups.offsets, groups.order, y, ly.tpconv_norm_forward(norm, x, stream=stream),
+                *ly.tpconv_norm_backward(norm, x, None, x, stream=stream),
+                *ly.tpconv_linear_backward(lin, groups, x, W, y, stream=stream),
+                ly.tpconv_muon_orthogonalize(muon, w, stream=stream), ly.tpconv_muon_orthogonalize(gaps, b, stream=stream),
+                *ly.tpconv_muon_step(muon, w, w, w, 0.1, stream=stream), *ly.tpconv_muon_step(gaps, b, b, b, 0.1, stream=stream)]
+
+    outs = results(side)
+    assert len(made) > len(outs)  # workspaces too
+    assert all(where is side for _, where in made)
+    assert {t.data_ptr() for t in outs} <= {p for p, s in kept if s == "current"}
+    made.clear(), kept.clear()
+    results(None)
+    assert made and all(where is None for _, where in made) and not kept
