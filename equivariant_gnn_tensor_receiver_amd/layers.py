@@ -407,9 +407,12 @@ class Muon(_Handle):
             rows, cols, count, offset, stride = (*b, *(1, 0, b[0] * b[1])[len(b) - 2:])
             full.append(MatrixBlock(rows, cols, count, offset, stride))
         arr = (MatrixBlock * max(1, len(full)))(*full)
+        steps = [tuple(s) for s in steps]
+        if any(len(s) != 3 for s in steps):
+            raise ValueError(f"steps: {steps}, expected (a, b, c) of every step")
         flat = [float(v) for s in steps for v in s]
         co = (c_float * max(1, len(flat)))(*flat)
-        desc = MuonDesc(len(full), arr, len(flat) // 3, co, eps)
+        desc = MuonDesc(len(full), arr, len(steps), co, eps)
         tp._check(L.tpconv_muon_create(ctypes.byref(h), ctypes.byref(desc)), "tpconv_muon_create")
         self.handle = h
         #: elements a weight tensor must have at least

@@ -120,3 +120,11 @@ def test_memory_of_a_call_on_another_stream_comes_from_that_streams_pool(calls, 
     made.clear(), kept.clear()
     results(None)
     assert made and all(where is None for _, where in made) and not kept
+
+
+def test_steps_that_are_not_triples_are_refused():
+    """Their numbers would be read on as the coefficients of other steps."""
+    for steps in ([(1.5, -0.5)] * 3, [(1.0, 2.0, 3.0, 4.0)] * 3, [(1.0, 0.0, 0.0), (1.0, 0.0)], [()]):
+        with pytest.raises(ValueError, match="steps"):
+            ly.Muon([(4, 4)], steps)
+    assert ly.Muon([(4, 4)], iter([(1.5, -0.5, 0.0)] * 2)).numel == 16
