@@ -80,8 +80,9 @@ tpconv_status tpconv_norm_backward(tpconv_norm norm, int64_t num_nodes, const vo
  * (an output irrep without such an input is zero).  W is [num_groups][w_numel],
  * per group the blocks [mul_i][mul_o] in the order of i, then o (at most 64
  * blocks and 2^31 - 1 weights per group, or UNSUPPORTED).
- * Products of fp32 operands are exact to fp32: each operand is the sum of three
- * bf16 values and the six products that matter are added in fp32.  A value
+ * A product of fp32 operands is within 2^-21 of its value, towards zero: each
+ * operand is exactly the sum of three bf16 values, of whose nine products the six
+ * largest are added in fp32 (fp32 x bf16: all three; bf16 x bf16: exact).  A value
  * that is not finite makes the results that it takes part in not finite. */
 typedef struct tpconv_linear_s* tpconv_linear;
 
@@ -188,7 +189,8 @@ typedef struct {
 
 /* m' = beta m + (1 - beta) grad;  W' = (1 - lr weight_decay) W - lr s X(u),
  * s = sqrt(max(1, cols / rows)): rows are the inputs of W, cols its outputs.
- * All fp32; W_out may be W and momentum_out may be momentum (in place).
+ * All tensors are fp32, the operands of the products within X(u) sums of two
+ * fp16 values (22 bits).  W_out may be W and momentum_out may be momentum (in place).
  * W_bf16: NULL, or the new weights rounded to bf16 as well, in the same layout
  * (what a forward with bf16 weights reads). */
 tpconv_status tpconv_muon_step(tpconv_muon muon, const tpconv_muon_step_args* args, const float* W,

@@ -127,3 +127,33 @@ def test_results_on_another_stream_have_memory_of_their_own(ly):
         assert y.data_ptr() != address and torch.empty_like(x).data_ptr() == address
         torch.cuda.current_stream().wait_stream(side)
         assert torch.equal(y, ref)
+
+
+def test_linear_products_within_their_bound(ly):
+    """Single products of fp32 operands whose three pieces are all as large as they can be (the products left out come
+    to 1.96 * 2^-22 of the term), as small as they can be, and at the end of the range: 2^-21, and six roundings."""
+    import torch
+
+    say("[case] linear: single products of the worst bit patterns")
+    bits = [0x3F80FFFF, 0xBF80FFFF, 0x3FFFFFFF, 0x3F800000, 0x3F810001, 0x3F80FF01, 0x7F7FFFFF, 0x5F80FFFF, 0x2080FFFF]
+    v = np.array(bits, dtype=np.uint32).view(np.float32)
+    w = np.array([0x3F80FFFF, 0xBFFFFFFF, 0x3F808080, 0x3F000001], dtype=np.uint32).view(np.float32)
+    lin = ly.Linear("1x0e", "1x0e")
+    x = torch.from_numpy(v.copy()).cuda().view(-1, 1)
+    for one in w:
+        W = torch.full(lin.w_shape, float(one), device="cuda")
+        y = ly.tpconv_linear_forward(lin, ly.Groups(len(v)), x, W)
+        gx, _ = ly.tpconv_linear_backward(lin, ly.Groups(len(v)), x, W, x, want=("x",))
+        ref = v.astype(np.float64) * np.float64(one)
+        fits = np.abs(ref) < 3.4e38
+        for got in (y, gx):
+            assert np.all(np.abs(f64(got)[:, 0] - ref)[fits] <= (2.0 ** -21 + 6 * U) * np.abs(ref)[fits])
+    # bf16 x fp32: every product of the pieces is kept
+    half = ly.Linear("1x0e", "1x0e", 1, ly.TPCONV_BF16)
+    xb = x.bfloat16()
+    keep = torch.isfinite(xb[:, 0]).cpu().numpy()
+    for one in w:
+        y = ly.tpconv_linear_forward(half, ly.Groups(len(v)), xb, torch.full(half.w_shape, float(one), device="cuda"))
+        ref = f64(xb)[:, 0] * np.float64(one)
+        keep &= np.abs(ref) < 3.4e38
+        assert np.all(np.abs(f64(y)[:, 0] - ref)[keep] <= 3 * U * np.abs(ref)[keep])
