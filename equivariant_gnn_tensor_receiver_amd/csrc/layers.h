@@ -95,7 +95,7 @@ struct LinGwJob {
   int32_t woff;         // weight block within a group's weights: also its first element of the reduction launch
   int32_t by_row;       // slots numbered by their first row (fewer rows than groups)
   int32_t first_tile;   // first block of the job
-  int64_t part_off;     // [slots][mi][mo] partial sums
+  int64_t part_off;     // [places][mi][mo] partial sums of the groups of several slots
 };
 struct LinGwArgs {
   int32_t njobs, G, x_bf16;

@@ -37,6 +37,7 @@
 #include "layers.h"
 #include "timing.h"
 
+#include <algorithm>
 #include <type_traits>
 
 namespace tpconv {
@@ -107,6 +108,15 @@ __device__ __forceinline__ bool find_slot(const int32_t* offsets, int G, int64_t
   }
   s.row0 = (t - (((o0 * n) >> shift) + s.g)) << shift;
   return s.row0 < s.rows;
+}
+
+// The weight gradient's partial sums of a group that starts at `row0` of `rows`.  Only groups of several
+// slots have any, that is of r > M = 1 << shift rows: ceil(r / M) of them, and floor(2 r / M) is at least as
+// many, so with fewer whole slots than groups floor(2 row0 / M) is a free place to start; else the slot's
+// own number is.  (1024 x 2048 weights of 64 groups: 8 MiB for 100 nodes; a place for every slot took 0.5 GiB.)
+__host__ __device__ inline int64_t first_part(int64_t rows, int64_t row0, int g, int G, int shift) {
+  const bool half = (rows >> shift) < G;
+  return (row0 << half >> shift) + (half ? 0 : g);
 }
 
 // The job of a block: the last one whose first tile is at or before it, one lane per job.
@@ -663,7 +673,10 @@ __device__ __forceinline__ void lin_gw(const LinGwArgs& a, int64_t tile, char* s
   constexpr int kCols = S::KS > 1 ? 1 : BN / S::WN;
   const int mw = (wave / kCols) * S::WM, nw = (wave % kCols) * S::WN;
   const bool whole = s.rows <= (int64_t(1) << a.rshift);
-  float* dst = whole ? a.gW + s.g * a.w_per_group + J.woff : a.part + J.part_off + slot * ((int64_t)J.mi * J.mo);
+  float* dst = a.gW + s.g * a.w_per_group + J.woff;
+  if (!whole)
+    dst = a.part + J.part_off + (first_part(a.N * J.n, s.node0 * J.n, s.g, a.G, a.rshift) + (s.row0 >> a.rshift)) *
+                                    ((int64_t)J.mi * J.mo);
 #pragma unroll
   for (int i = 0; i < S::MT; ++i)
 #pragma unroll
@@ -714,8 +727,9 @@ __global__ __launch_bounds__(kThreads) void lin_gw_reduce_kernel(const LinGwArgs
     const int64_t slots = ((o1 - o0) * J.n + (int64_t(1) << a.rshift) - 1) >> a.rshift;
     if (slots == 1) continue;
     const int64_t size = (int64_t)J.mi * J.mo;
-    const float* p = a.part + J.part_off + (J.by_row ? o0 * J.n : ((o0 * J.n) >> a.rshift) + g) * size;
-    const int64_t next = J.by_row ? size << a.rshift : size;
+    const float* p = a.part + J.part_off + first_part(a.N * J.n, o0 * J.n, g, a.G, a.rshift) * size;
+    int64_t next = size;
+    asm("" : "+s"(next));  // a value of its own: the compiler makes slower loads of a known product (8.8 us against 10.9)
     float* dst = a.gW + g * a.w_per_group + J.woff;
     const int64_t e1 = min(last - J.woff, size);
     for (int64_t e = max(first - J.woff, int64_t(0)) + threadIdx.x; e < e1; e += kThreads) {
@@ -1025,7 +1039,8 @@ int64_t lin_gw_plan(LinGwArgs& a) {
     J.first_tile = (int32_t)(a.tiles < INT32_MAX ? a.tiles : INT32_MAX);  // (the launch refuses more)
     a.tiles += slots * tiles(J);
     J.part_off = part;
-    part += slots * J.mi * J.mo;
+    // (one place at least, so that a missing workspace is always noticed)
+    part += std::max<int64_t>(1, first_part(a.N * J.n, a.N * J.n, a.G, a.G, shift)) * J.mi * J.mo;
   }
   return part;
 }

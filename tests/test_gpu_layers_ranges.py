@@ -147,7 +147,7 @@ def test_linear_products_within_their_bound(ly):
         ref = v.astype(np.float64) * np.float64(one)
         fits = np.abs(ref) < 3.4e38
         for got in (y, gx):
-            assert np.all(np.abs(f64(got)[:, 0] - ref)[fits] <= (2.0 ** -21 + 6 * U) * np.abs(ref)[fits])
+            assert np.all(np.abs(f64(got)[fits, 0] - ref[fits]) <= (2.0 ** -21 + 6 * U) * np.abs(ref[fits]))
     # bf16 x fp32: every product of the pieces is kept
     half = ly.Linear("1x0e", "1x0e", 1, ly.TPCONV_BF16)
     xb = x.bfloat16()
@@ -155,5 +155,28 @@ def test_linear_products_within_their_bound(ly):
     for one in w:
         y = ly.tpconv_linear_forward(half, ly.Groups(len(v)), xb, torch.full(half.w_shape, float(one), device="cuda"))
         ref = f64(xb)[:, 0] * np.float64(one)
-        keep &= np.abs(ref) < 3.4e38
-        assert np.all(np.abs(f64(y)[:, 0] - ref)[keep] <= 3 * U * np.abs(ref)[keep])
+        keep = keep & (np.abs(ref) < 3.4e38)
+        assert np.all(np.abs(f64(y)[keep, 0] - ref[keep]) <= 3 * U * np.abs(ref[keep]))
+
+
+@pytest.mark.parametrize("sizes", [[128, 129, 127, 0, 256, 257, 0, 1] + [0] * 40, [0] * 300 + [130], [129] * 9, [5000, 0, 1],
+                                   [64] * 100 + [500] + [3] * 50, [128] * 4, [1] * 70])
+def test_weight_gradient_partial_sums_stay_in_their_workspace(ly, sizes):
+    """Groups of one slot and of several, with many groups and few: a workspace of exactly the size asked for."""
+    import torch
+    from test_gpu_layers_shapes import grouped
+
+    ii, oo, G, N = "9x0e+5x1o", "7x0e+6x1o", len(sizes), sum(sizes)
+    say(f"[case] linear weight gradient of {N} nodes in {G} groups, the largest of {max(sizes)}")
+    lin, rng = ly.Linear(ii, oo, G), np.random.default_rng(38)
+    group = rng.permutation(np.repeat(np.arange(G), sizes)).astype(np.int32)
+    x, W, g = (rng.standard_normal(s).astype(np.float32) for s in ((N, lin.feat_in), lin.w_shape, (N, lin.feat_out)))
+    groups = ly.tpconv_linear_groups(lin, torch.from_numpy(group).cuda())
+    size = lin.workspace_size(N)
+    memory = torch.full((size + 4096,), 77, dtype=torch.uint8, device="cuda")
+    gx, gW = ly.tpconv_linear_backward(lin, groups, cuda(x), cuda(W), cuda(g), workspace=memory[:size])
+    assert (memory[size:] == 77).all()
+    (_, rx, rW), (_, mx, mW) = (grouped(ii, oo, group, x, W, g, m) for m in (False, True))
+    near = lambda K: (6 * K / 16 + 16) * U + 2.0 ** -21
+    assert np.all(np.abs(f64(gx) - rx) <= near(13) * mx)
+    assert np.all(np.abs(f64(gW) - rW) <= near(3 * max(sizes)) * mW)

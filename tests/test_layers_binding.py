@@ -128,3 +128,17 @@ def test_steps_that_are_not_triples_are_refused():
         with pytest.raises(ValueError, match="steps"):
             ly.Muon([(4, 4)], steps)
     assert ly.Muon([(4, 4)], iter([(1.5, -0.5, 0.0)] * 2)).numel == 16
+
+
+def test_weight_gradient_workspace_holds_what_several_slots_need():
+    """Partial sums are for groups of more than 128 rows (one slot is written to the gradient itself): at most two per
+    128 rows, and never more than one per slot and group; one where there are none, so that a workspace is always asked
+    for."""
+    size = 1024 * 2048 * 4
+    for groups in (1, 2, 64, 4096):
+        lin = ly.Linear("1024x0e", "2048x0e", groups)
+        for n in (1, 4, 100, 128, 129, 1000, 5000):
+            places, left = divmod(lin.workspace_size(n), size)
+            # (slots of 128 rows or more)
+            assert left == 0 and 1 <= places <= max(1, min(2 * n // 128, n // 128 + groups)), (groups, n, places)
+    assert ly.Linear("8x0e", "8x1o", 3).workspace_size(100) == 0
