@@ -14,10 +14,14 @@
 // the nodes it takes, and the blocks' sums are added in a fixed order.
 //
 // Measured (kernel times; a plain copy of the sizes runs at 5.4 to 8.5 TB/s on
-// this chip): 32768 nodes of 288 fp32 values forward 14.4 us (5.2 TB/s),
-// backward 20.8 (5.5) and 4.3 for the sums of the parameters; 8192 rows of 4096
-// bf16 values forward 28.7 us (4.7 TB/s), backward 65.6 (fp32 gradients, 5.1)
-// and 4.9; 64 nodes of 32 values 3.1 us (a launch).
+// this chip): 32768 nodes of 288 fp32 values forward 14.2 us (5.3 TB/s),
+// backward 20.5 (5.5) and 4.1 for the sums of the parameters; 8192 rows of 4096
+// bf16 values forward 25 us (5.4 TB/s; 28.7 with other inputs in between),
+// backward 65.1 (fp32 gradients, 5.2) and 5.0; 64 nodes of 32 values 3.1 us (a
+// launch).
+//
+// Range: sums are plain fp32 sums, so a block whose sum of squares passes 3.4e38
+// has r = 0 (or NaN, once its plain sum does).
 #include "device_common.h"
 #include "layers.h"
 #include "timing.h"
@@ -484,7 +488,9 @@ __global__ __launch_bounds__(kThreads) void norm_backward_wide_kernel(const Norm
 }
 
 // ---- everything else (several rows of more than 256 channels, longer rows) -----------
-// A block of threads per (node, irrep) that reads the block again for each sum.
+// A block of threads per (node, irrep) that reads the block again for each sum
+// (4096 x 8193 fp32: forward 85 us, backward 511, where 8192 channels take 42 and
+// 93; 16384 nodes of 300x1o: 33 and 160).
 
 // Mean and 1 / deviation of one block of values, one thread block per (node, irrep).
 template <typename TX>

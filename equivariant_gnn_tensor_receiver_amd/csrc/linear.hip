@@ -30,9 +30,10 @@
 // together, so address setup, loads, splitting, products and stores follow one
 // another over the whole chip, and no single one of them is the limit (leaving
 // any one out saves 6 to 8 us).  8192 nodes of 1024x0e in bf16 to 2048x0e, 8
-// groups: forward 75 us (34 GFLOP, 460 TFLOP/s), both gradients 285 (69 GFLOP
-// x 3 products, 720 TFLOP/s; three waves per SIMD), bound by the splitting of
-// the fp32 gradients into pieces beside the products.
+// groups, on one set of inputs: forward 65 us (34 GFLOP, 525 TFLOP/s; one LDS
+// buffer and two barriers per chunk), both gradients 254 (69 GFLOP x 3
+// products, 810 TFLOP/s; three waves per SIMD), bound by the splitting of the
+// fp32 gradients into pieces beside the products.
 #include "device_common.h"
 #include "layers.h"
 #include "timing.h"
@@ -953,7 +954,8 @@ int64_t row_tiles(int64_t rows, int G, int shift, int32_t& by_row) {
 // launches of fewer blocks than CUs reach only their share: 1024 rows x 1024 x
 // 1024 in fp32 take 63 us in 64 blocks of 128 columns, 43.5 in 256 of 32; 2048
 // rows 64.5 in 128 blocks, 57.5 in 256 of 64; 4000 x 256 x 256 21.5 against
-// 13.9; 20000 nodes of 48x0e+48x1o 23.9 at 128, 14.9 at 64.
+// 13.9; 20000 nodes of 48x0e+48x1o 23.9 at 128, 14.9 at 64.  The groups' sizes
+// are not known here and take no part: tiles of small groups are partly empty.
 // 0: the 32 x 32 shape, its reduction split over the waves, below 64 blocks of
 // 128 x 128: 512 rows of 1024 channels 33.2 us against 36.9, 256 rows 19.8
 // against 36.9; at 1024 rows (64 blocks) it takes 47.4 against 43.5.
@@ -1056,8 +1058,9 @@ hipError_t launch_lin_backward(LinBackwardArgs& a, hipStream_t s) {
                        : width == 32 ? launch_backward_shapes<32>(a.gw.width, a, s)
                                      : launch_backward_shapes<0>(a.gw.width, a, s);
   if (e != hipSuccess || a.gw.njobs == 0) return e;
-  // (49152 x 16 elements over two slots each: 10.6 us with one per thread, 22 with eight;
-  // 2 M x 8 of groups with one slot: 25 us with one, 5.8 with eight)
+  // How many groups have one slot, and so nothing to do here, is known on the device only; the number of
+  // elements stands for it (49152 x 16 elements over two slots each: 10.6 us with one per thread, 22 with
+  // eight; 2 M x 8 of groups with one slot: 25 us with one, 5.8 with eight; nothing between was measured)
   const int run = a.gw.w_per_group * a.gw.G < (int64_t(1) << 22) ? 1 : 8;
   hipLaunchKernelGGL(lin_gw_reduce_kernel, dim3(blocks(a.gw.w_per_group, kThreads * run), (unsigned)a.gw.G), dim3(kThreads), 0, s,
                      a.gw, run);

@@ -18,15 +18,17 @@
 // block of threads; larger ones run one launch per product (norm, init, then
 // three per step), with X, X^T, A and B as hi and lo planes in the workspace.
 //
-// Measured (kernel times, five steps): 88 matrices of 32 x 32 9.0 us, 184 of
-// 64 x 64 17.8 and 176 of 128 x 128 47 (one block per CU, each a chain of 15
-// dependent products through LDS: bound by that latency, not by the matrix
-// cores, which see 11 GFLOP x 3 = 0.7 PFLOP/s at 128).  Two of 1024 x 2048:
-// X X^T 39 us (half of it: 13.7 GFLOP of fp16 products), A A 25, B X 40 (25.8
-// GFLOP, 0.65 PFLOP/s), the last B X with the update 55, init 19, norm 13.
+// Measured (traced kernels, five steps, one set of inputs): 88 matrices of 32 x
+// 32 9.0 us, 184 of 64 x 64 17.5 and 176 of 128 x 128 46 to 49 (40 a call in a
+// row of calls): one block per CU, each a chain of 15 dependent products through
+// LDS, bound by that latency and, at 64 and 128, by four LDS reads for three
+// products; the matrix cores see 11 GFLOP x 3 = 0.7 PFLOP/s at 128.  Two of 1024 x
+// 2048: X X^T 34 us (half of it: 13.7 GFLOP of fp16 products), A A 22, B X 36 (25.8
+// GFLOP, 0.72 PFLOP/s), the last B X with the update 44, init 18, norm 11.
 // There 272 blocks share 256 CUs in the r x r products: the doubled-up CUs set
 // the time (256 blocks of the same size take 60% of it); cutting the reduction
-// into equal parts instead gave 25 + 8 us (the join) and 18 + 8, no gain.
+// into equal parts instead gave 25 + 8 us (the join) and 18 + 8 where X X^T took
+// 39 and A A 25, no gain.
 #include "device_common.h"
 #include "layers.h"
 #include "timing.h"

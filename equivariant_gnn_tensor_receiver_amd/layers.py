@@ -23,7 +23,8 @@ EXPORTS = ("tpconv_norm_create", "tpconv_norm_destroy", "tpconv_norm_info", "tpc
            "tpconv_plan_weight_blocks", "tpconv_linear_weight_blocks", "tpconv_muon_orthogonalize",
            "tpconv_muon_step")
 
-#: Quintic coefficients (a, b, c) of one step that drives singular values in (0, 1] towards 1; five steps are usual.
+#: Quintic coefficients (a, b, c) of one step that drives singular values in (0, 1] towards 1, as published for the
+#: Muon optimiser (K. Jordan et al., 2024); five steps are usual.
 QUINTIC = (3.4445, -4.7750, 2.0315)
 
 
@@ -315,7 +316,8 @@ class Groups:
 
 
 def tpconv_linear_groups(linear: Linear, group, validate: bool = True, workspace=None, stream=None) -> Groups:
-    """The grouping of the nodes with group ids `group` (int32 [N], 0..num_groups-1), for all later calls."""
+    """The grouping of the nodes with group ids `group` (int32 [N], 0..num_groups-1), for all later calls.  validate: ids
+    outside the range raise (the call waits for the answer, so it cannot be captured); else such nodes are left out."""
     dev = _device(group, "group")
     n = group.numel()
     _need(group, "group", torch.int32, n, dev)

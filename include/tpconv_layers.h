@@ -39,7 +39,10 @@ extern "C" {
  * (means over the block's (2l+1) mul values; a mean or a bias on a block that
  * rotates or changes sign would break its equivariance).  w has one value per
  * channel of every irrep, b one per channel of every 0e irrep, in order.
- * A block of zeros gives b (0 without bias) and gradients scaled by 1/sqrt(eps). */
+ * A block of zeros gives b (0 without bias) and gradients scaled by 1/sqrt(eps).
+ * A block whose sum of squares passes 3.4e38 is out of range (z is zero or NaN).
+ * First derivatives only: neither the norm nor the linear layer has an entry
+ * point for the second. */
 typedef struct tpconv_norm_s* tpconv_norm;
 
 typedef struct {
