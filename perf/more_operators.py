@@ -1,0 +1,546 @@
+"""The operators of an attention block over the nodes of each graph of a batch, on their own: attention with a distance
+bias and capped scores, the embedding of node types with its gradient by sorted types, and dropout from a counter-based
+generator.
+
+Each case names an operator, its sizes and its direction.  ``run`` computes it in plain torch operations in 32 bits
+(``own = False``) or through the library's entry points (``own = True``); ``exact`` computes the same in 64 bits from
+the definition.  Features are [N][F]: per node the blocks [2l+1][mul] of the irreps string in order; a head takes an
+equal share of the channels of every row.
+"""
+import math
+import re
+
+import numpy as np
+import torch
+
+own = False
+
+
+def listed():
+    return [
+        # the smallest model's graph (64 nodes), one call: latency only
+        dict(name="attention_tiny_forward", op="attention", queries=64, keys=0, graphs=1, qk="8x0e+8x1o",
+             v="8x0e+8x1o", heads=4, x="f32", y="f32", cap=0.0, bias=True, mode="forward"),
+        # the molecular workload's nodes as a batch of small molecules, training on outputs and positions
+        dict(name="attention_molecules_train", op="attention", queries=4096, keys=0, graphs=128,
+             qk="32x0e+32x1o+32x2e", v="32x0e+32x1o+32x2e", heads=8, x="f32", y="f32", cap=0.0, bias=True,
+             mode="train"),
+        # the force workload's node features, graphs of some hundred nodes, training
+        dict(name="attention_force_train", op="attention", queries=8192, keys=0, graphs=16,
+             qk="128x0e+128x1o+128x2e", v="128x0e+128x1o+128x2e", heads=8, x="f32", y="f32", cap=0.0, bias=True,
+             mode="train"),
+        # wide scalar channels in bf16, a few long graphs of odd lengths, capped scores, training
+        dict(name="attention_scalars_bf16_train", op="attention", queries=8191, keys=0, graphs=4, qk="1024x0e",
+             v="1024x0e", heads=16, x="bf16", y="bf16", cap=30.0, bias=False, mode="train"),
+        # one large structure, every node with every other, forward
+        dict(name="attention_long_bf16_forward", op="attention", queries=16384, keys=0, graphs=1, qk="512x0e",
+             v="512x0e", heads=8, x="bf16", y="bf16", cap=0.0, bias=True, mode="forward"),
+        # a readout: one query per graph over all of its nodes, the read of keys and values is all there is
+        dict(name="attention_readout_forward", op="attention", queries=16, keys=32768, graphs=16,
+             qk="32x0e+32x1o+32x2e", v="32x0e+32x1o+32x2e", heads=4, x="f32", y="f32", cap=0.0, bias=False,
+             mode="forward"),
+        # the smallest model's nodes: a few chemical elements
+        dict(name="embed_tiny_train", op="embed", nodes=64, rows=10, features=8, w="f32", y="f32", mode="train"),
+        # the edge-scaling workload's nodes, most of the periodic table, some elements far more frequent
+        dict(name="embed_elements_train", op="embed", nodes=32768, rows=89, features=128, w="f32", y="f32",
+             mode="train"),
+        # a large vocabulary of fragments in bf16, most of its rows unused in a step
+        dict(name="embed_fragments_bf16_train", op="embed", nodes=16383, rows=32000, features=1024, w="bf16",
+             y="bf16", mode="train"),
+        # the smallest model's nodes
+        dict(name="dropout_tiny_forward", op="dropout", nodes=64, irreps="8x0e+8x1o", p=0.1, x="f32", y="f32",
+             mode="forward"),
+        # the edge-scaling workload's node features on a residual branch, training
+        dict(name="dropout_edge_train", op="dropout", nodes=32768, irreps="32x0e+32x1o+32x2e", p=0.1, x="f32",
+             y="f32", mode="train"),
+        # wide scalar channels kept in bf16 between layers, training
+        dict(name="dropout_scalars_bf16_train", op="dropout", nodes=8192, irreps="4096x0e", p=0.25, x="bf16",
+             y="bf16", mode="train"),
+    ]
+
+
+def _log(rng, lo, hi):
+    return min(hi, max(lo, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def _irreps_text(muls):
+    return "+".join("%dx%d%s" % (m, l, "eo"[l % 2]) for l, m in enumerate(muls))
+
+
+def _draw_heads(rng, heads):
+    """Irreps whose channels divide by the heads, 2 to 256 values per head."""
+    if rng.random() < 0.4:
+        return "%dx0e" % (heads * _log(rng, 4, 192))
+    lmax = rng.randint(1, 3)
+    per = _log(rng, 1, 256 // (lmax + 1) ** 2)
+    if rng.random() < 0.5 and per >= 4:
+        per -= per % 4
+    return _irreps_text([heads * (per if rng.random() < 0.7 else max(1, per // 2)) for _ in range(lmax + 1)])
+
+
+def draw(rng):
+    """A case of the ranges above; it costs no more than the largest listed case of its operator."""
+    op = rng.choice(("attention", "attention", "embed", "dropout"))
+    most = [work(c) for c in listed() if c["op"] == op]
+    while True:
+        x = rng.choice(("f32", "bf16"))
+        y = rng.choice(("f32", x))
+        mode = rng.choice(("forward", "train"))
+        if op == "attention":
+            heads = rng.choice((1, 2, 4, 8, 16))
+            n, qk = _log(rng, 2, 16384), _draw_heads(rng, heads)
+            graphs = _log(rng, 1, max(1, n // 8))
+            # most have the queries' own nodes as keys, some a few queries per graph
+            q, k = (n, 0) if rng.random() < 0.75 else (graphs * rng.randint(1, 4), n)
+            c = dict(op=op, queries=q, keys=k, graphs=graphs, qk=qk,
+                     v=qk if rng.random() < 0.6 else _draw_heads(rng, heads), heads=heads, x=x, y=y,
+                     cap=rng.choice((0.0, 0.0, 30.0)), bias=rng.random() < 0.6, mode=mode)
+        elif op == "embed":
+            c = dict(op=op, nodes=_log(rng, 1, 32768), rows=_log(rng, 2, 32000), features=_log(rng, 3, 2048), w=x,
+                     y=y, mode=mode)
+        else:
+            irreps = ("%dx0e" % _log(rng, 8, 4096) if rng.random() < 0.4 else
+                      _irreps_text([_log(rng, 2, 128) if rng.random() < 0.5 else 8 * rng.randint(1, 16)
+                                    for _ in range(rng.randint(1, 4))]))
+            c = dict(op=op, nodes=_log(rng, 1, 32768), irreps=irreps, p=rng.choice((0.05, 0.1, 0.25, 0.5)), x=x, y=y,
+                     mode=mode)
+        w = work(c)
+        if all(w[k] <= max(m[k] for m in most) for k in w):
+            return c
+
+
+def _irreps(text):
+    """[(mul, 2l+1, offset)], features per node."""
+    got, at = [], 0
+    for mul, l in re.findall(r"(\d+)x(\d+)[eo]", text):
+        n = 2 * int(l) + 1
+        got.append((int(mul), n, at))
+        at += int(mul) * n
+    return got, at
+
+
+def _lengths(case):
+    """Nodes of every graph, (of queries, of keys): between a third and about twice the mean; the same for all seeds, as
+    the shapes of a workload are."""
+    b, n = case["graphs"], case["keys"] or case["queries"]
+    share = np.array([0.35 + (0.61803398875 * (g + 1)) % 1.0 * 1.3 for g in range(b)])
+    edge = np.floor(np.cumsum(share) / share.sum() * n + 0.5).astype(int)
+    edge[-1] = n
+    k = np.diff(edge, prepend=0)
+    if not case["keys"]:
+        return k, k
+    return np.full(b, case["queries"] // b), k
+
+
+def work(case):
+    size = {"f32": 4, "bf16": 2}
+    train = case["mode"] == "train"
+    if case["op"] == "attention":
+        fq, fv, h = _irreps(case["qk"])[1], _irreps(case["v"])[1], case["heads"]
+        nq = case["queries"]
+        nk = case["keys"] or nq
+        lq, lk = _lengths(case)
+        pairs = float((lq.astype(float) * lk).sum())
+        moved = size[case["x"]] * (nq * fq + nk * (fq + fv)) + size[case["y"]] * nq * fv
+        moved += 12 * (nq + (nk if case["keys"] else 0)) if case["bias"] else 0
+        flops = 2.0 * pairs * (fq + fv)
+        if train:
+            moved += 4 * (nq * fv + nq * fq + nk * (fq + fv))
+            moved += 12 * (nq + (nk if case["keys"] else 0)) if case["bias"] else 0
+        return {"bytes": moved, "flops": flops * (3 if train else 1)}
+    if case["op"] == "embed":
+        n, f, r = case["nodes"], case["features"], case["rows"]
+        used = len(np.unique(_types_of(case, 0)))
+        moved = n * (4 + f * size[case["y"]]) + used * f * size[case["w"]]
+        return {"bytes": moved + (4 * f * (n + r) if train else 0), "flops": n * f * (2 if train else 1)}
+    n = case["nodes"] * _irreps(case["irreps"])[1]
+    return {"bytes": n * (size[case["x"]] + 2 * size[case["y"]] + (8 if train else 0)), "flops": n * (3 if train else 2)}
+
+
+_TYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def _randn(shape, seed, dtype="f32", scale=1.0):
+    g = torch.Generator("cuda").manual_seed(seed)
+    return (torch.randn(shape, generator=g, device="cuda") * scale).to(_TYPES[dtype])
+
+
+def _types_of(case, seed):
+    """Types of the nodes: the first ones far more frequent than the last, about one in a hundred nodes without any (-1,
+    the padding of a batch)."""
+    rng = np.random.default_rng(seed)
+    s = 1.0 / (np.arange(case["rows"]) + 4.0)
+    z = rng.choice(case["rows"], size=case["nodes"], p=s / s.sum())
+    z[rng.random(case["nodes"]) < 0.01] = -1
+    return z.astype(np.int32)
+
+
+def _inputs(case, seed):
+    """The tensors of a case, from the seed alone."""
+    train = case["mode"] == "train"
+    if case["op"] == "embed":
+        s = dict(index=torch.from_numpy(_types_of(case, seed)).cuda(),
+                 W=_randn((case["rows"], case["features"]), 11 * seed, case["w"], case["features"] ** -0.5))
+        if train:
+            s["grad"] = _randn((case["nodes"], case["features"]), 11 * seed + 1)
+        return s
+    if case["op"] == "dropout":
+        n, f = case["nodes"], _irreps(case["irreps"])[1]
+        s = dict(x=_randn((n, f), 11 * seed, case["x"]), residual=_randn((n, f), 11 * seed + 1, case["y"]),
+                 rng=torch.tensor([0x1234567890ABCDE + seed, 7 * seed + (1 << 33)], dtype=torch.int64, device="cuda"))
+        if train:
+            s["grad"] = _randn((n, f), 11 * seed + 2)
+        return s
+    fq, fv, nq = _irreps(case["qk"])[1], _irreps(case["v"])[1], case["queries"]
+    nk = case["keys"] or nq
+    lq, lk = _lengths(case)
+    # scores of a few units: what a norm in front of the projections and a scale of D^-1/2 give
+    s = dict(q=_randn((nq, fq), 11 * seed, case["x"], 1.3), k=_randn((nk, fq), 11 * seed + 1, case["x"], 1.3),
+             v=_randn((nk, fv), 11 * seed + 2, case["x"]))
+    if train:
+        s["grad"] = _randn((nq, fv), 11 * seed + 3)
+    if case["bias"]:
+        # about 20 cubic Angstrom per node, every structure in a cube of its own; slopes halve from head to head
+        def places(lengths, sd):
+            side = np.repeat((20.0 * np.maximum(lk, 1)) ** (1.0 / 3.0), lengths)
+            u = torch.rand((int(lengths.sum()), 3), generator=torch.Generator("cuda").manual_seed(sd), device="cuda")
+            return u * torch.from_numpy(side.astype(np.float32)).cuda()[:, None]
+
+        s["pos"] = places(lq, 11 * seed + 4)
+        if case["keys"]:
+            s["key_pos"] = places(lk, 11 * seed + 5)
+        s["slope"] = torch.tensor([2.0 ** (-8.0 * (h + 1) / case["heads"]) for h in range(case["heads"])],
+                                  device="cuda") * (1.0 + 0.05 * _randn((case["heads"],), 11 * seed + 6))
+    return s
+
+
+def _offsets(lengths):
+    return torch.from_numpy(np.concatenate([[0], np.cumsum(lengths)]).astype(np.int32)).cuda()
+
+
+def _padded(lengths):
+    """Node ids [graphs][longest] (the graph's first node behind its end)."""
+    first = np.cumsum(lengths) - lengths
+    j = np.arange(max(1, lengths.max()))
+    return np.where(j[None] < lengths[:, None], first[:, None] + j[None], np.minimum(first, lengths.sum() - 1)[:, None])
+
+
+def _chunks(case):
+    """What the plain form computes at a time, at most 2^27 scores: graphs padded to the longest, or rows of one graph."""
+    lq, lk = _lengths(case)
+    h, got, g = case["heads"], [], 0
+    while g < len(lk):
+        e = g + 1
+        while e < len(lk) and (e + 1 - g) * h * int(lq[g:e + 1].max()) * int(lk[g:e + 1].max()) <= 1 << 27:
+            e += 1
+        q, k = _padded(lq[g:e]) + lq[:g].sum(), _padded(lk[g:e]) + lk[:g].sum()
+        qm, km = (np.arange(q.shape[1])[None] < lq[g:e, None]), (np.arange(k.shape[1])[None] < lk[g:e, None])
+        step = q.shape[1] if e > g + 1 else max(1, min(q.shape[1], (1 << 27) // (h * max(1, k.shape[1]))))
+        for r in range(0, q.shape[1], step):
+            qs, ms = q[:, r:r + step], qm[:, r:r + step]
+            got.append(dict(q=qs, q_real=ms, q_at=qs[ms], q_row=np.flatnonzero(ms), k=k, k_real=km, k_at=k[km],
+                            k_row=np.flatnonzero(km)))
+        g = e
+    return [{n: torch.from_numpy(np.ascontiguousarray(t)).cuda() for n, t in c.items()} for c in got]
+
+
+def prepare(case, seed):
+    """Inputs and, as a user keeps them from call to call, the layer's handle, the batch's offsets and a workspace."""
+    s = dict(_inputs(case, seed), case=case)
+    if not own:
+        if case["op"] == "attention":
+            s["chunks"] = _chunks(case)
+        return s
+    from equivariant_gnn_tensor_receiver_amd import attention as at
+
+    code = {"f32": at.TPCONV_F32, "bf16": at.TPCONV_BF16}
+    if case["op"] == "embed":
+        s["layer"] = at.Embedding(case["rows"], case["features"], _embed_scale(case), code[case["w"]], code[case["y"]])
+        size = s["layer"].workspace_size(case["nodes"])
+    elif case["op"] == "dropout":
+        s["layer"] = at.Dropout(case["irreps"], case["p"], code[case["x"]], code[case["y"]])
+        size = 0
+    else:
+        lq, lk = _lengths(case)
+        s["layer"] = at.Attention(case["qk"], case["v"], case["heads"], _scale(case), case["cap"], code[case["x"]],
+                                  code[case["y"]])
+        s["batch"] = at.Batch(case["queries"], _offsets(lq), s.get("pos"),
+                              *((case["keys"], _offsets(lk), s.get("key_pos")) if case["keys"] else ()))
+        size = s["layer"].workspace_size(s["batch"], at.OP_BACKWARD if case["mode"] == "train" else at.OP_FORWARD)
+    s["workspace"] = torch.empty(max(1, size), dtype=torch.uint8, device="cuda")
+    return s
+
+
+def _run_own(s):
+    from equivariant_gnn_tensor_receiver_amd import attention as at
+
+    case, h, ws = s["case"], s["layer"], s["workspace"]
+    train = case["mode"] == "train"
+    if case["op"] == "embed":
+        y = at.tpconv_embed_forward(h, s["index"], s["W"])
+        return (y, at.tpconv_embed_backward(h, s["index"], s["grad"], workspace=ws)) if train else y
+    if case["op"] == "dropout":
+        y = at.tpconv_dropout_forward(h, s["x"], s["rng"], residual=s["residual"])
+        return (y, at.tpconv_dropout_backward(h, s["grad"], s["rng"])) if train else y
+    b, slope = s["batch"], s.get("slope")
+    if not train:
+        return at.tpconv_attention_forward(h, b, s["q"], s["k"], s["v"], slope=slope, workspace=ws)
+    saved = torch.empty(h.saved_size(case["queries"]), device="cuda")
+    out = at.tpconv_attention_forward(h, b, s["q"], s["k"], s["v"], slope=slope, saved=saved, workspace=ws)
+    want = ("q", "k", "v") + (("slope", "pos") if case["bias"] else ())
+    got = at.tpconv_attention_backward(h, b, s["q"], s["k"], s["v"], out, saved, s["grad"], slope=slope, want=want,
+                                       workspace=ws)
+    return (out, *(t for t in got if t is not None))
+
+
+def _scale(case):
+    return (_irreps(case["qk"])[1] // case["heads"]) ** -0.5
+
+
+def _embed_scale(case):
+    return case["features"] ** 0.5
+
+
+def _split(x, irreps, heads):
+    """[N][F] -> [N][heads][F / heads]"""
+    n = x.shape[0]
+    return torch.cat([x[:, at:at + m * r].view(n, r, heads, m // heads).transpose(1, 2).reshape(n, heads, -1)
+                      for m, r, at in _irreps(irreps)[0]], 2)
+
+
+def _join(x, irreps, heads):
+    n, at, got = x.shape[0], 0, []
+    for m, r, _ in _irreps(irreps)[0]:
+        w = r * m // heads
+        got.append(x[:, :, at:at + w].reshape(n, heads, r, m // heads).transpose(1, 2).reshape(n, r * m))
+        at += w
+    return torch.cat(got, 1)
+
+
+def _run_attention(s):
+    case, h = s["case"], s["case"]["heads"]
+    train, cap = case["mode"] == "train", case["cap"]
+    q, k, v = (_split(s[n].float(), case["v" if n == "v" else "qk"], h) for n in "qkv")
+    out = torch.zeros(q.shape[0], h, v.shape[2], device="cuda")
+    if train:
+        do = _split(s["grad"], case["v"], h)
+        gq, gk, gv = torch.zeros_like(q), torch.zeros_like(k), torch.zeros_like(v)
+    if case["bias"]:
+        pos, slope = s["pos"], s["slope"][None, :, None, None]
+        key_pos = s.get("key_pos", pos)
+        gslope, gpos = torch.zeros(h, device="cuda"), torch.zeros_like(pos)
+        gkey = torch.zeros_like(key_pos) if case["keys"] else gpos
+
+    def pad(x, rows):  # [graphs, heads, rows, width]
+        return x[rows.reshape(-1)].view(*rows.shape, h, -1).transpose(1, 2).contiguous()
+
+    def rows_of(x, rows):  # the real rows, [rows][heads][width]
+        return x.transpose(1, 2).reshape(-1, h, x.shape[3])[rows]
+
+    for c in s["chunks"]:
+        kp, vp, qp = pad(k, c["k"]), pad(v, c["k"]), pad(q, c["q"])
+        t = torch.matmul(qp, kp.transpose(2, 3)) * _scale(case)
+        if cap:
+            th = torch.tanh(t / cap)
+            t = th * cap
+        if case["bias"]:
+            diff = pos[c["q"]][:, :, None] - key_pos[c["k"]][:, None]
+            d = torch.sqrt((diff * diff).sum(3))
+            t = t - slope * d[:, None]
+        t = torch.where(c["k_real"][:, None, None, :], t, -math.inf)
+        t = t - t.amax(3, keepdim=True).clamp_min(-3e38)
+        p = torch.exp(t)
+        total = p.sum(3, keepdim=True)
+        p = p / torch.where(total > 0, total, 1.0)
+        o = torch.matmul(p, vp)
+        out.index_copy_(0, c["q_at"], rows_of(o, c["q_row"]))
+        if not train:
+            continue
+        g = pad(do, c["q"]) * c["q_real"][:, None, :, None]
+        gv.index_add_(0, c["k_at"], rows_of(torch.matmul(p.transpose(2, 3), g), c["k_row"]))
+        ds = p * (torch.matmul(g, vp.transpose(2, 3)) - (g * o).sum(3, keepdim=True))
+        if case["bias"]:
+            gslope -= (ds * d[:, None]).sum((0, 2, 3))
+            pull = -(ds * slope).sum(1) / torch.where(d > 0, d, 1.0)  # diff is 0 where d is
+            gpos.index_add_(0, c["q_at"], (pull[..., None] * diff).sum(2).view(-1, 3)[c["q_row"]])
+            gkey.index_add_(0, c["k_at"], -(pull[..., None] * diff).sum(1).view(-1, 3)[c["k_row"]])
+        if cap:
+            ds = ds * (1.0 - th * th)
+        ds = ds * _scale(case)
+        gq.index_copy_(0, c["q_at"], rows_of(torch.matmul(ds, kp), c["q_row"]))
+        gk.index_add_(0, c["k_at"], rows_of(torch.matmul(ds.transpose(2, 3), qp), c["k_row"]))
+    y = _join(out, case["v"], h).to(_TYPES[case["y"]])
+    if not train:
+        return y
+    got = (y, _join(gq, case["qk"], h), _join(gk, case["qk"], h), _join(gv, case["v"], h))
+    if case["bias"]:
+        got += (gslope, gpos) + ((gkey,) if case["keys"] else ())
+    return got
+
+
+def _run_embed(s):
+    case, z = s["case"], s["index"].long()
+    there = (z >= 0) & (z < case["rows"])
+    row = torch.where(there, z, 0)
+    y = torch.where(there[:, None], s["W"][row].float() * _embed_scale(case), 0.0).to(_TYPES[case["y"]])
+    if case["mode"] == "forward":
+        return y
+    g = torch.where(there[:, None], s["grad"] * _embed_scale(case), 0.0)
+    return y, torch.zeros(case["rows"], case["features"], device="cuda").index_add_(0, row, g)
+
+
+_LOW = 0xFFFFFFFF
+
+
+def _philox(b, seed, offset):
+    """Ten rounds of Philox 4x32 (Salmon et al., 2011) on 64-bit counters b (low words), as [len(b)][4] words."""
+    c = [b & _LOW, (b >> 32) & _LOW, (offset & _LOW).expand_as(b), ((offset >> 32) & _LOW).expand_as(b)]
+    k0, k1 = seed & _LOW, (seed >> 32) & _LOW
+    for _ in range(10):
+        x, y = c[0] * 0xD2511F53, c[2] * 0xCD9E8D57
+        c = [((y >> 32) & _LOW) ^ c[1] ^ k0, y & _LOW, ((x >> 32) & _LOW) ^ c[3] ^ k1, x & _LOW]
+        k0, k1 = (k0 + 0x9E3779B9) & _LOW, (k1 + 0xBB67AE85) & _LOW
+    return torch.stack(c, 1)
+
+
+def _factors(case, rng):
+    """The factor of every value of a node tensor: 0, or the inverse of the share that is kept."""
+    n, (blocks, _) = case["nodes"], _irreps(case["irreps"])
+    per = sum((m + 7) // 8 for m, _, _ in blocks)
+    words = _philox(torch.arange(n * per, device="cuda"), rng[0], rng[1])
+    words = torch.stack([words & 0xFFFF, words >> 16], 2).view(n, per * 8)  # 16 bits per channel
+    limit = round(case["p"] * 65536)
+    keep = torch.where(words >= limit, 65536.0 / (65536 - limit), 0.0)
+    got, at = [], 0
+    for m, r, _ in blocks:
+        got.append(keep[:, None, at:at + m].expand(n, r, m).reshape(n, -1))
+        at += (m + 7) // 8 * 8
+    return torch.cat(got, 1)
+
+
+def run(state):
+    if own:
+        return _run_own(state)
+    case = state["case"]
+    if case["op"] == "attention":
+        return _run_attention(state)
+    if case["op"] == "embed":
+        return _run_embed(state)
+    f = _factors(case, state["rng"])
+    y = (state["residual"].float() + state["x"].float() * f).to(_TYPES[case["y"]])
+    return (y, state["grad"] * _factors(case, state["rng"])) if case["mode"] == "train" else y
+
+
+def exact(case, seed):
+    s = {k: v.double() if v.is_floating_point() else v for k, v in _inputs(case, seed).items()}
+    if case["op"] == "attention":
+        return _exact_attention(case, s)
+    if case["op"] == "embed":
+        return _exact_embed(case, s)
+    return _exact_dropout(case, {k: v.cpu().numpy() for k, v in s.items()})
+
+
+def _exact_attention(case, s):
+    """Graph by graph and head by head, with the columns of a head gathered from the node tensors."""
+    heads = case["heads"]
+
+    def columns(irreps):
+        return [torch.tensor([at + r * m + h * (m // heads) + c for m, n, at in _irreps(irreps)[0] for r in range(n)
+                              for c in range(m // heads)], device="cuda") for h in range(heads)]
+
+    cq, cv, (lq, lk) = columns(case["qk"]), columns(case["v"]), _lengths(case)
+    train, nq = case["mode"] == "train", case["queries"]
+    y = torch.zeros(nq, s["v"].shape[1], dtype=torch.float64, device="cuda")
+    if train:
+        gq, gk, gv = torch.zeros_like(s["q"]), torch.zeros_like(s["k"]), torch.zeros_like(s["v"])
+    if case["bias"]:
+        key_pos = s["key_pos"] if case["keys"] else s["pos"]
+        gs, gp = torch.zeros_like(s["slope"]), torch.zeros_like(s["pos"])
+        gkp = torch.zeros_like(key_pos)
+    q1 = k1 = 0
+    for nqg, nkg in zip(lq, lk):
+        q0, k0 = q1, k1
+        q1, k1 = q0 + int(nqg), k0 + int(nkg)
+        if nqg == 0 or nkg == 0:
+            continue
+        if case["bias"]:
+            a, b = s["pos"][q0:q1], key_pos[k0:k1]
+            d = torch.sqrt(sum((a[:, i, None] - b[None, :, i]) ** 2 for i in range(3)))
+            over = torch.where(d > 0, 1.0 / d, 0.0)
+        for h in range(heads):
+            q, k, v = s["q"][q0:q1][:, cq[h]], s["k"][k0:k1][:, cq[h]], s["v"][k0:k1][:, cv[h]]
+            t = q @ k.T * _scale(case)
+            if case["cap"]:
+                t = case["cap"] * torch.tanh(t / case["cap"])
+            slope = 1.0
+            if case["cap"] and train:
+                slope = 1.0 - (t / case["cap"]) ** 2
+            if case["bias"]:
+                t = t - s["slope"][h] * d
+            lse = torch.logsumexp(t, 1, keepdim=True)
+            p = torch.exp(t - lse)
+            y[q0:q1, cv[h]] = p @ v
+            if not train:
+                continue
+            g = s["grad"][q0:q1][:, cv[h]]
+            gv[k0:k1, cv[h]] = p.T @ g
+            dp = g @ v.T
+            ds = p * (dp - (p * dp).sum(1, keepdim=True))
+            if case["bias"]:
+                gs[h] -= (ds * d).sum()
+                # sum_j w (a_i - b_j) = a_i sum_j w - sum_j w b_j
+                w = -s["slope"][h] * ds * over
+                gp[q0:q1] += a * w.sum(1, keepdim=True) - w @ b
+                gkp[k0:k1] += b * w.sum(0)[:, None] - w.T @ a
+            ds = ds * slope * _scale(case)
+            gq[q0:q1, cq[h]] = ds @ k
+            gk[k0:k1, cq[h]] = ds.T @ q
+    if not train:
+        return y
+    if not case["bias"]:
+        return y, gq, gk, gv
+    return (y, gq, gk, gv, gs, gp, gkp) if case["keys"] else (y, gq, gk, gv, gs, gp + gkp)
+
+
+def _exact_embed(case, s):
+    """As products with the matrix of ones that the types give, in the form of a sort and running sums."""
+    z = s["index"].cpu().numpy()
+    there = np.flatnonzero((z >= 0) & (z < case["rows"]))
+    y = torch.zeros(case["nodes"], case["features"], dtype=torch.float64, device="cuda")
+    rows = torch.from_numpy(there).cuda()
+    y[rows] = s["W"][torch.from_numpy(z[there].astype(np.int64)).cuda()] * math.sqrt(case["features"])
+    if case["mode"] == "forward":
+        return y
+    g = torch.zeros(case["rows"], case["features"], dtype=torch.float64, device="cuda")
+    order = there[np.argsort(z[there], kind="stable")]
+    kinds, first = np.unique(z[order], return_index=True)
+    if len(order):
+        ends = np.append(first[1:], len(order))
+        total = torch.cat([torch.zeros(1, case["features"], dtype=torch.float64, device="cuda"),
+                           s["grad"][torch.from_numpy(order).cuda()].cumsum(0)])
+        part = total[torch.from_numpy(ends).cuda()] - total[torch.from_numpy(first).cuda()]
+        g[torch.from_numpy(kinds.astype(np.int64)).cuda()] = part * math.sqrt(case["features"])
+    return y, g
+
+
+def _exact_dropout(case, s):
+    n, (blocks, f) = case["nodes"], _irreps(case["irreps"])
+    per = sum(-(-m // 8) for m, _, _ in blocks)
+    seed, offset = (int(v) % (1 << 64) for v in s["rng"])
+    low, half = np.uint64(0xFFFFFFFF), np.uint64(32)
+    b = np.arange(n * per, dtype=np.uint64)
+    x0, x1, x2, x3 = b & low, b >> half, np.uint64(offset) & low, np.uint64(offset) >> half
+    for r in range(10):
+        p, t = np.uint64(0xD2511F53) * x0, np.uint64(0xCD9E8D57) * x2
+        ka, kb = np.uint64((seed + r * 0x9E3779B9) % (1 << 32)), np.uint64(((seed >> 32) + r * 0xBB67AE85) % (1 << 32))
+        x0, x1, x2, x3 = (t >> half) ^ x1 ^ ka, t & low, (p >> half) ^ x3 ^ kb, p & low
+    bits = np.stack([x0, x1, x2, x3], 1).astype("<u4").view("<u2").reshape(n, per * 8)
+    limit = round(case["p"] * 65536)
+    factor, at = np.empty((n, f), dtype=np.float32), 0
+    for m, r, off in blocks:
+        keep = (bits[:, at:at + m] >= limit).astype(np.float32)
+        factor[:, off:off + m * r] = np.tile(keep, (1, r))
+        at += -(-m // 8) * 8
+    scale = 65536.0 / (65536 - limit)
+    y = s["residual"] + s["x"] * factor * scale
+    return (y, s["grad"] * factor * scale) if case["mode"] == "train" else y
