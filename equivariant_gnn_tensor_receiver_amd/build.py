@@ -41,6 +41,8 @@ POS_VARIANTS = [("bpos_f32", "float", 0), ("bpos_bf16", "uint16_t", 0), ("hess_f
 # The edge streams keep their matrix-core accumulators in ordinary VGPRs
 # (the accumulation registers would otherwise be copied back and forth).
 STREAM_FLAGS = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
+# Values per head of the attention kernels' width classes (attention_join.hip lists the same)
+ATTENTION_WIDTHS = (32, 64, 96, 128, 160, 256)
 UNITS = ([(f"stream_{n}", "stream_gf.hip", STREAM_FLAGS + [f"-DTP_MODE={m}", f"-DTP_LO={lo}",
                                                           f"-DTP_LAUNCHER=launch_stream_{n}"])
           for n, m, lo in STREAM_VARIANTS]
@@ -51,7 +53,9 @@ UNITS = ([(f"stream_{n}", "stream_gf.hip", STREAM_FLAGS + [f"-DTP_MODE={m}", f"-
                                              ("scratch", ".hip"), ("ragged", ".hip"), ("api", ".cpp"),
                                              ("stream_dispatch", ".cpp"), ("plan", ".cpp"),
                                              ("timing", ".cpp"), ("layer_norm", ".hip"), ("linear", ".hip"),
-                                             ("muon", ".hip"), ("layers", ".cpp"))])
+                                             ("muon", ".hip"), ("layers", ".cpp"), ("embedding", ".hip"),
+                                             ("dropout", ".hip"), ("attention_join", ".hip"), ("attention", ".cpp"))]
+         + [(f"attention_{dc}", "attention_class.hip", [f"-DTP_DC={dc}"]) for dc in ATTENTION_WIDTHS])
 
 
 def run(cmd):

@@ -5,13 +5,14 @@
 
 namespace tpconv {
 
-// Kernel classes; the numbering matches tpconv_kernel in include/tpconv.h and
-// tpconv_layer_kernel in include/tpconv_layers.h.
+// Kernel classes; the numbering matches tpconv_kernel in include/tpconv.h,
+// tpconv_layer_kernel in include/tpconv_layers.h and tpconv_attention_kernel in
+// include/tpconv_attention.h.
 enum KernelClass : int {
   kcStreamFwd = 0, kcStreamJvp, kcStreamSnd, kcStreamSndT, kcStreamBwdPos,
   kcGemmOut, kcGemmGs, kcGemmGx, kcGemmGw, kcGwReduce, kcFill, kcGraph,
   kcCwContract, kcCwGw, kcCwReduce, kcStreamHess, kcStateDot,
-  kcNorm, kcLinear, kcMuon, kcCount
+  kcNorm, kcLinear, kcMuon, kcAttention, kcEmbed, kcDropout, kcCount
 };
 
 // While timing is enabled, brackets the launches issued in its lifetime with

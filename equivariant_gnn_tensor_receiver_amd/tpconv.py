@@ -31,7 +31,7 @@ EXPORTS = ("tpconv_plan_create", "tpconv_plan_destroy", "tpconv_plan_info", "tpc
            "tpconv_plan_features", "tpconv_forward_mlp", "tpconv_backward_mlp", "tpconv_double_backward_mlp")
 KERNELS = ("stream_fwd", "stream_jvp", "stream_snd", "stream_sndt", "stream_bwdpos", "gemm_out", "gemm_gs",
            "gemm_gx", "gemm_gw", "gw_reduce", "fill", "graph", "cw_contract", "cw_gw", "cw_reduce", "stream_hess",
-           "state_dot", "norm", "linear", "muon")
+           "state_dot", "norm", "linear", "muon", "attention", "embed", "dropout")
 
 
 class TpconvError(RuntimeError):

@@ -335,7 +335,7 @@ typedef enum {
   TPCONV_KERNEL_CW_REDUCE = 14,    /* channel-wise: ordered sum of the partials */
   TPCONV_KERNEL_STREAM_HESS = 15,  /* receiver stream: position derivative of the force loss */
   TPCONV_KERNEL_STATE_DOT = 16,    /* per-k dot products of two states (radial MLP weight gradient) */
-  TPCONV_KERNEL_COUNT = 20         /* 17..19: tpconv_layers.h */
+  TPCONV_KERNEL_COUNT = 23         /* 17..19: tpconv_layers.h, 20..22: tpconv_attention.h */
 } tpconv_kernel;
 
 /* Diagnostics for roofline measurements (not needed for computing).

@@ -18,6 +18,7 @@ sh       real spherical harmonics (component normalised) and their Jacobian
 radial   Bessel radial basis with the p=6 polynomial envelope, and R'(d)
 tpconv   forward / backward / double backward, materialising schedule
 layers   layer norm over irreps, grouped linear layer, orthogonalised update
+attention  attention among the nodes of each graph, embedding of node types, dropout
 
 Every function is pinned by ``tests/test_oracle_*.py`` against closed forms,
 library routines (sympy CG, scipy spherical harmonics, scipy quadrature),

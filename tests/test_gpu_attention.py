@@ -1,0 +1,476 @@
+"""GPU parity of the attention block's operators with their fp64 definitions.
+
+Tolerances, fixed before the first run (u = 2^-24, the rounding of fp32; A(t) the sum of the magnitudes of a result's
+terms, from the definition):
+  scores:     six products of pieces per 16 reductions are added in fp32 and 2^-21 is left out: per score
+              ((6 D / 16 + 16) u + 2^-21) A(s); 16 u |s| more for the scale, the cap and the distance.  E is the largest
+              of a case, so a weight exp(s - lse) is off by 2 E + 16 u relative to itself.
+  out:        weights, sums over L keys and the products' pieces: w = 2 E + 16 u + (6 L / 16 + 16) u + 2^-21 of A(out); weights
+              of two pieces 2^-17 more; bf16 results half a unit in the last place of their 8-bit significand more.
+  gradients:  dS = P (dP - D) is off by e = 2 w + 2 ((6 D_v / 16 + 16) u + 2^-21) of its terms' magnitudes, capped scores
+              by 2 E / cap + 16 u more (the factor 1 - tanh^2); results e + (6 L / 16 + 16) u + 2^-21 of A, those of slopes
+              and positions, which are added one by one over all pairs of a query or key, e + 4 L u, and the slopes' then
+              over up to N / 32 blocks: N u more.
+  underflow:  weights, and pieces of them, below the smallest normal fp32 value 2^-126 are zero: each term of a sum is off by
+              at most 3 2^-126 (one per piece) times what it is multiplied by, which is |v| or |grad_out| for a weight and at
+              most 2 D_v max|grad_out| max|v| max|q or k| for dS: 8 L 2^-126 D_v M^3 with M the largest input, at least 1.
+  embedding:  one product per value (u, half a unit in the last place for bf16); gradient n u of the sum of magnitudes,
+              n the most nodes of a type.
+  dropout:    the factor 65536 / (65536 - t) is rounded, then a product and a sum: 3 u of the magnitudes, 2 u without a sum.
+"""
+import numpy as np
+import pytest
+
+from gpu_cases import say
+from oracle import attention as oa
+from oracle.layers import irreps
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def at():
+    from equivariant_gnn_tensor_receiver_amd import attention
+
+    return attention
+
+
+def cuda(a, bf16=False):
+    import torch
+
+    t = torch.from_numpy(np.ascontiguousarray(a, dtype=np.float32)).cuda()
+    return t.bfloat16() if bf16 else t
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def half_ulp(a):
+    """Half a unit in the last place of a's values in bf16 (8-bit significand)."""
+    a = np.abs(a)
+    return np.where(a > 0, 2.0 ** (np.floor(np.log2(np.where(a > 0, a, 1.0))) - 8), 0.0)
+
+
+def offsets(lens, first=0):
+    import torch
+
+    return torch.from_numpy(np.concatenate([[first], first + np.cumsum(lens)]).astype(np.int32)).cuda()
+
+
+def near(got, ref, tol, what):
+    got = f64(got)
+    bad = np.abs(got - ref) - tol
+    assert np.all(bad <= 0), f"{what}: off by {np.abs(got - ref).max():.3e}, allowed {np.asarray(tol).max():.3e}"
+
+
+class Case:
+    """Inputs of one case, what the GPU gets exact in its type, and its fp64 results."""
+
+    def __init__(self, qk, v, heads, lens, key_lens=None, xb=False, yb=False, cap=0.0, bias=False, seed=0, spread=1.0):
+        rng = np.random.default_rng(seed)
+        self.qk, self.vt, self.heads, self.lens, self.key_lens = qk, v, heads, lens, key_lens
+        self.xb, self.yb, self.cap, self.bias = xb, yb, cap, bias
+        self.nq, self.nk = sum(lens), sum(lens if key_lens is None else key_lens)
+        fq, fv = irreps(qk)[1], irreps(v)[1]
+        self.q, self.k = (cuda(spread * rng.standard_normal((n, fq)), xb) for n in (self.nq, self.nk))
+        self.v, self.g = cuda(rng.standard_normal((self.nk, fv)), xb), cuda(rng.standard_normal((self.nq, fv)))
+        self.pos = cuda(3 * rng.standard_normal((self.nq, 3))) if bias else None
+        self.key_pos = cuda(3 * rng.standard_normal((self.nk, 3))) if bias and key_lens is not None else None
+        self.slope = cuda(0.02 + rng.random(heads)) if bias else None
+        self.D, self.Dv = fq // heads, fv // heads
+        self.scale = self.D ** -0.5
+
+    def layer(self, at):
+        code = (at.TPCONV_F32, at.TPCONV_BF16)
+        return at.Attention(self.qk, self.vt, self.heads, self.scale, self.cap, code[self.xb], code[self.yb])
+
+    def batch(self, at):
+        cross = () if self.key_lens is None else (self.nk, offsets(self.key_lens), self.key_pos)
+        return at.Batch(self.nq, offsets(self.lens), self.pos, *cross)
+
+    def want(self):
+        return ("q", "k", "v") + (("slope", "pos") if self.bias else ())
+
+    def run(self, at, **kw):
+        import torch
+
+        h, b = self.layer(at), self.batch(at)
+        saved = torch.full((h.saved_size(self.nq),), float("nan"), device="cuda")
+        out = at.tpconv_attention_forward(h, b, self.q, self.k, self.v, slope=self.slope, saved=saved)
+        plain = at.tpconv_attention_forward(h, b, self.q, self.k, self.v, slope=self.slope)
+        grads = at.tpconv_attention_backward(h, b, self.q, self.k, self.v, out, saved, self.g, slope=self.slope,
+                                             want=self.want(), **kw)
+        torch.cuda.synchronize()
+        return out, plain, saved, grads
+
+    def check(self, at):
+        out, plain, saved, grads = self.run(at)
+        n = lambda t: None if t is None else f64(t)  # noqa: E731
+        off = np.concatenate([[0], np.cumsum(self.lens)])
+        ko = None if self.key_lens is None else np.concatenate([[0], np.cumsum(self.key_lens)])
+        q, k = n(self.q), n(self.k)
+        ref = oa.attention(self.qk, self.vt, self.heads, q, k, n(self.v), off, ko, self.scale, self.cap, n(self.slope),
+                           n(self.pos), n(self.key_pos), n(self.g))
+        E = 0.0
+        for g in range(len(self.lens)):
+            a, b = slice(off[g], off[g + 1]), slice(*(off if ko is None else ko)[g:g + 2])
+            if a.start == a.stop or b.start == b.stop:
+                continue
+            for h, c in enumerate(oa.head_columns(self.qk, self.heads)):
+                mag = self.scale * (np.abs(q[a][:, c]) @ np.abs(k[b][:, c]).T)
+                s = mag + 0.0
+                if self.bias:
+                    kp = n(self.key_pos if ko is not None else self.pos)
+                    s = s + n(self.slope)[h] * np.sqrt(((n(self.pos)[a][:, None] - kp[b][None]) ** 2).sum(-1))
+                E = max(E, (((6 * self.D / 16 + 16) * U + 2.0 ** -21) * mag + 16 * U * s).max())
+        L = max(max(self.lens, default=0), max(self.key_lens or self.lens, default=0))
+        largest = max(1.0, *(float(t.abs().max()) for t in (self.q, self.k, self.v, self.g)))
+        tiny = 8 * L * 2.0 ** -126 * max(self.D, self.Dv) * largest ** 3
+        sums = (6 * L / 16 + 16) * U + 2.0 ** -21
+        w = 2 * E + 16 * U + sums
+        mag = ref["abs_out"]
+        for o, tol in ((out, w), (plain, w + (2.0 ** -17 if self.xb and self.yb else 0.0))):
+            t = tol * mag + tiny
+            near(o, ref["out"], t + (half_ulp(np.abs(ref["out"]) + t) if self.yb else 0.0), "out")
+        m, inv = f64(saved)[:2 * self.heads * self.nq].reshape(2, self.heads, self.nq)
+        assert np.all(inv[m == -np.inf] == 0)
+        lse = m - np.log2(np.where(inv > 0, inv, 1.0))
+        finite = np.isfinite(ref["lse"])
+        assert np.all(np.abs(lse[finite] - ref["lse"][finite]) <= 2 * E + 16 * U * (1 + np.abs(ref["lse"][finite])))
+        assert np.all(lse[~finite] == -np.inf)
+        if self.yb:
+            near(saved[2 * self.heads * self.nq:].view(self.nq, -1), ref["out"], w * mag + tiny, "saved output")
+        e = 2 * w + 2 * ((6 * self.Dv / 16 + 16) * U + 2.0 ** -21)
+        ec = e + (2 * E / self.cap + 16 * U if self.cap else 0.0)
+        gq, gk, gv, gs, gp, gkp = grads
+        near(gv, ref["grad_v"], w * ref["abs_grad_v"] + tiny, "grad_v")
+        near(gq, ref["grad_q"], (ec + sums) * ref["abs_grad_q"] + tiny, "grad_q")
+        near(gk, ref["grad_k"], (ec + sums) * ref["abs_grad_k"] + tiny, "grad_k")
+        if self.bias:
+            near(gs, ref["grad_slope"], (e + (4 * L + self.nq) * U) * ref["abs_grad_slope"], "grad_slope")
+            near(gp, ref["grad_pos"], (e + 4 * L * U) * ref["abs_grad_pos"], "grad_pos")
+            if ko is not None:
+                near(gkp, ref["grad_key_pos"], (e + 4 * L * U) * ref["abs_grad_key_pos"], "grad_key_pos")
+        return out, grads
+
+
+# every width class, widths that end inside a tile, channels per head that are and are not multiples of four
+SIDES = [("4x0e", "4x0e", 4), ("8x0e+8x1o", "8x0e+8x1o", 4), ("32x0e", "12x0e+4x1o", 2), ("66x0e", "62x0e", 2),
+         ("16x0e+16x1o+16x2e", "24x0e+24x1o", 2), ("100x0e", "20x0e+20x1o+4x2e", 1), ("18x1o+36x2e", "128x0e", 2),
+         ("32x0e+32x1o+32x2e", "32x0e+32x1o+32x2e", 2), ("150x0e+4x1o", "15x2e+9x3o", 1),
+         ("16x0e+16x1o+16x2e+16x3o", "200x0e", 1), ("7x0e+5x1o+3x2e+1x3o", "3x0e+31x1o", 1)]
+LENS = [(1,), (5, 0, 33, 1), (31, 32, 65), (130, 3)]
+
+
+@pytest.mark.parametrize("qk,v,heads", SIDES)
+@pytest.mark.parametrize("xb,yb", [(False, False), (True, True), (True, False)])
+def test_attention_matches_definition(at, qk, v, heads, xb, yb):
+    for i, lens in enumerate(LENS):
+        say(f"[case] attention {qk} {v} heads={heads} {lens} x={'bf16' if xb else 'f32'} y={'bf16' if yb else 'f32'}")
+        Case(qk, v, heads, lens, None, xb, yb, cap=4.0 if i % 2 else 0.0, bias=i >= 2, seed=i).check(at)
+
+
+@pytest.mark.parametrize("xb", [False, True])
+@pytest.mark.parametrize("lens,key_lens", [((1, 2, 1), (40, 0, 7)), ((1,), (700,)), ((0, 3), (5, 129)), ((150, 4), (3, 1)),
+                                           ((1, 1, 1, 1), (300, 1, 513, 64)), ((300,), (1,))])
+@pytest.mark.parametrize("cap,bias", [(0.0, True), (3.0, False)])
+def test_cross_form(at, xb, lens, key_lens, cap, bias):
+    say(f"[case] cross {lens} {key_lens} x={'bf16' if xb else 'f32'} cap={cap} bias={bias}")
+    Case("12x0e+4x1o", "8x0e+8x1o", 4, lens, key_lens, xb, xb, cap, bias, 3).check(at)
+
+
+@pytest.mark.parametrize("xb,cap,bias", [(False, 0.0, True), (True, 3.0, True), (False, 2.0, False)])
+def test_long_rows_in_parts(at, xb, cap, bias):
+    """Few blocks and a long axis: cut into parts and joined, forward and in both directions of the backward."""
+    say(f"[case] parts x={'bf16' if xb else 'f32'}")
+    c = Case("32x0e", "16x0e+8x1o", 1, (1111,), None, xb, xb, cap, bias, 4)
+    assert c.layer(at).workspace_size(c.batch(at), at.OP_FORWARD) > 0
+    c.check(at)
+
+
+@pytest.mark.parametrize("lens", [(400, 200, 100), (97, 96, 95)])
+def test_blocks_of_four_waves(at, lens):
+    say(f"[case] four waves {lens}")
+    for heads, xb in ((8, False), (8, True)):
+        Case("64x0e+32x1o", "64x0e+32x1o", heads, lens, None, xb, False, 0.0, True, 5).check(at)
+
+
+@pytest.mark.parametrize("spread", [1e-18, 30.0])
+def test_very_small_and_very_large_scores(at, spread):
+    """Scores that vanish beside the others, and a softmax of few keys: the largest weights are near one."""
+    say(f"[case] spread {spread}")
+    Case("32x0e", "32x0e", 2, (50, 40), None, False, False, 0.0, False, 6, spread).check(at)
+
+
+def test_rows_outside_of_graphs(at):
+    """They are not read and stay as they were: NaN in the inputs, marks in the outputs; a first row behind row 0."""
+    import torch
+
+    say("[case] rows outside")
+    for self_form in (True, False):
+        c = Case("8x0e+8x1o", "8x0e+8x1o", 2, (7, 40), None if self_form else (3, 90), bias=True, seed=7)
+        ref_out, _, _, ref = c.run(at)
+        h = c.layer(at)
+
+        def pad(t, front, back):
+            p = torch.full((front + t.shape[0] + back, t.shape[1]), float("nan"), device="cuda")
+            p[front:front + t.shape[0]] = t
+            return p
+
+        f, b = 5, 60
+        q, pos, g, k, v = (pad(t, f, b) for t in (c.q, c.pos, c.g, c.k, c.v))
+        cross = () if self_form else (c.nk + f + b, offsets(c.key_lens, f), pad(c.key_pos, f, b))
+        batch = at.Batch(c.nq + f + b, offsets(c.lens, f), pos, *cross)
+        out = torch.full((c.nq + f + b, h.feat_v), 7.0, device="cuda")
+        saved = torch.zeros(h.saved_size(c.nq + f + b), device="cuda")
+        at.tpconv_attention_forward(h, batch, q, k, v, slope=c.slope, out=out, saved=saved)
+        grads = dict(grad_q=torch.full_like(q, 7.0), grad_k=torch.full_like(k, 7.0), grad_v=torch.full_like(v, 7.0),
+                     grad_pos=torch.full_like(pos, 7.0))
+        if not self_form:
+            grads["grad_key_pos"] = torch.full((c.nk + f + b, 3), 7.0, device="cuda")
+        got = at.tpconv_attention_backward(h, batch, q, k, v, out, saved, g, slope=c.slope, want=("slope",), **grads)
+        assert torch.equal(got[3], ref[3])
+        for t, r in zip((out, *got[:3], *got[4:]), (ref_out, *ref[:3], *ref[4:])):
+            if t is None:
+                assert r is None
+                continue
+            assert torch.equal(t[f:f + r.shape[0]], r)
+            assert torch.all(t[:f] == 7.0) and torch.all(t[f + r.shape[0]:] == 7.0)
+
+
+@pytest.mark.parametrize("xb", [False, True])
+def test_columns_of_wider_tensors(at, xb):
+    """q, k and v as column ranges of one projection, their gradients into one tensor; odd first columns."""
+    import torch
+
+    say("[case] columns")
+    for qk, v, heads in (("16x0e+8x1o", "16x0e+8x1o", 4), ("6x0e", "10x0e", 2)):
+        c = Case(qk, v, heads, (20, 33), None, xb, xb, seed=8)
+        ref_out, _, _, ref = c.run(at)
+        h, b = c.layer(at), c.batch(at)
+        widths = [h.feat_qk, h.feat_qk, h.feat_v]
+        wide = torch.full((c.nq, sum(widths) + 5), float("nan"), dtype=c.q.dtype, device="cuda")
+        gwide = torch.full((c.nq, sum(widths) + 5), 7.0, device="cuda")
+        first = np.cumsum([1] + widths)
+        parts = [wide[:, a:a + w] for a, w in zip(first, widths)]
+        gparts = [gwide[:, a:a + w] for a, w in zip(first, widths)]
+        for p, t in zip(parts, (c.q, c.k, c.v)):
+            p.copy_(t)
+        saved = torch.empty(h.saved_size(c.nq), device="cuda")
+        out = at.tpconv_attention_forward(h, b, *parts, saved=saved)
+        got = at.tpconv_attention_backward(h, b, *parts, out, saved, c.g, want=(), grad_q=gparts[0], grad_k=gparts[1],
+                                           grad_v=gparts[2])
+        assert torch.equal(out, ref_out)
+        for t, r in zip(got[:3], ref[:3]):
+            assert torch.equal(t, r)
+        assert torch.all(gwide[:, 0] == 7.0) and torch.all(gwide[:, 1 + sum(widths):] == 7.0)
+
+
+def test_each_gradient_on_its_own(at):
+    import torch
+
+    say("[case] single gradients")
+    c = Case("8x0e+8x1o", "8x0e+8x1o", 2, (30, 50), bias=True, seed=9)
+    out, _, saved, ref = c.run(at)
+    h, b = c.layer(at), c.batch(at)
+    for i, name in ((0, "q"), (1, "k"), (2, "v"), (3, "slope"), (4, "pos")):
+        got = at.tpconv_attention_backward(h, b, c.q, c.k, c.v, out, saved, c.g, slope=c.slope, want=(name,))
+        assert torch.equal(got[i], ref[i]) and all(t is None for j, t in enumerate(got) if j != i)
+
+
+def test_one_graph_without_offsets(at):
+    import torch
+
+    say("[case] no offsets")
+    c = Case("8x0e", "8x0e", 2, (45,), seed=10)
+    out = c.run(at)[0]
+    assert torch.equal(at.tpconv_attention_forward(c.layer(at), at.Batch(45), c.q, c.k, c.v), out)
+
+
+def test_nothing_to_attend(at):
+    """No queries, no keys, no graphs, graphs without nodes."""
+    import torch
+
+    say("[case] empty")
+    h = at.Attention("8x0e", "8x0e", 2)
+    z = lambda n, f=8: torch.zeros(n, f, device="cuda")  # noqa: E731
+    empty = torch.zeros(1, dtype=torch.int32, device="cuda")
+    assert at.tpconv_attention_forward(h, at.Batch(0), z(0), z(0), z(0)).shape == (0, 8)
+    out = torch.full((3, 8), 7.0, device="cuda")
+    at.tpconv_attention_forward(h, at.Batch(3, empty), z(3), z(3), z(3), out=out)  # no graphs: no row is in one
+    assert torch.all(out == 7.0)
+    b = at.Batch(2, offsets((1, 1)), z(2, 3), 0, offsets((0, 0)), z(0, 3))  # queries without keys
+    slope = torch.ones(2, device="cuda")
+    saved = torch.empty(h.saved_size(2), device="cuda")
+    out = at.tpconv_attention_forward(h, b, z(2) + 1, z(0), z(0), slope=slope, saved=saved)
+    assert torch.all(out == 0)
+    got = at.tpconv_attention_backward(h, b, z(2) + 1, z(0), z(0), out, saved, z(2) + 1, slope=slope,
+                                       want=("q", "k", "v", "slope", "pos"))
+    assert all(torch.all(t == 0) for t in got) and got[1].shape == (0, 8)
+    b = at.Batch(0, offsets((0, 0)), z(0, 3), 2, offsets((1, 1)), z(2, 3))  # keys without queries
+    got = at.tpconv_attention_backward(h, b, z(0), z(2) + 1, z(2) + 1, z(0), torch.empty(0, device="cuda"), z(0),
+                                       slope=slope, want=("q", "k", "v", "slope", "pos"))
+    assert all(torch.all(t == 0) for t in got) and got[2].shape == (2, 8)
+
+
+def test_values_that_are_not_finite_stay_in_their_graph(at):
+    import torch
+
+    say("[case] not finite")
+    for xb in (False, True):
+        c = Case("8x0e", "8x0e", 2, (20, 40, 20), None, xb, False, seed=11)
+        ref = c.run(at)[0]
+        c.k[25, 1] = float("inf")  # a key of the second graph, first head
+        c.v[70, 7] = float("nan")  # a value of the third, second head
+        out = c.run(at)[0]
+        assert torch.equal(out[:20], ref[:20]) and torch.equal(out[20:60, 4:], ref[20:60, 4:])
+        assert torch.equal(out[60:, :7], ref[60:, :7]) and torch.all(out[60:, 7].isnan())
+        # scores of plus infinity; those of minus infinity are weights of zero where the product is exact (bf16)
+        up = c.q[20:60, 1] > 0 if xb else torch.ones(40, dtype=torch.bool, device="cuda")
+        assert up.any() and not torch.any(out[20:60, :4][up].isfinite())
+
+
+def test_offsets_that_decrease_or_leave_the_rows_stay_inside_the_tensors(at):
+    """Their results are anything; what lies behind the tensors is not touched (the tile search and the key ranges clamp)."""
+    import torch
+
+    say("[case] bad offsets")
+    h = at.Attention("8x0e", "8x0e", 2)
+    for bad in ([0, 50, 20, 64], [-5, 10, 1000, 2000], [64, 0, 64, 0], [2 ** 31 - 1, -2 ** 31, 5, 64]):
+        n = 64
+        buf = torch.full((3 * n, 8), 7.0, device="cuda")
+        q = torch.randn(n, 8, device="cuda")
+        off = torch.tensor(bad, dtype=torch.int64).to(torch.int32).cuda()
+        saved = torch.zeros(h.saved_size(n), device="cuda")
+        batch = at.Batch(n, off)
+        out = at.tpconv_attention_forward(h, batch, q, q, q, out=buf[n:2 * n], saved=saved)
+        at.tpconv_attention_backward(h, batch, q, q, q, out, saved, q)
+        torch.cuda.synchronize()
+        assert torch.all(buf[:n] == 7.0) and torch.all(buf[2 * n:] == 7.0)
+
+
+def test_the_same_results_every_time_and_on_any_stream(at):
+    import torch
+
+    say("[case] repeated")
+    for lens, heads in (((300, 7, 90), 4), ((1200,), 1)):
+        c = Case("16x0e+16x1o", "16x0e+16x1o", heads, lens, bias=True, cap=3.0, seed=12)
+        out, plain, saved, grads = c.run(at)
+        assert torch.equal(out, plain)
+        again = c.run(at)
+        assert torch.equal(out, again[0]) and all(torch.equal(a, b) for a, b in zip(grads[:5], again[3][:5]))
+        side, h, b = torch.cuda.Stream(), c.layer(at), c.batch(at)
+        side.wait_stream(torch.cuda.current_stream())
+        saved2 = torch.empty_like(saved)
+        o2 = at.tpconv_attention_forward(h, b, c.q, c.k, c.v, slope=c.slope, saved=saved2, stream=side)
+        g2 = at.tpconv_attention_backward(h, b, c.q, c.k, c.v, o2, saved2, c.g, slope=c.slope, want=c.want(), stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(out, o2) and all(torch.equal(a, b) for a, b in zip(grads[:5], g2[:5]))
+
+
+# ---- embedding ------------------------------------------------------------------------
+
+
+def embed_case(at, n, rows, features, xb, yb, seed, hot=0.0, scale=1.5):
+    import torch
+
+    rng = np.random.default_rng(seed)
+    z = rng.integers(-1, rows + 1, n).astype(np.int32)  # -1 and rows: no type
+    z[rng.random(n) < hot] = rows // 2
+    if n > 3:
+        z[:2] = 2 ** 31 - 1, -2 ** 31
+    W, g = cuda(rng.standard_normal((rows, features)), xb), cuda(rng.standard_normal((n, features)))
+    code = (at.TPCONV_F32, at.TPCONV_BF16)
+    e = at.Embedding(rows, features, scale, code[xb], code[yb])
+    index = torch.from_numpy(z).cuda()
+    y = at.tpconv_embed_forward(e, index, W)
+    gW = at.tpconv_embed_backward(e, index, g, grad_W=torch.full((rows, features), float("nan"), device="cuda"))
+    torch.cuda.synchronize()
+    ref = oa.embed(z, f64(W), scale)
+    near(y, ref, 2 * U * np.abs(ref) + (half_ulp(ref) if yb else 0.0), "embedding")
+    rg, mag = oa.embed_backward(z, f64(g), rows, scale)
+    most = np.bincount(z[(z >= 0) & (z < rows)], minlength=1).max(initial=0)
+    near(gW, rg, (most + 4) * U * mag, "grad_W")
+    return e, index, g, gW
+
+
+@pytest.mark.parametrize("n", [0, 1, 5, 64, 128, 129, 1000, 4097, 16384, 16385, 30011])
+@pytest.mark.parametrize("rows,features", [(1, 1), (10, 8), (89, 65), (256, 128), (300, 129), (5000, 3), (70000, 7)])
+def test_embedding_matches_definition(at, n, rows, features):
+    say(f"[case] embed n={n} rows={rows} features={features}")
+    embed_case(at, n, rows, features, n % 2 == 1, features % 2 == 1, n + rows)
+
+
+@pytest.mark.parametrize("n,rows,features,hot", [(20000, 4, 257, 0.9), (3000, 1000, 515, 0.5), (50000, 89, 32, 0.3),
+                                                 (16384, 3, 1024, 1.0), (129, 2, 70, 1.0)])
+def test_embedding_of_uneven_types(at, n, rows, features, hot):
+    say(f"[case] embed n={n} rows={rows} features={features} hot={hot}")
+    embed_case(at, n, rows, features, False, False, n, hot)
+
+
+def test_embedding_gradient_is_the_same_every_time(at):
+    import torch
+
+    say("[case] embed repeated")
+    for n in (100, 9000, 40000):
+        e, index, g, gW = embed_case(at, n, 30, 100, False, False, 1, 0.4)
+        ws = torch.empty(max(1, e.workspace_size(n)), dtype=torch.uint8, device="cuda").fill_(255)
+        assert torch.equal(gW, at.tpconv_embed_backward(e, index, g, workspace=ws))
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        got = at.tpconv_embed_backward(e, index, g, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(gW, got)
+
+
+# ---- dropout --------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("text", ["1x0e", "8x0e+8x1o", "9x0e+5x1o+8x2e", "32x0e+32x1o+17x2e+3x3o", "1031x0e", "16x1e+4096x0e"])
+@pytest.mark.parametrize("xb,yb", [(False, False), (True, True), (False, True), (True, False)])
+def test_dropout_matches_definition(at, text, xb, yb):
+    import torch
+
+    F = irreps(text)[1]
+    code = (at.TPCONV_F32, at.TPCONV_BF16)
+    for n, p, seed, offset in ((1, 0.5, 0, 0), (13, 0.1, -1, -1), (5, 1.0, 3, 2 ** 40), (4, 0.0, 2 ** 62, 5)):
+        if n * F > 30000:
+            n = 2
+        say(f"[case] dropout {text} n={n} p={p}")
+        rng = np.random.default_rng(n)
+        x, r, g = cuda(rng.standard_normal((n, F)), xb), cuda(rng.standard_normal((n, F)), yb), cuda(rng.standard_normal((n, F)))
+        d = at.Dropout(text, p, code[xb], code[yb])
+        state = torch.tensor([seed, offset], dtype=torch.int64, device="cuda")
+        f = oa.dropout_factors(text, n, p, seed, offset)
+        assert abs(d.p - round(p * 65536) / 65536) < 1e-9
+        for res in (r, None):
+            y = at.tpconv_dropout_forward(d, x, state, residual=res)
+            ref = f64(x) * f + (0.0 if res is None else f64(r))
+            mag = np.abs(f64(x) * f) + (0.0 if res is None else np.abs(f64(r)))
+            near(y, ref, 3 * U * mag + (half_ulp(np.abs(ref) + 3 * U * mag) if yb else 0.0), "dropout")
+        gx = at.tpconv_dropout_backward(d, g, state)
+        near(gx, f64(g) * f, 2 * U * np.abs(f64(g) * f), "dropout gradient")
+        # in place, and a dropped value that is not finite
+        at.tpconv_dropout_forward(d, x, state, residual=r, out=r)
+        y = at.tpconv_dropout_forward(d, x, state)
+        if xb == yb:
+            assert torch.equal(at.tpconv_dropout_forward(d, x, state, out=x), y)
+        bad = torch.where(torch.from_numpy(f).cuda() == 0, float("nan"), g)
+        assert torch.equal(at.tpconv_dropout_backward(d, bad, state, grad_x=bad), gx)
+
+
+def test_dropout_of_many_nodes(at):
+    """Counters that differ in the node alone, past the nodes of one block and the launch's first step."""
+    import torch
+
+    say("[case] dropout many nodes")
+    n = 70001
+    d = at.Dropout("3x0e", 0.3)
+    state = torch.tensor([11, 12], dtype=torch.int64, device="cuda")
+    y = at.tpconv_dropout_forward(d, torch.ones(n, 3, device="cuda"), state)
+    for first in (0, 511, 69990):
+        f = oa.dropout_factors("3x0e", 11, 0.3, 11, 12, first)
+        near(y[first:first + 11], f, 2 * U * f, "dropout")
+    assert abs(float((y > 0).float().mean()) - 0.7) < 0.01
