@@ -10,6 +10,7 @@ from __future__ import annotations
 import argparse
 import glob
 import os
+import re
 import subprocess
 import sys
 from concurrent.futures import ThreadPoolExecutor
@@ -41,6 +42,7 @@ POS_VARIANTS = [("bpos_f32", "float", 0), ("bpos_bf16", "uint16_t", 0), ("hess_f
 # The edge streams keep their matrix-core accumulators in ordinary VGPRs
 # (the accumulation registers would otherwise be copied back and forth).
 STREAM_FLAGS = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
+RESOURCES = "-Rpass-analysis=kernel-resource-usage"
 # Values per head of the attention kernels' width classes (attention_join.hip lists the same)
 ATTENTION_WIDTHS = (32, 64, 96, 128, 160, 256)
 UNITS = ([(f"stream_{n}", "stream_gf.hip", STREAM_FLAGS + [f"-DTP_MODE={m}", f"-DTP_LO={lo}",
@@ -55,7 +57,7 @@ UNITS = ([(f"stream_{n}", "stream_gf.hip", STREAM_FLAGS + [f"-DTP_MODE={m}", f"-
                                              ("timing", ".cpp"), ("layer_norm", ".hip"), ("linear", ".hip"),
                                              ("muon", ".hip"), ("layers", ".cpp"), ("embedding", ".hip"),
                                              ("dropout", ".hip"), ("attention_join", ".hip"), ("attention", ".cpp"))]
-         + [(f"attention_{dc}", "attention_class.hip", [f"-DTP_DC={dc}"]) for dc in ATTENTION_WIDTHS])
+         + [(f"attention_{dc}", "attention_class.hip", [f"-DTP_DC={dc}", RESOURCES]) for dc in ATTENTION_WIDTHS])
 
 
 def run(cmd):
@@ -86,9 +88,28 @@ def compile_one(unit, incremental=False):
     if incremental and os.path.exists(obj) and os.path.getmtime(obj) > _newest_input(src):
         return obj
     lang = ["-x", "hip"] if src.endswith(".hip") else []
-    run([HIPCC] + HIP_FLAGS + defines + ["-I", GEN, "-I", CSRC, "-I", os.path.join(ROOT, "include")] + lang +
-        ["-c", os.path.join(CSRC, src), "-o", obj])
+    out = run([HIPCC] + HIP_FLAGS + defines + ["-I", GEN, "-I", CSRC, "-I", os.path.join(ROOT, "include")] + lang +
+              ["-c", os.path.join(CSRC, src), "-o", obj])
+    if RESOURCES in defines:
+        try:
+            check_registers(name, out)
+        except RuntimeError:
+            os.remove(obj)
+            raise
     return obj
+
+
+def check_registers(unit: str, remarks: str) -> None:
+    """Refuse kernels that use accumulation registers and spill as well: the compiler of ROCm 7.2 ended in its pass over
+    MFMA operands in accumulation registers on some of them, and gave others that computed wrong results."""
+    kernel, agprs = "", 0
+    for line in remarks.splitlines():
+        if m := re.search(r"Function Name: (\S+)", line):
+            kernel, agprs = m[1], 0
+        elif m := re.search(r"\sAGPRs: (\d+)", line):
+            agprs = int(m[1])
+        elif (m := re.search(r"VGPRs Spill: (\d+)", line)) and int(m[1]) and agprs:
+            raise RuntimeError(f"{unit}: {kernel} spills {m[1]} registers with {agprs} accumulation registers in use")
 
 
 def build(jobs: int = 8, verbose: bool = False, incremental: bool = False) -> str:

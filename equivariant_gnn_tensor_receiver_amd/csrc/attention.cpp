@@ -96,7 +96,7 @@ int64_t keys_of(const tpconv_attention_batch& b) { return b.key_offsets ? b.num_
 // Blocks of a launch: their threads must stay below 2^32.
 bool too_many(const AttnShape& s, int heads) {
   return s.tiles > (int64_t(1) << 40) / (heads * s.nsplit) ||
-         (s.tiles * heads * s.nsplit + 8) * 64 * s.waves >= (int64_t(1) << 32);
+         (s.tiles * heads * s.nsplit + 8) * 4 * s.cols >= (int64_t(1) << 32);
 }
 
 tpconv_status plan_of(const tpconv_attention_s& h, int op, const tpconv_attention_batch& b, AttnPlan& p) {

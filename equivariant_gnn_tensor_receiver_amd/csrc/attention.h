@@ -67,10 +67,13 @@ struct AttnJoinArgs {
 
 constexpr int kAttnMaxHead = 256;
 
-// Rows per block: 32 per wave, one or four waves.
+// Rows per block where the graphs are small: 32, but blocks of wide heads need LDS for
+// several waves' worth of registers (a CU's LDS holds two of 160 values, one of 256).
+constexpr int attn_small_cols(int DC) { return DC <= 96 ? 32 : DC <= 160 ? 64 : 128; }
+
 struct AttnShape {
   int cls;       // index of the width class
-  int waves;     // 1 or 4
+  int cols;      // rows per block: 128 or attn_small_cols
   int nsplit;
   int64_t tiles;
 };

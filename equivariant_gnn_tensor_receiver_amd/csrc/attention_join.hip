@@ -8,12 +8,12 @@
 
 namespace tpconv {
 
-hipError_t launch_attn_class_32(int kind, const AttnArgs& a, int waves, hipStream_t st);
-hipError_t launch_attn_class_64(int kind, const AttnArgs& a, int waves, hipStream_t st);
-hipError_t launch_attn_class_96(int kind, const AttnArgs& a, int waves, hipStream_t st);
-hipError_t launch_attn_class_128(int kind, const AttnArgs& a, int waves, hipStream_t st);
-hipError_t launch_attn_class_160(int kind, const AttnArgs& a, int waves, hipStream_t st);
-hipError_t launch_attn_class_256(int kind, const AttnArgs& a, int waves, hipStream_t st);
+hipError_t launch_attn_class_32(int kind, const AttnArgs& a, int cols, hipStream_t st);
+hipError_t launch_attn_class_64(int kind, const AttnArgs& a, int cols, hipStream_t st);
+hipError_t launch_attn_class_96(int kind, const AttnArgs& a, int cols, hipStream_t st);
+hipError_t launch_attn_class_128(int kind, const AttnArgs& a, int cols, hipStream_t st);
+hipError_t launch_attn_class_160(int kind, const AttnArgs& a, int cols, hipStream_t st);
+hipError_t launch_attn_class_256(int kind, const AttnArgs& a, int cols, hipStream_t st);
 
 namespace {
 
@@ -148,7 +148,7 @@ hipError_t launch_class(int kind, AttnArgs& a, const AttnShape& s, hipStream_t s
   TimingScope ts(kcAttention, st);
   a.tiles = s.tiles;
   a.nsplit = s.nsplit;
-  return kLaunch[s.cls](kind, a, s.waves, st);
+  return kLaunch[s.cls](kind, a, s.cols, st);
 }
 
 }  // namespace
@@ -158,13 +158,12 @@ AttnShape attn_shape(int D, int64_t rows, int64_t other, int64_t graphs, int hea
   s.cls = 0;
   while (kWidth[s.cls] < D) ++s.cls;
   const int64_t g = std::max<int64_t>(1, graphs);
-  s.waves = rows / g >= 96 ? 4 : 1;
-  const int64_t m = 32 * s.waves;
+  s.cols = rows / g >= 96 ? 128 : attn_small_cols(kWidth[s.cls]);
+  const int64_t m = s.cols;
   s.tiles = rows / m + g;
   // too few blocks for the 256 CUs: cut the long axis, 64 rows of it at least per part
   const int64_t blocks = std::max<int64_t>((rows + m - 1) / m, std::min(rows, g)) * heads;
-  const int64_t most = std::max<int64_t>(1, other / g / 64);
-  const int64_t enough = s.waves == 1 ? 2048 : 512;
+  const int64_t most = std::max<int64_t>(1, other / g / 64), enough = s.cols < 128 ? 2048 : 512;
   s.nsplit = (int)std::min<int64_t>(std::min<int64_t>(64, most), std::max<int64_t>(1, enough / std::max<int64_t>(1, blocks)));
   return s;
 }

@@ -1,6 +1,6 @@
 // Attention among the nodes of each graph (include/tpconv_attention.h).
 //
-// A wave takes 32 columns of a head (queries in the forward and in the
+// A wave takes CT = 32 or 16 columns of a head (queries in the forward and in the
 // gradient of the queries, keys in the gradients of keys and values) and runs
 // over the rows of the other side, 32 at a time:
 //
@@ -11,10 +11,17 @@
 // Every score tile has its own column in the lane and its other index along the
 // accumulator registers, so that softmax statistics are sums over a lane's
 // registers and one swap of the two half waves, and the tile is, as it stands,
-// the right operand of the product that follows: v_mfma_f32_32x32x16_bf16 wants
+// the right operand of the product that follows: a matrix instruction wants
 // eight reductions per lane, and which eight they are does not matter as long
-// as the left operand's are the same (the transposing LDS reads take keys
-// 4h..4h+3 and 8+4h..8+4h+3 for half wave h, which is how the accumulators lie).
+// as the left operand's are the same (the transposing LDS reads take the two
+// quads of rows that the accumulators of a lane's group hold).
+//
+// bf16 takes 32 columns and v_mfma_f32_32x32x16_bf16, four waves per block: bound by
+// the vector unit (exponentials, distances, splitting), with two to four waves per
+// SIMD.  fp32, and bf16 heads wider than 96, take 16 columns and v_mfma_f32_16x16x32_bf16, eight waves per block:
+// its three pieces per operand would leave room for one wave of 32 columns per SIMD
+// only, whose products and vector work then follow one another (8192 nodes of
+// 128x0e+128x1o+128x2e, 8 heads: forward 369 us, gradients 725 and 1130; now 263, 463 and 710).
 //
 // Precision: an fp32 operand is the sum of three bf16 pieces, each the rounded
 // rest of those before (|p1| <= 2^-9 |x|, |p2| <= 2^-18 |x|, 2^-27 |x| is left out),
@@ -60,38 +67,125 @@ constexpr int pieces() {
 // LDS row length in values (see the header of this file; checked for 64 banks).
 constexpr int row_len(int D) { return D + (D % 64 == 32 || D % 128 == 0 ? 16 : 8); }
 
+// Columns per wave (see the header of this file).
+template <typename T, int DC>
+constexpr int col_tile() {
+  return sizeof(T) == 4 || DC > 96 ? 16 : 32;
+}
+
+__device__ __forceinline__ int lane_id() { return threadIdx.x & 63; }
+
 // ---- pieces ---------------------------------------------------------------------
 
+// Three pieces of inputs.  Each value on its own, so that one that is not finite stays alone.
+__device__ __forceinline__ void split_inputs(const float (&v)[8], bf16x8 (&p)[3]) {
+#pragma unroll
+  for (int t = 0; t < 8; ++t) {
+    p[0][t] = (__bf16)v[t];
+    const float r = v[t] - (float)p[0][t];
+    p[1][t] = (__bf16)r;
+    p[2][t] = (__bf16)(r - (float)p[1][t]);
+  }
+}
+
+// Pieces of weights, made beside every tile of scores: the rest v - p comes from a
+// dot product of the pair with (-1, 0) or (0, -1), one instruction in place of two.
 template <int P>
-__device__ __forceinline__ void split(const float (&v)[8], bf16x8 (&p)[P]) {
-  if constexpr (P == 3) {
+__device__ __forceinline__ void split_weights(const float (&v)[8], bf16x8 (&p)[P], const SplitConsts& k) {
 #pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      p[0][t] = (__bf16)v[t];
-      const float r = v[t] - (float)p[0][t];
-      p[1][t] = (__bf16)r;
-      p[2][t] = (__bf16)(r - (float)p[1][t]);
-    }
-  } else {
-    static_assert(P == 2, "fp32 values are three or two pieces");
+  for (int t = 0; t < 4; ++t) {
+    float x = v[2 * t], y = v[2 * t + 1];
 #pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      p[0][t] = (__bf16)v[t];
-      p[1][t] = (__bf16)(v[t] - (float)p[0][t]);
+    for (int i = 0; i < P; ++i) {
+      const bf16x2 h = {(__bf16)x, (__bf16)y};
+      p[i][2 * t] = h[0];
+      p[i][2 * t + 1] = h[1];
+      if (i + 1 < P) {
+        x = __builtin_amdgcn_fdot2_f32_bf16(h, k.neg_x, x, false);
+        y = __builtin_amdgcn_fdot2_f32_bf16(h, k.neg_y, y, false);
+      }
     }
   }
 }
 
+__device__ __forceinline__ floatx16 mfma(bf16x8 a, bf16x8 b, floatx16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ floatx4 mfma(bf16x8 a, bf16x8 b, floatx4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
 // acc += sum of the products of pieces of ranks up to 2, smallest first.
-template <int PA, int PB>
-__device__ __forceinline__ void mul(const bf16x8 (&a)[PA], const bf16x8 (&b)[PB], floatx16& acc) {
+template <int PA, int PB, typename ACC>
+__device__ __forceinline__ void mul(const bf16x8 (&a)[PA], const bf16x8 (&b)[PB], ACC& acc) {
 #pragma unroll
   for (int rank = 2; rank >= 0; --rank)
 #pragma unroll
     for (int i = 0; i < PA; ++i)
 #pragma unroll
       for (int j = 0; j < PB; ++j)
-        if (i + j == rank) acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[j], acc, 0, 0, 0);
+        if (i + j == rank) acc = mfma(a[i], b[j], acc);
+}
+
+// ---- tiles ------------------------------------------------------------------------
+
+// CT columns: lane = group * CT + column.  A tile of 32 rows of scores is a lane's
+// registers 4 q + e, row first_row(q) + e; right operands hold 512 / CT reductions
+// per step, 8 per lane, from 8 * group on.
+template <int CT>
+struct Geo;
+template <>
+struct Geo<32> {
+  using Acc = floatx16;                   // one matrix instruction's result
+  static constexpr int kRows = 32;        // its rows
+  static constexpr int kStep = 16;        // its reductions
+  static constexpr int kQuads = 4;        // quads of rows per lane in 32 rows
+  static __device__ __forceinline__ int col() { return lane_id() & 31; }
+  static __device__ __forceinline__ int group() { return lane_id() >> 5; }
+  static __device__ __forceinline__ int first_row(int q) { return 8 * q + 4 * group(); }
+};
+template <>
+struct Geo<16> {
+  using Acc = floatx4;
+  static constexpr int kRows = 16;
+  static constexpr int kStep = 32;
+  static constexpr int kQuads = 2;
+  static __device__ __forceinline__ int col() { return lane_id() & 15; }
+  static __device__ __forceinline__ int group() { return lane_id() >> 4; }
+  static __device__ __forceinline__ int first_row(int q) { return 16 * q + 4 * group(); }
+};
+
+// 32 rows x CT columns of scores.
+template <int CT>
+struct Tile32 {
+  using G = Geo<CT>;
+  static constexpr int kTiles = 32 / G::kRows, kRegs = 4 * G::kQuads, kPer = kRegs / kTiles;
+  typename G::Acc a[kTiles];
+  __device__ __forceinline__ float get(int r) const { return a[r / kPer][r % kPer]; }
+  __device__ __forceinline__ void set(int r, float v) { a[r / kPer][r % kPer] = v; }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int r = 0; r < kRegs; ++r) set(r, 0.f);
+  }
+};
+
+// Sums and maxima over the groups of lanes that share a column.
+template <int CT, typename F>
+__device__ __forceinline__ float join_groups(float v, F f) {
+  if constexpr (CT == 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = f(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  }
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return f(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+template <int CT>
+__device__ __forceinline__ float col_sum(float v) {
+  return join_groups<CT>(v, [](float a, float b) { return a + b; });
+}
+template <int CT>
+__device__ __forceinline__ float col_max(float v) {
+  return join_groups<CT>(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
 // ---- loads ----------------------------------------------------------------------
@@ -126,7 +220,7 @@ struct Octet<float> {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] *= f;
   }
-  __device__ __forceinline__ void planes(bf16x8 (&p)[3]) const { split<3>(v, p); }
+  __device__ __forceinline__ void planes(bf16x8 (&p)[3]) const { split_inputs(v, p); }
 };
 template <>
 struct Octet<uint16_t> {
@@ -172,16 +266,13 @@ __device__ __forceinline__ void fill_table(int* at, const AttnSide& s, int h) {
 
 // R rows of the other side from row0 on, `valid` of them there: into registers, and
 // from there as planes into LDS, each row multiplied by its factor (fp32 rows
-// alone) where there are any.  Blocks of four waves share the rows; a block of one
-// wave (R = 32) loads them as the left operand of the products wants them, lane
-// (i, h) values 16 c + 8 h.. of row i, and uses them from the registers too.
-template <typename T, int DC, int R, int W, bool VEC>
+// alone) where there are any.
+template <typename T, int DC, int R, int THREADS, bool VEC>
 struct Stage {
   static constexpr int P = pieces<T>(), LD = row_len(DC), plane = R * LD, per = DC / 8, total = R * per;
-  static constexpr int passes = (total + 64 * W - 1) / (64 * W);
-  static_assert(W == 4 || R == 32, "one wave takes 32 rows");
+  static constexpr int passes = (total + THREADS - 1) / THREADS;
   // Without whole quads the loads are many: each is stored before the next, to keep the code short.
-  static constexpr bool held = VEC || W == 1;
+  static constexpr bool held = VEC;
   Octet<T> o[held ? passes : 1];
   const T* base;
   const float* factor;
@@ -191,14 +282,9 @@ struct Stage {
   __device__ __forceinline__ Stage(const void* b, int64_t l, const int* t, int d, const float* f = nullptr)
       : base(static_cast<const T*>(b)), factor(f), ld(l), at(t), D(d) {}
   static __device__ __forceinline__ void place(int pass, int& row, int& e0) {
-    if constexpr (W == 1) {
-      row = threadIdx.x & 31;
-      e0 = 16 * pass + 8 * ((threadIdx.x >> 5) & 1);
-    } else {
-      const int idx = pass * 64 * W + (int)threadIdx.x;
-      row = idx / per;
-      e0 = (idx - row * per) * 8;
-    }
+    const int idx = pass * THREADS + (int)threadIdx.x;
+    row = idx / per;
+    e0 = (idx - row * per) * 8;
   }
   __device__ __forceinline__ void get(int pass, Octet<T>& x, int64_t row0, int valid) const {
     int row, e0;
@@ -213,7 +299,7 @@ struct Stage {
   static __device__ __forceinline__ void set(int pass, const Octet<T>& x, uint16_t* s) {
     int row, e0;
     place(pass, row, e0);
-    if (row < R) {
+    if (total % THREADS == 0 || row < R) {
       bf16x8 pl[P];
       x.planes(pl);
 #pragma unroll
@@ -239,43 +325,104 @@ struct Stage {
   }
 };
 
-// Left operand whose rows are rows of LDS: lane (i, h) reads values k + 8h.. of row `row` + i.
-template <int P, int DC, int R>
+// Left operand whose rows are rows of LDS: lane (row, group) reads values k + 8 group.. of row `row` + its own.
+template <int CT, int P, int DC, int R>
 __device__ __forceinline__ void rows_frag(const uint16_t* s, int row, int k, bf16x8 (&f)[P]) {
   constexpr int LD = row_len(DC), plane = R * LD;
-  const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int i = 0; i < P; ++i)
-    f[i] = *reinterpret_cast<const bf16x8*>(s + i * plane + (row + (lane & 31)) * LD + k + 8 * (lane >> 5));
+    f[i] = *reinterpret_cast<const bf16x8*>(s + i * plane + (row + Geo<CT>::col()) * LD + k + 8 * Geo<CT>::group());
 }
 
-// The same, of rows that a block of one wave holds in its registers.
-template <typename T, int DC, int R, int W, bool VEC>
-__device__ __forceinline__ void left_rows(const Stage<T, DC, R, W, VEC>& st, const uint16_t* s, int row, int c,
-                                          bf16x8 (&f)[pieces<T>()]) {
-  if constexpr (W == 1)
-    st.o[c].planes(f);
-  else
-    rows_frag<pieces<T>(), DC, R>(s, row, 16 * c, f);
-}
-
-// Left operand whose rows are columns d + 0..31 of LDS and whose reductions are
-// LDS rows row + 4h + 0..3 and row + 8 + 4h + 0..3.  Each group of 16 lanes turns
-// 4 rows x 16 columns: lane l supplies the address of four columns of row l / 4
-// and receives column l of the four rows.
-template <int P, int DC, int R>
-__device__ __forceinline__ void cols_frag(const uint16_t* s, int row, int d, bf16x8 (&f)[P]) {
+// Left operand whose rows are columns d.. of LDS and whose reductions are the LDS
+// rows of the registers 8 step .. 8 step + 7 of a lane's scores: two quads of rows.
+// Each group of 16 lanes turns 4 rows x 16 columns: lane l supplies the address of
+// four columns of row l / 4 and receives column l of the four rows.
+template <int CT, int P, int DC, int R>
+__device__ __forceinline__ void cols_frag(const uint16_t* s, int row, int step, int d, bf16x8 (&f)[P]) {
   constexpr int LD = row_len(DC), plane = R * LD;
   typedef __attribute__((address_space(3))) s16x4* lds_ptr;
-  const int lane = threadIdx.x & 63, l = lane & 15;
-  const uint16_t* p = s + (row + 4 * (lane >> 5) + (l >> 2)) * LD + d + 16 * ((lane >> 4) & 1) + 4 * (l & 3);
+  const int l = lane_id() & 15;
+  const uint16_t* p = s + (row + Geo<CT>::first_row(2 * step) + (l >> 2)) * LD + d + (lane_id() & (CT - 16)) + 4 * (l & 3);
+  constexpr int next = (CT == 32 ? 8 : 16) * LD;  // the other quad
 #pragma unroll
   for (int i = 0; i < P; ++i) {
     const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + i * plane));
-    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + i * plane + 8 * LD));
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + i * plane + next));
     f[i] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
   }
 }
+
+// s += left rows (LDS) x right operand, 32 rows from `row` on, the c-th reduction step.
+template <int CT, int PA, int PB, int DC, int R>
+__device__ __forceinline__ void add_scores(const uint16_t* lds, int row, int c, const bf16x8 (&b)[PB], Tile32<CT>& s) {
+  using G = Geo<CT>;
+#pragma unroll
+  for (int t = 0; t < Tile32<CT>::kTiles; ++t) {
+    bf16x8 f[PA];
+    rows_frag<CT, PA, DC, R>(lds, row + G::kRows * t, G::kStep * c, f);
+    mul<PA, PB>(f, b, s.a[t]);
+  }
+}
+
+// A transposed result: rows are head elements, columns the wave's own.
+template <int CT, int DC>
+struct Result {
+  using G = Geo<CT>;
+  static constexpr int kTiles = DC / G::kRows, kQuads = CT == 32 ? 4 : 1;
+  typename G::Acc a[kTiles];
+  __device__ __forceinline__ void scale(float f) {
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+      for (int r = 0; r < 4 * kQuads; ++r) a[t][r] *= f;
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+      for (int r = 0; r < 4 * kQuads; ++r) a[t][r] = 0.f;
+  }
+  // += columns of LDS (rows row..) x right operand of the step
+  template <int PA, int PB, int R>
+  __device__ __forceinline__ void add(const uint16_t* lds, int row, int step, const bf16x8 (&b)[PB]) {
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+      bf16x8 f[PA];
+      cols_frag<CT, PA, DC, R>(lds, row, step, G::kRows * t, f);
+      mul<PA, PB>(f, b, a[t]);
+    }
+  }
+  // Writes a lane's column, times f, to its row of features.
+  template <bool VEC, typename O>
+  __device__ __forceinline__ void put(float f, const int* at, int D, O* row) const {
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+      for (int q = 0; q < kQuads; ++q) {
+        const int e0 = G::kRows * t + (CT == 32 ? 8 * q : 0) + 4 * G::group();
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = a[t][4 * q + e] * f;
+        if constexpr (VEC) {
+          if (e0 < D) put4(row + at[e0], v);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (e0 + e < D) put1(row + at[e0 + e], v[e]);
+        }
+      }
+  }
+  static __device__ __forceinline__ uint32_t bits(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
+  static __device__ __forceinline__ void put1(float* p, float v) { *p = v; }
+  static __device__ __forceinline__ void put1(uint16_t* p, float v) { *p = (uint16_t)bits(v); }
+  static __device__ __forceinline__ void put4(float* p, const float (&v)[4]) {
+    *reinterpret_cast<floatx4_any*>(p) = (floatx4){v[0], v[1], v[2], v[3]};
+  }
+  static __device__ __forceinline__ void put4(uint16_t* p, const float (&v)[4]) {
+    *reinterpret_cast<u32x2_any*>(p) = (u32x2){bits(v[0]) | (bits(v[1]) << 16), bits(v[2]) | (bits(v[3]) << 16)};
+  }
+};
 
 // ---- rows of graphs ---------------------------------------------------------------
 
@@ -338,47 +485,46 @@ __device__ __forceinline__ void other_rows(const int32_t* off, int g, int64_t N,
   }
 }
 
-// Row of accumulator register r: columns run along the lanes.
-__device__ __forceinline__ int acc_row(int r) { return 8 * (r >> 2) + 4 * ((threadIdx.x >> 5) & 1) + (r & 3); }
-
-// The other half wave's value of the same column.
-__device__ __forceinline__ float other_half(float v) {
-  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  // r[0]: lower half's values in both halves, r[1]: the upper half's
-  return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
+// A value that is the same in all lanes, kept in a scalar register.
+__device__ __forceinline__ float uniform(float v) {
+  return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(v)));
 }
-__device__ __forceinline__ float half_sum(float v) { return v + other_half(v); }
 
 __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
 
-// tanh, accurate relative to its value: the odd series below 1/4 (the next term
-// is below 2^-26 there), (1 - e) / (1 + e) with e = exp(-2 |x|) above.
-__device__ __forceinline__ float tanh_acc(float x) {
-  const float a = fabsf(x), t = x * x;
-  const float e = exp2_fast(-2.f * kLog2e * a);
-  const float big = copysignf((1.f - e) * __builtin_amdgcn_rcpf(1.f + e), x);
-  const float small =
-      x + x * t * (-1.f / 3.f + t * (2.f / 15.f + t * (-17.f / 315.f + t * (62.f / 2835.f - t * (1382.f / 155925.f)))));
-  return a < 0.25f ? small : big;
+// Which part, head and tile a block works on: the tiles of a head run together
+// on an XCD, whose L2 then holds that head's other side.
+struct Work {
+  int part, h;
+  uint32_t tile;
+};
+__device__ __forceinline__ bool find_work(const AttnArgs& a, Work& w) {
+  const uint32_t tiles = (uint32_t)a.tiles, items = tiles * (uint32_t)a.H * (uint32_t)a.nsplit;
+  const uint32_t per = gridDim.x >> 3, item = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if (item >= items) return false;
+  const uint32_t ph = item / tiles;
+  w.tile = item - ph * tiles;
+  w.part = (int)(ph / (uint32_t)a.H);
+  w.h = (int)(ph - (uint32_t)w.part * (uint32_t)a.H);
+  return true;
 }
 
-// Per-row fp32 values of the other side in LDS (positions: one plane per
-// coordinate), loaded ahead like the rows.
-template <int R, int W>
+// Per-row positions of the other side in LDS, one plane per coordinate, loaded ahead like the rows.
+template <int R, int THREADS>
 struct StagePos {
-  static constexpr int passes = (3 * R + 64 * W - 1) / (64 * W);
+  static constexpr int passes = (3 * R + THREADS - 1) / THREADS;
   float v[passes];
   __device__ __forceinline__ void load(const float* pos, int64_t row0, int valid) {
 #pragma unroll
     for (int p = 0; p < passes; ++p) {
-      const int i = p * 64 * W + (int)threadIdx.x;
+      const int i = p * THREADS + (int)threadIdx.x;
       v[p] = i < 3 * valid ? pos[row0 * 3 + i] : 0.f;
     }
   }
   __device__ __forceinline__ void put(float* s) const {
 #pragma unroll
     for (int p = 0; p < passes; ++p) {
-      const int i = p * 64 * W + (int)threadIdx.x;
+      const int i = p * THREADS + (int)threadIdx.x;
       if (i < 3 * R) s[(i % 3) * R + i / 3] = v[p];
     }
   }
@@ -388,13 +534,13 @@ struct StagePos {
 struct Place {
   float x, y, z, slope2;  // position, slope in units of log2
 };
-__device__ __forceinline__ Place place_of(const AttnArgs& a, const float* pos, int64_t row, int h) {
+__device__ __forceinline__ Place place_of(const AttnArgs& a, bool bias, const float* pos, int64_t row, int h) {
   Place p = {0.f, 0.f, 0.f, 0.f};
-  if (a.slope) {
+  if (bias) {
     p.x = pos[row * 3];
     p.y = pos[row * 3 + 1];
     p.z = pos[row * 3 + 2];
-    p.slope2 = a.slope[h] * kLog2e;
+    p.slope2 = uniform(a.slope[h] * kLog2e);
   }
   return p;
 }
@@ -405,44 +551,116 @@ struct BiasSums {
   float x = 0.f, y = 0.f, z = 0.f;    // of dS (r - r') / d
 };
 
-// Scores of a 32 x 32 tile.  CAP or BIAS: in units of log2; otherwise as they
-// are, to be multiplied by scale log2(e).
-template <bool CAP, bool BIAS, int R>
-__device__ __forceinline__ void score_tile(const AttnArgs& a, floatx16& s, const float* spos, int row, const Place& p) {
-  const float in = CAP ? a.scale / a.cap : 0.f, out = a.cap * kLog2e, c = a.scale * kLog2e;
+// How scores are capped: not at all; all of a tile below a quarter of the cap, where
+// the odd series of tanh does (the next term is below 2^-26 there); any.
+enum CapKind { kNoCap, kSmall, kAnyCap };
+
+// cap tanh(scale s / cap) log2(e), accurate relative to its value.
+struct Cap {
+  float in, out, unout;  // scale / cap, cap log2(e), 1 / out
+  float k[6];            // of the series in s^2, times s
+  __device__ __forceinline__ Cap(const AttnArgs& a) {
+    in = uniform(a.cap > 0.f ? a.scale / a.cap : 0.f);
+    out = uniform(a.cap * kLog2e);
+    unout = uniform(a.cap > 0.f ? 1.f / out : 0.f);
+    const float i2 = in * in;
+    float f = in * out;
+    const float c[6] = {1.f, -1.f / 3.f, 2.f / 15.f, -17.f / 315.f, 62.f / 2835.f, -1382.f / 155925.f};
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
+    for (int i = 0; i < 6; ++i) {
+      k[i] = uniform(c[i] * f);
+      f *= i2;
+    }
+  }
+  __device__ __forceinline__ float series(float s) const {
+    const float t = s * s;
+    float v = k[5];
+#pragma unroll
+    for (int i = 4; i >= 0; --i) v = fmaf(v, t, k[i]);
+    return v * s;
+  }
+  __device__ __forceinline__ float any(float s) const {
+    const float x = s * in, e = exp2_fast(-2.f * kLog2e * fabsf(x));
+    const float big = copysignf((1.f - e) * __builtin_amdgcn_rcpf(1.f + e) * out, x);
+    return fabsf(x) < 0.25f ? series(s) : big;
+  }
+};
+
+// What scores get, known to the compiler: the two kinds of branches around every
+// tile would keep copies of it in registers (16384 nodes x 512 in bf16: 1944 us of kernel, 1722 without).
+// kRuntime leaves both to the run: heads whose channels are not whole quads.
+enum ScoreKind { kRuntime = -1, kPlain = 0, kBiased = 1, kCapped = 2, kCappedBiased = 3 };
+template <int KIND>
+__device__ __forceinline__ bool has_bias(const AttnArgs& a) {
+  return KIND == kRuntime ? a.slope != nullptr : (KIND & kBiased) != 0;
+}
+template <int KIND>
+__device__ __forceinline__ bool has_cap(const AttnArgs& a) {
+  return KIND == kRuntime ? a.cap > 0.f : (KIND & kCapped) != 0;
+}
+
+// f(cap kind, bias) with the two as compile-time constants.
+template <int KIND, int CT, typename F>
+__device__ __forceinline__ void with_kind(const AttnArgs& a, const Cap& cap, const Tile32<CT>& s, F f) {
+  auto go = [&](auto kind) {
+    if (has_bias<KIND>(a))
+      f(kind, std::true_type{});
+    else
+      f(kind, std::false_type{});
+  };
+  if (!has_cap<KIND>(a)) {
+    go(std::integral_constant<int, kNoCap>{});
+    return;
+  }
+  float top = fabsf(s.get(0));
+#pragma unroll
+  for (int r = 1; r < Tile32<CT>::kRegs; ++r) top = fmaxf(top, fabsf(s.get(r)));
+  if (__any(!(top * fabsf(cap.in) < 0.25f)))
+    go(std::integral_constant<int, kAnyCap>{});
+  else
+    go(std::integral_constant<int, kSmall>{});
+}
+
+// Scores of a tile.  CAP or BIAS: in units of log2; otherwise as they are, to be
+// multiplied by scale log2(e).
+template <int CAP, bool BIAS, int R, int CT>
+__device__ __forceinline__ void score_tile(const Cap& cap, float c, Tile32<CT>& s, const float* spos, int row,
+                                           const Place& p) {
+  using G = Geo<CT>;
+#pragma unroll
+  for (int q = 0; q < G::kQuads; ++q) {
     floatx4 x, y, z;
     if constexpr (BIAS) {
-      const int at = row + 8 * q + 4 * ((threadIdx.x >> 5) & 1);
+      const int at = row + G::first_row(q);
       x = *reinterpret_cast<const floatx4*>(spos + at);
       y = *reinterpret_cast<const floatx4*>(spos + R + at);
       z = *reinterpret_cast<const floatx4*>(spos + 2 * R + at);
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      float v = s[4 * q + e];
-      if constexpr (CAP) v = tanh_acc(v * in) * out;
+      float v = s.get(4 * q + e);
+      if constexpr (CAP == kSmall) v = cap.series(v);
+      if constexpr (CAP == kAnyCap) v = cap.any(v);
       if constexpr (BIAS) {
         const float dx = p.x - x[e], dy = p.y - y[e], dz = p.z - z[e];
         const float dist = __builtin_amdgcn_sqrtf(fmaf(dx, dx, fmaf(dy, dy, dz * dz)));
-        v = CAP ? fmaf(-p.slope2, dist, v) : fmaf(v, c, -p.slope2 * dist);
+        v = CAP != kNoCap ? fmaf(-p.slope2, dist, v) : fmaf(v, c, -p.slope2 * dist);
       }
-      s[4 * q + e] = v;
+      s.set(4 * q + e, v);
     }
   }
 }
 
-// The tile of the backward: s (scores as products) -> weights against the
-// rows' references `ref(r)`, ds (dP) -> dS = P (dP - delta(r)), in the end with the
-// cap's factor; adds to the column's sums where there is a bias.
-template <bool CAP, bool BIAS, int R, typename REF, typename DELTA>
-__device__ __forceinline__ void grad_tile(const AttnArgs& a, floatx16& s, floatx16& ds, const float* spos, int row,
-                                          const Place& p, BiasSums& b, REF ref, DELTA delta) {
-  const float in = CAP ? a.scale / a.cap : 0.f, out = a.cap * kLog2e, c = a.scale * kLog2e;
+// The tile of the backward: s (scores as products) -> weights against the rows'
+// references ref(q), ds (dP) -> dS = P (dP - delta(q)), in the end with the cap's
+// factor; adds to the column's sums where there is a bias.
+template <int CAP, bool BIAS, int R, int CT, typename REF, typename DELTA>
+__device__ __forceinline__ void grad_tile(const Cap& cap, float c, Tile32<CT>& s, Tile32<CT>& ds, const float* spos,
+                                          int row, const Place& p, BiasSums& b, REF ref, DELTA delta) {
+  using G = Geo<CT>;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int at = row + 8 * q + 4 * ((threadIdx.x >> 5) & 1);
+  for (int q = 0; q < G::kQuads; ++q) {
+    const int at = row + G::first_row(q);
     floatx4 x, y, z;
     if constexpr (BIAS) {
       x = *reinterpret_cast<const floatx4*>(spos + at);
@@ -453,17 +671,18 @@ __device__ __forceinline__ void grad_tile(const AttnArgs& a, floatx16& s, floatx
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int r = 4 * q + e;
-      float th = 0.f, v;
-      if constexpr (CAP) th = tanh_acc(s[r] * in);
-      float dx, dy, dz, d2, over;
+      float u = s.get(r);
+      if constexpr (CAP == kSmall) u = cap.series(u);
+      if constexpr (CAP == kAnyCap) u = cap.any(u);
+      float v = CAP != kNoCap ? u - m4[e] : fmaf(u, c, -m4[e]);
+      float g;
       if constexpr (BIAS) {
-        dx = p.x - x[e], dy = p.y - y[e], dz = p.z - z[e];
-        d2 = fmaf(dx, dx, fmaf(dy, dy, dz * dz));
-        over = d2 > 0.f ? __builtin_amdgcn_rsqf(d2) : 0.f;
+        const float dx = p.x - x[e], dy = p.y - y[e], dz = p.z - z[e];
+        const float d2 = fmaf(dx, dx, fmaf(dy, dy, dz * dz));
+        const float over = d2 > 0.f ? __builtin_amdgcn_rsqf(d2) : 0.f;
         const float dist = d2 * over;
-        v = CAP ? fmaf(th, out, -m4[e]) : fmaf(s[r], c, -m4[e]);
         v = exp2_fast(fmaf(-p.slope2, dist, v));
-        const float g = v * (ds[r] - d4[e]);
+        g = v * (ds.get(r) - d4[e]);
         b.sd = fmaf(g, dist, b.sd);
         b.s += g;
         b.pd = fmaf(v, dist, b.pd);
@@ -471,106 +690,72 @@ __device__ __forceinline__ void grad_tile(const AttnArgs& a, floatx16& s, floatx
         b.x = fmaf(w, dx, b.x);
         b.y = fmaf(w, dy, b.y);
         b.z = fmaf(w, dz, b.z);
-        ds[r] = g;
       } else {
-        v = exp2_fast(CAP ? fmaf(th, out, -m4[e]) : fmaf(s[r], c, -m4[e]));
-        ds[r] = v * (ds[r] - d4[e]);
+        v = exp2_fast(v);
+        g = v * (ds.get(r) - d4[e]);
       }
-      if constexpr (CAP) ds[r] *= fmaf(-th, th, 1.f);
-      s[r] = v;
+      if constexpr (CAP != kNoCap) {
+        const float th = u * cap.unout;
+        g *= fmaf(-th, th, 1.f);
+      }
+      ds.set(r, g);
+      s.set(r, v);
     }
   }
 }
 
-// f(cap, bias) with the two as compile-time constants.
-template <typename F>
-__device__ __forceinline__ void with_kind(const AttnArgs& a, F f) {
-  if (a.cap > 0.f) {
-    if (a.slope)
-      f(std::true_type{}, std::true_type{});
-    else
-      f(std::true_type{}, std::false_type{});
-  } else {
-    if (a.slope)
-      f(std::false_type{}, std::true_type{});
-    else
-      f(std::false_type{}, std::false_type{});
-  }
+// Eight registers of a tile as a right operand's pieces.
+template <int P, int CT>
+__device__ __forceinline__ void weights_frag(const Tile32<CT>& s, int step, bf16x8 (&p)[P], const SplitConsts& k) {
+  float v[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = s.get(8 * step + e);
+  split_weights<P>(v, p, k);
 }
 
-// Writes a lane's column of a transposed result (rows: head elements) to its row of features.
-template <int DC, bool VEC>
-__device__ __forceinline__ void put_column(const floatx16 (&acc)[DC / 32], float f, const int* at, int D, float* row) {
-#pragma unroll
-  for (int t = 0; t < DC / 32; ++t)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int e0 = 32 * t + 8 * q + 4 * ((threadIdx.x >> 5) & 1);
-      if constexpr (VEC) {
-        if (e0 < D) {
-          floatx4 v;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = acc[t][4 * q + e] * f;
-          *reinterpret_cast<floatx4_any*>(row + at[e0]) = v;
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (e0 + e < D) row[at[e0 + e]] = acc[t][4 * q + e] * f;
-      }
-    }
-}
-template <int DC, bool VEC>
-__device__ __forceinline__ void put_column(const floatx16 (&acc)[DC / 32], float f, const int* at, int D,
-                                           uint16_t* row) {
-#pragma unroll
-  for (int t = 0; t < DC / 32; ++t)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int e0 = 32 * t + 8 * q + 4 * ((threadIdx.x >> 5) & 1);
-      uint16_t b[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) b[e] = __builtin_bit_cast(uint16_t, (__bf16)(acc[t][4 * q + e] * f));
-      if constexpr (VEC) {
-        if (e0 < D)
-          *reinterpret_cast<u32x2_any*>(row + at[e0]) =
-              (u32x2){b[0] | ((uint32_t)b[1] << 16), b[2] | ((uint32_t)b[3] << 16)};
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (e0 + e < D) row[at[e0 + e]] = b[e];
-      }
-    }
-}
-
-template <int N>
-__device__ __forceinline__ void zero(floatx16 (&acc)[N]) {
-#pragma unroll
-  for (int t = 0; t < N; ++t)
-#pragma unroll
-    for (int r = 0; r < 16; ++r) acc[t][r] = 0.f;
-}
-
-// Which part, head and tile a block works on: the tiles of a head run together
-// on an XCD, whose L2 then holds that head's other side.
-struct Work {
-  int part, h;
-  int64_t tile, item;
+// A block takes 128 columns of a head, or attn_small_cols where the graphs are small.  (64 for
+// wide fp32 heads, which lets a CU hold two blocks, splits the other side's rows
+// twice as often: 286, 523, 578 and 291 us where 128 take 264, 460, 449 and 267.)
+template <typename T, int DC, int COLS>
+struct Block {
+  static constexpr int CT = col_tile<T, DC>(), kWaves = COLS / CT, kThreads = 64 * kWaves;
+  static constexpr int kShift = COLS == 128 ? 7 : COLS == 64 ? 6 : 5;
+  static_assert(COLS == 128 || COLS == attn_small_cols(DC), "rows per block");
+  // the block's column of this lane
+  static __device__ __forceinline__ int col() { return (int)(threadIdx.x >> 6) * CT + Geo<CT>::col(); }
 };
-__device__ __forceinline__ bool find_work(const AttnArgs& a, Work& w) {
-  const int64_t items = a.tiles * a.H * a.nsplit;
-  w.item = xcd_item(blockIdx.x, gridDim.x);
-  if (w.item >= items) return false;
-  const int64_t ph = w.item / a.tiles;
-  w.tile = w.item - ph * a.tiles;
-  w.part = (int)(ph / a.H);
-  w.h = (int)(ph - (int64_t)w.part * a.H);
-  return true;
+
+// A column's right operand: values of the row at p.
+template <typename T, int DC, bool VEC, int CT, int P>
+__device__ __forceinline__ void own_row(const T* p, const int* at, int D, bf16x8 (&f)[DC / Geo<CT>::kStep][P]) {
+#pragma unroll
+  for (int c = 0; c < DC / Geo<CT>::kStep; ++c) {
+    Octet<T> o;
+    o.template load<VEC>(p, at, Geo<CT>::kStep * c + 8 * Geo<CT>::group(), D);
+    o.planes(f[c]);
+  }
 }
 
-// Waves per SIMD that the registers are held to: two where a wave's operands and
-// sums leave room (one hides the latency of the other), else one.
-constexpr int waves_for(int regs) { return regs <= 200 ? 2 : 1; }
+// Waves per SIMD that the registers are held to, from an estimate of what a wave
+// holds: a block's waves meet at every step, and others hide the latency.  Two at
+// least, which also keeps every kernel out of the accumulation registers: with these
+// in use and values spilled at once, ROCm 7.2's compiler ended in its pass over MFMA
+// operands in accumulation registers or made kernels with wrong results (the build
+// refuses such a kernel).
+constexpr int waves_for(int regs) { return regs <= 110 ? 4 : regs <= 150 ? 3 : 2; }
+// registers of: right operands of n pieces in all, results, scores, and the rest
+template <typename T, int DC>
+constexpr int regs_for(int right, int results, int rest) {
+  return DC * col_tile<T, DC>() / 128 * right + results * DC * col_tile<T, DC>() / 64 + rest;
+}
+
+// Whether a kernel holds the other side's next rows in registers while it works on
+// the present ones: not where wide heads leave none for it, nor for small graphs,
+// which take one or two steps.
+template <typename T, int DC, int COLS>
+constexpr bool rows_ahead(bool forward) {
+  return COLS == 128 && (forward ? DC <= 160 : DC <= 96);
+}
 
 // ---- forward ----------------------------------------------------------------------
 
@@ -579,152 +764,139 @@ constexpr int waves_for(int regs) { return regs <= 200 ? 2 : 1; }
 // stay below 2^kSlack, which fp32 sums and bf16 pieces hold as well as below 1.
 constexpr float kSlack = 8.f;
 
-template <typename T, int DC, int W, int PP, bool VEC>
-__global__ __launch_bounds__(64 * W, waves_for(DC / 4 * pieces<T>() + DC / 2 + 60)) void forward_kernel(const AttnArgs a) {
-  constexpr int P = pieces<T>(), R = W == 4 && DC <= 64 ? 64 : 32, LD = row_len(DC), NT = DC / 32, NC = DC / 16;
-  constexpr int kShift = W == 4 ? 7 : 5;
-  __shared__ __align__(16) uint16_t sk[W == 1 ? 8 : P * R * LD], sv[P * R * LD];
+template <typename T, int DC, int COLS, int PP, bool VEC, int KIND>
+__global__ __launch_bounds__((Block<T, DC, COLS>::kThreads), (waves_for(regs_for<T, DC>(pieces<T>(), 1, (KIND & kCapped) != 0 ? 80 : 60)))) void forward_kernel(
+    const AttnArgs a) {
+  using B = Block<T, DC, COLS>;
+  constexpr int CT = B::CT, P = pieces<T>(), R = 32, LD = row_len(DC);
+  using G = Geo<CT>;
+  constexpr int NC = DC / G::kStep, kRegs = Tile32<CT>::kRegs;
+  __shared__ __align__(16) uint16_t sk[P * R * LD], sv[P * R * LD];
   __shared__ int at_qk[DC], at_v[DC];
   __shared__ __align__(16) float spos[3 * R];
   Work w;
   Tile t;
-  if (!find_work(a, w) || !find_tile(a.qo, a.G, a.Nq, kShift, w.tile, t)) return;
+  if (!find_work(a, w) || !find_tile(a.qo, a.G, a.Nq, B::kShift, w.tile, t)) return;
   fill_table<DC>(at_qk, a.sqk, w.h);
   fill_table<DC>(at_v, a.sv, w.h);
   __syncthreads();
-  const int lane = threadIdx.x & 63, half = lane >> 5;
-  const int col = (threadIdx.x >> 6) * 32 + (lane & 31);
+  const int col = B::col();
   const bool mine = col < t.rows;
   const int64_t query = t.row0 + min(col, t.rows - 1);
   const int Dqk = a.sqk.D, Dv = a.sv.D;
-  const bool bias = a.slope != nullptr;
+  const bool bias = has_bias<KIND>(a);
   int64_t kb, ke;
   other_rows<R>(a.ko, t.g, a.Nk, w.part, a.nsplit, kb, ke);
-  Stage<T, DC, R, W, VEC> rk(a.k, a.ldk, at_qk, Dqk), rv(a.v, a.ldv, at_v, Dv);
-  StagePos<R, W> rp;
+  Stage<T, DC, R, B::kThreads, VEC> rk(a.k, a.ldk, at_qk, Dqk), rv(a.v, a.ldv, at_v, Dv);
+  StagePos<R, B::kThreads> rp;
   auto load = [&](int64_t k0) {
     const int valid = (int)(ke - k0 < R ? ke - k0 : R);
     rk.load(k0, valid);
     rv.load(k0, valid);
     if (bias) rp.load(a.kpos, k0, valid);
   };
-  if (kb < ke) load(kb);
+  constexpr bool kAhead = rows_ahead<T, DC, COLS>(true);
+  if (kAhead && kb < ke) load(kb);
   bf16x8 q[NC][P];
-#pragma unroll
-  for (int c = 0; c < NC; ++c) {
-    Octet<T> o;
-    o.template load<VEC>(static_cast<const T*>(a.q) + query * a.ldq, at_qk, 16 * c + 8 * half, Dqk);
-    o.planes(q[c]);
-  }
-  const Place place = place_of(a, a.qpos, query, w.h);
+  own_row<T, DC, VEC, CT>(static_cast<const T*>(a.q) + query * a.ldq, at_qk, Dqk, q);
+  const Place place = place_of(a, bias, a.qpos, query, w.h);
+  const Cap cap(a);
+  const SplitConsts consts;
   // scores are multiplied by this on their way into the exponent
-  const bool raw = !bias && !(a.cap > 0.f);
-  const float unit = raw ? a.scale * kLog2e : 1.f;
-  floatx16 acc[NT];
-  zero(acc);
+  const float c2 = uniform(a.scale * kLog2e);
+  const bool raw = !bias && !has_cap<KIND>(a);
+  const float unit = uniform(raw ? c2 : 1.f);
+  Result<CT, DC> acc;
+  acc.clear();
   float m = -INFINITY, l = 0.f;
   for (int64_t k0 = kb; k0 < ke; k0 += R) {
     const int valid = (int)(ke - k0 < R ? ke - k0 : R);
+    if (!kAhead) load(k0);
     __syncthreads();
-    if constexpr (W == 4) rk.put(sk, k0, valid);
+    rk.put(sk, k0, valid);
     rv.put(sv, k0, valid);
     if (bias) rp.put(spos);
     __syncthreads();
-    if (W == 4 && k0 + R < ke) {
+    if (kAhead && k0 + R < ke) {
       load(k0 + R);
       __builtin_amdgcn_sched_barrier(0);  // the loads stay ahead of the products
     }
-    for (int sub = 0; sub < (W == 1 ? 1 : valid); sub += 32) {
-      floatx16 s;
+    for (int sub = 0; sub < valid; sub += 32) {
+      Tile32<CT> s;
+      s.clear();
 #pragma unroll
-      for (int r = 0; r < 16; ++r) s[r] = 0.f;
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        bf16x8 f[P];
-        left_rows(rk, sk, sub, c, f);
-        mul<P, P>(f, q[c], s);
-      }
-      if (W == 1 && k0 + R < ke) load(k0 + R);
-      if (!raw) with_kind(a, [&](auto cap, auto bs) {
-        score_tile<decltype(cap)::value, decltype(bs)::value, R>(a, s, spos, sub, place);
-      });
+      for (int c = 0; c < NC; ++c) add_scores<CT, P, P, DC, R>(sk, sub, c, q[c], s);
+      if (!raw)
+        with_kind<KIND>(a, cap, s, [&](auto kind, auto bs) {
+          score_tile<decltype(kind)::value, decltype(bs)::value, R>(cap, c2, s, spos, sub, place);
+        });
       if (valid - sub < 32)
 #pragma unroll
-        for (int r = 0; r < 16; ++r)
-          if (sub + acc_row(r) >= valid) s[r] = unit < 0.f ? INFINITY : -INFINITY;
-      float top = s[0];
+        for (int r = 0; r < kRegs; ++r)
+          if (sub + G::first_row(r / 4) + r % 4 >= valid) s.set(r, unit < 0.f ? INFINITY : -INFINITY);
+      float top = s.get(0);
       if (unit < 0.f) {
 #pragma unroll
-        for (int r = 1; r < 16; ++r) top = fminf(top, s[r]);
+        for (int r = 1; r < kRegs; ++r) top = fminf(top, s.get(r));
       } else {
 #pragma unroll
-        for (int r = 1; r < 16; ++r) top = fmaxf(top, s[r]);
+        for (int r = 1; r < kRegs; ++r) top = fmaxf(top, s.get(r));
       }
-      top *= unit;
-      top = fmaxf(top, other_half(top));
+      top = col_max<CT>(top * unit);
       if (__any(top > m + kSlack)) {
         const float next = fmaxf(m, top);
         const float f = m == -INFINITY ? 0.f : exp2_fast(m - next);
         l *= f;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) acc[n][r] *= f;
+        acc.scale(f);
         m = next;
       }
       const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        s[r] = exp2_fast(fmaf(s[r], unit, -ref));
-        l += s[r];
+      for (int r = 0; r < kRegs; ++r) {
+        const float p = exp2_fast(fmaf(s.get(r), unit, -ref));
+        s.set(r, p);
+        l += p;
       }
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
-        float pv[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) pv[e] = s[8 * kk + e];
+      for (int st = 0; st < kRegs / 8; ++st) {
         bf16x8 p[PP];
-        split<PP>(pv, p);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          bf16x8 f[P];
-          cols_frag<P, DC, R>(sv, sub + 16 * kk, 32 * n, f);
-          mul<P, PP>(f, p, acc[n]);
-        }
+        weights_frag<PP>(s, st, p, consts);
+        acc.template add<P, PP, R>(sv, sub, st, p);
       }
     }
   }
-  l = half_sum(l);
+  l = col_sum<CT>(l);
   if (!mine) return;
   if (a.nsplit > 1) {
     const int64_t at = ((int64_t)w.part * a.H + w.h) * a.Nq + query;
-    if (half == 0) {
+    if (G::group() == 0) {
       a.part_ml[2 * at] = m;
       a.part_ml[2 * at + 1] = l;
     }
-    put_column<DC, VEC>(acc, 1.f, at_v, Dv, a.part_o + ((int64_t)w.part * a.Nq + query) * a.sv.F);
+    acc.template put<VEC>(1.f, at_v, Dv, a.part_o + ((int64_t)w.part * a.Nq + query) * a.sv.F);
     return;
   }
   const float f = l > 0.f || l != l ? 1.f / l : 0.f;
-  if (a.stat && half == 0) {
+  if (a.stat && G::group() == 0) {
     a.stat[(int64_t)w.h * a.Nq + query] = m;
     a.stat[(int64_t)(a.H + w.h) * a.Nq + query] = f;
   }
-  if (a.out32) put_column<DC, VEC>(acc, f, at_v, Dv, a.out32 + query * a.sv.F);
+  if (a.out32) acc.template put<VEC>(f, at_v, Dv, a.out32 + query * a.sv.F);
   if (a.y_bf16)
-    put_column<DC, VEC>(acc, f, at_v, Dv, static_cast<uint16_t*>(a.out) + query * a.sv.F);
+    acc.template put<VEC>(f, at_v, Dv, static_cast<uint16_t*>(a.out) + query * a.sv.F);
   else
-    put_column<DC, VEC>(acc, f, at_v, Dv, static_cast<float*>(a.out) + query * a.sv.F);
+    acc.template put<VEC>(f, at_v, Dv, static_cast<float*>(a.out) + query * a.sv.F);
 }
 
 // A column's share of its position's gradient, per part and head.
-__device__ __forceinline__ void put_pos(const AttnArgs& a, const Work& w, int64_t rows, int64_t row, bool mine,
+template <int CT>
+__device__ __forceinline__ void put_pos(const AttnArgs& a, bool bias, const Work& w, int64_t rows, int64_t row, bool mine,
                                         BiasSums& b, float f) {
-  if (!a.part_pos) return;
-  b.x = half_sum(b.x);
-  b.y = half_sum(b.y);
-  b.z = half_sum(b.z);
-  if (!mine || (threadIdx.x & 32)) return;
+  if (!bias || !a.part_pos) return;
+  b.x = col_sum<CT>(b.x);
+  b.y = col_sum<CT>(b.y);
+  b.z = col_sum<CT>(b.z);
+  if (!mine || Geo<CT>::group() != 0) return;
   float* o = a.part_pos + (((int64_t)w.part * a.H + w.h) * rows + row) * 3;
   f *= -a.slope[w.h];
   o[0] = f * b.x;
@@ -734,173 +906,160 @@ __device__ __forceinline__ void put_pos(const AttnArgs& a, const Work& w, int64_
 
 // ---- gradient of the queries ----------------------------------------------------------
 
-template <typename T, int DC, int W, bool VEC>
-__global__ __launch_bounds__(64 * W, waves_for(DC / 4 * (pieces<T>() + 3) + DC / 2 + 80)) void grad_q_kernel(
-    const AttnArgs a) {
-  constexpr int P = pieces<T>(), R = W == 4 && DC <= 64 ? 64 : 32, LD = row_len(DC), NT = DC / 32, NC = DC / 16;
-  constexpr int kShift = W == 4 ? 7 : 5;
-  __shared__ __align__(16) uint16_t sk[P * R * LD], sv[W == 1 ? 8 : P * R * LD];
+template <typename T, int DC, int COLS, bool VEC, int KIND>
+__global__ __launch_bounds__((Block<T, DC, COLS>::kThreads),
+                             (waves_for(regs_for<T, DC>(pieces<T>() + 3, 1, 110)))) void grad_q_kernel(const AttnArgs a) {
+  using B = Block<T, DC, COLS>;
+  constexpr int CT = B::CT, P = pieces<T>(), R = COLS > 32 && DC <= 64 ? 64 : 32, LD = row_len(DC);
+  using G = Geo<CT>;
+  constexpr int NC = DC / G::kStep, kRegs = Tile32<CT>::kRegs;
+  __shared__ __align__(16) uint16_t sk[P * R * LD], sv[P * R * LD];
   __shared__ int at_qk[DC], at_v[DC];
   __shared__ __align__(16) float spos[3 * R];
   Work w;
   Tile t;
-  if (!find_work(a, w) || !find_tile(a.qo, a.G, a.Nq, kShift, w.tile, t)) return;
+  if (!find_work(a, w) || !find_tile(a.qo, a.G, a.Nq, B::kShift, w.tile, t)) return;
   fill_table<DC>(at_qk, a.sqk, w.h);
   fill_table<DC>(at_v, a.sv, w.h);
   __syncthreads();
-  const int lane = threadIdx.x & 63, half = lane >> 5;
-  const int col = (threadIdx.x >> 6) * 32 + (lane & 31);
+  const int col = B::col();
   const bool mine = col < t.rows;
   const int64_t query = t.row0 + min(col, t.rows - 1);
   const int Dqk = a.sqk.D, Dv = a.sv.D;
-  const bool bias = a.slope != nullptr;
+  const bool bias = has_bias<KIND>(a);
   int64_t kb, ke;
   other_rows<R>(a.ko, t.g, a.Nk, w.part, a.nsplit, kb, ke);
-  Stage<T, DC, R, W, VEC> rk(a.k, a.ldk, at_qk, Dqk), rv(a.v, a.ldv, at_v, Dv);
-  StagePos<R, W> rp;
+  Stage<T, DC, R, B::kThreads, VEC> rk(a.k, a.ldk, at_qk, Dqk), rv(a.v, a.ldv, at_v, Dv);
+  StagePos<R, B::kThreads> rp;
   auto load = [&](int64_t k0) {
     const int valid = (int)(ke - k0 < R ? ke - k0 : R);
     rk.load(k0, valid);
     rv.load(k0, valid);
     if (bias) rp.load(a.kpos, k0, valid);
   };
-  if (kb < ke) load(kb);
+  constexpr bool kAhead = rows_ahead<T, DC, COLS>(false);
+  if (kAhead && kb < ke) load(kb);
   bf16x8 q[NC][P], g[NC][3];
+  own_row<T, DC, VEC, CT>(static_cast<const T*>(a.q) + query * a.ldq, at_qk, Dqk, q);
   float delta = 0.f;
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    Octet<T> o;
-    o.template load<VEC>(static_cast<const T*>(a.q) + query * a.ldq, at_qk, 16 * c + 8 * half, Dqk);
-    o.planes(q[c]);
     Octet<float> go, y;
-    go.template load<VEC>(a.go + query * a.sv.F, at_v, 16 * c + 8 * half, Dv);
-    y.template load<VEC>(a.o + query * a.sv.F, at_v, 16 * c + 8 * half, Dv);
+    go.template load<VEC>(a.go + query * a.sv.F, at_v, G::kStep * c + 8 * G::group(), Dv);
+    y.template load<VEC>(a.o + query * a.sv.F, at_v, G::kStep * c + 8 * G::group(), Dv);
     go.planes(g[c]);
 #pragma unroll
     for (int e = 0; e < 8; ++e) delta = fmaf(go.v[e], y.v[e], delta);
   }
-  delta = half_sum(delta);
-  if (mine && half == 0 && w.part == 0) a.delta[(int64_t)w.h * a.Nq + query] = delta;
+  delta = col_sum<CT>(delta);
+  if (mine && G::group() == 0 && w.part == 0) a.delta[(int64_t)w.h * a.Nq + query] = delta;
   const float m = a.stat[(int64_t)w.h * a.Nq + query], inv = a.stat[(int64_t)(a.H + w.h) * a.Nq + query];
-  const Place place = place_of(a, a.qpos, query, w.h);
-  const floatx4 m4 = {m, m, m, m}, delta4 = {delta, delta, delta, delta};
+  const Place place = place_of(a, bias, a.qpos, query, w.h);
+  const floatx4 delta4 = {delta, delta, delta, delta};
+  const Cap cap(a);
+  const SplitConsts consts;
+  const float c2 = uniform(a.scale * kLog2e);
   BiasSums sums;
-  floatx16 acc[NT];
-  zero(acc);
+  Result<CT, DC> acc;
+  acc.clear();
   for (int64_t k0 = kb; k0 < ke; k0 += R) {
     const int valid = (int)(ke - k0 < R ? ke - k0 : R);
+    if (!kAhead) load(k0);
     __syncthreads();
     rk.put(sk, k0, valid);
-    if constexpr (W == 4) rv.put(sv, k0, valid);
+    rv.put(sv, k0, valid);
     if (bias) rp.put(spos);
     __syncthreads();
-    if (W == 4 && k0 + R < ke) {
+    if (kAhead && k0 + R < ke) {
       load(k0 + R);
       __builtin_amdgcn_sched_barrier(0);
     }
-    for (int sub = 0; sub < (W == 1 ? 1 : valid); sub += 32) {
-      floatx16 s, ds;
-#pragma unroll
-      for (int r = 0; r < 16; ++r) s[r] = ds[r] = 0.f;
+    for (int sub = 0; sub < valid; sub += 32) {
+      Tile32<CT> s, ds;
+      s.clear();
+      ds.clear();
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        bf16x8 f[P];
-        left_rows(rk, sk, sub, c, f);
-        mul<P, P>(f, q[c], s);
-        left_rows(rv, sv, sub, c, f);
-        mul<P, 3>(f, g[c], ds);
+        add_scores<CT, P, P, DC, R>(sk, sub, c, q[c], s);
+        add_scores<CT, P, 3, DC, R>(sv, sub, c, g[c], ds);
       }
-      if (W == 1 && k0 + R < ke) load(k0 + R);
-      if (valid - sub < 32) {
-        // keys that are not there: a weight of zero
+      with_kind<KIND>(a, cap, s, [&](auto kind, auto bs) {
+        grad_tile<decltype(kind)::value, decltype(bs)::value, R>(
+            cap, c2, s, ds, spos, sub, place, sums,
+            [&](int q4) {  // keys that are not there: a weight of zero
+              floatx4 v;
 #pragma unroll
-        for (int r = 0; r < 16; ++r)
-          if (sub + acc_row(r) >= valid) s[r] = ds[r] = 0.f;
-        with_kind(a, [&](auto cap, auto bs) {
-          grad_tile<decltype(cap)::value, decltype(bs)::value, R>(
-              a, s, ds, spos, sub, place, sums,
-              [&](int q4) {
-                floatx4 v;
+              for (int e = 0; e < 4; ++e) v[e] = sub + G::first_row(q4) + e < valid ? m : INFINITY;
+              return v;
+            },
+            [&](int) { return delta4; });
+      });
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = sub + acc_row(4 * q4 + e) < valid ? m : INFINITY;
-                return v;
-              },
-              [&](int) { return delta4; });
-        });
-      } else {
-        with_kind(a, [&](auto cap, auto bs) {
-          grad_tile<decltype(cap)::value, decltype(bs)::value, R>(
-              a, s, ds, spos, sub, place, sums, [&](int) { return m4; }, [&](int) { return delta4; });
-        });
-      }
-#pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
-        float pv[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) pv[e] = ds[8 * kk + e];
+      for (int st = 0; st < kRegs / 8; ++st) {
         bf16x8 p[3];
-        split<3>(pv, p);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          bf16x8 f[P];
-          cols_frag<P, DC, R>(sk, sub + 16 * kk, 32 * n, f);
-          mul<P, 3>(f, p, acc[n]);
-        }
+        weights_frag<3>(ds, st, p, consts);
+        acc.template add<P, 3, R>(sk, sub, st, p);
       }
     }
   }
-  put_pos(a, w, a.Nq, query, mine, sums, inv);
-  if (a.part_slope) {
+  put_pos<CT>(a, bias, w, a.Nq, query, mine, sums, inv);
+  if (bias && a.part_slope) {
     // sum dS d = sum dS (d - mean d) as far as the sum of dS is zero, which it is but for
     // rounding: the join takes sum dS d - sum dS * sum P d, which does not see that rounding
-    sums.sd = half_sum(sums.sd);
-    sums.s = half_sum(sums.s);
-    sums.pd = half_sum(sums.pd);
-    if (mine && half == 0) {
+    sums.sd = col_sum<CT>(sums.sd);
+    sums.s = col_sum<CT>(sums.s);
+    sums.pd = col_sum<CT>(sums.pd);
+    if (mine && G::group() == 0) {
       float* o = a.part_slope + (((int64_t)w.part * a.H + w.h) * a.Nq + query) * 3;
       o[0] = sums.sd * inv;
       o[1] = sums.s * inv;
       o[2] = sums.pd * inv;
     }
   }
-  if (a.gq && mine) put_column<DC, VEC>(acc, a.scale * inv, at_qk, Dqk, a.gq + ((int64_t)w.part * a.Nq + query) * a.ldgq);
+  if (a.gq && mine)
+    acc.template put<VEC>(a.scale * inv, at_qk, Dqk, a.gq + ((int64_t)w.part * a.Nq + query) * a.ldgq);
 }
 
 // ---- gradients of keys and values --------------------------------------------------------
 
-// fp32 operands of more than 128 values leave no registers to hold the next rows in.
+// Wide heads take the two gradients in two launches: the operands and sums of
+// both are 200 registers of the 256 that two waves per SIMD leave each, and what
+// went to scratch memory cost more than doing the scores twice (8192 nodes of
+// 128x0e+128x1o+128x2e, 8 heads: 952 us in one launch, 710 in two).
+enum KvPart { kBoth, kValues, kKeys };
 template <typename T, int DC>
-constexpr bool kv_ahead() {
-  return sizeof(T) == 2 || DC <= 128;
+constexpr bool kv_in_two() {
+  return DC > (sizeof(T) == 4 ? 96 : 160);
 }
 
-template <typename T, int DC, int W, bool VEC>
-__global__ __launch_bounds__(64 * W, waves_for(DC / 4 * 2 * pieces<T>() + DC + 80)) void grad_kv_kernel(const AttnArgs a) {
-  constexpr int P = pieces<T>(), R = W == 4 && DC <= 64 && P == 1 ? 64 : 32, LD = row_len(DC), NT = DC / 32, NC = DC / 16;
-  constexpr int kShift = W == 4 ? 7 : 5;
-  constexpr bool kAhead = W == 4 && kv_ahead<T, DC>();
+template <typename T, int DC, int COLS, bool VEC, int KIND, int PART>
+__global__ __launch_bounds__((Block<T, DC, COLS>::kThreads),
+                             (waves_for(regs_for<T, DC>((PART == kValues ? 1 : 2) * pieces<T>(), PART == kBoth ? 2 : 1, 110)))) void grad_kv_kernel(const AttnArgs a) {
+  using B = Block<T, DC, COLS>;
+  constexpr int CT = B::CT, P = pieces<T>(), R = COLS > 32 && DC <= 64 && P == 1 ? 64 : 32, LD = row_len(DC);
+  using G = Geo<CT>;
+  constexpr int NC = DC / G::kStep, kRegs = Tile32<CT>::kRegs;
   __shared__ __align__(16) uint16_t sq[P * R * LD], sg[3 * R * LD];
   __shared__ int at_qk[DC], at_v[DC];
   __shared__ __align__(16) float spos[3 * R], sl[R], sd[R];
   Work w;
   Tile t;
-  if (!find_work(a, w) || !find_tile(a.ko, a.G, a.Nk, kShift, w.tile, t)) return;
+  if (!find_work(a, w) || !find_tile(a.ko, a.G, a.Nk, B::kShift, w.tile, t)) return;
   fill_table<DC>(at_qk, a.sqk, w.h);
   fill_table<DC>(at_v, a.sv, w.h);
   __syncthreads();
-  const int lane = threadIdx.x & 63, half = lane >> 5;
-  const int col = (threadIdx.x >> 6) * 32 + (lane & 31);
+  const int col = B::col();
   const bool mine = col < t.rows;
   const int64_t key = t.row0 + min(col, t.rows - 1);
   const int Dqk = a.sqk.D, Dv = a.sv.D;
-  const bool bias = a.slope != nullptr;
+  const bool bias = has_bias<KIND>(a);
   int64_t qb, qe;
   other_rows<R>(a.qo, t.g, a.Nq, w.part, a.nsplit, qb, qe);
   // rows of grad_out are taken times 1 / l, so that the weights need no factor of their own
   const float *ref = a.stat + (int64_t)w.h * a.Nq, *inv = ref + (int64_t)a.H * a.Nq, *delta = a.delta + (int64_t)w.h * a.Nq;
-  Stage<T, DC, R, W, VEC> rq(a.q, a.ldq, at_qk, Dqk);
-  Stage<float, DC, R, W, VEC> rg(a.go, a.sv.F, at_v, Dv, inv);
-  StagePos<R, W> rp;
+  Stage<T, DC, R, B::kThreads, VEC> rq(a.q, a.ldq, at_qk, Dqk);
+  Stage<float, DC, R, B::kThreads, VEC> rg(a.go, a.sv.F, at_v, Dv, inv);
+  StagePos<R, B::kThreads> rp;
   float row_m = INFINITY, row_d = 0.f;
   auto load = [&](int64_t q0) {
     const int valid = (int)(qe - q0 < R ? qe - q0 : R);
@@ -914,25 +1073,23 @@ __global__ __launch_bounds__(64 * W, waves_for(DC / 4 * 2 * pieces<T>() + DC + 8
       row_d = delta[q0 + threadIdx.x] * inv[q0 + threadIdx.x];
     }
   };
+  constexpr bool kAhead = rows_ahead<T, DC, COLS>(false);
   if (kAhead && qb < qe) load(qb);
   bf16x8 k[NC][P], v[NC][P];
-#pragma unroll
-  for (int c = 0; c < NC; ++c) {
-    Octet<T> o;
-    o.template load<VEC>(static_cast<const T*>(a.k) + key * a.ldk, at_qk, 16 * c + 8 * half, Dqk);
-    o.planes(k[c]);
-    o.template load<VEC>(static_cast<const T*>(a.v) + key * a.ldv, at_v, 16 * c + 8 * half, Dv);
-    o.planes(v[c]);
-  }
-  const Place place = place_of(a, a.kpos, key, w.h);
+  own_row<T, DC, VEC, CT>(static_cast<const T*>(a.k) + key * a.ldk, at_qk, Dqk, k);
+  if constexpr (PART != kValues) own_row<T, DC, VEC, CT>(static_cast<const T*>(a.v) + key * a.ldv, at_v, Dv, v);
+  const Place place = place_of(a, bias, a.kpos, key, w.h);
+  const Cap cap(a);
+  const SplitConsts consts;
+  const float c2 = uniform(a.scale * kLog2e);
   BiasSums sums;
-  floatx16 gv[NT], gk[NT];
-  zero(gv);
-  zero(gk);
+  Result<CT, DC> gv, gk;
+  gv.clear();
+  gk.clear();
   for (int64_t q0 = qb; q0 < qe; q0 += R) {
     const int valid = (int)(qe - q0 < R ? qe - q0 : R);
+    if (!kAhead) load(q0);
     __syncthreads();
-    if constexpr (!kAhead) load(q0);
     rq.put(sq, q0, valid);
     rg.put(sg, q0, valid);
     if (bias) rp.put(spos);
@@ -945,50 +1102,50 @@ __global__ __launch_bounds__(64 * W, waves_for(DC / 4 * 2 * pieces<T>() + DC + 8
       load(q0 + R);
       __builtin_amdgcn_sched_barrier(0);
     }
-    for (int sub = 0; sub < (W == 1 ? 1 : valid); sub += 32) {
-      floatx16 s, ds;
-#pragma unroll
-      for (int r = 0; r < 16; ++r) s[r] = ds[r] = 0.f;
+    for (int sub = 0; sub < valid; sub += 32) {
+      Tile32<CT> s, ds;
+      s.clear();
+      ds.clear();
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        bf16x8 f[P], f3[3];
-        left_rows(rq, sq, sub, c, f);
-        mul<P, P>(f, k[c], s);
-        left_rows(rg, sg, sub, c, f3);
-        mul<3, P>(f3, v[c], ds);
+        add_scores<CT, P, P, DC, R>(sq, sub, c, k[c], s);
+        if constexpr (PART != kValues) add_scores<CT, 3, P, DC, R>(sg, sub, c, v[c], ds);
       }
-      with_kind(a, [&](auto cap, auto bs) {
-        grad_tile<decltype(cap)::value, decltype(bs)::value, R>(
-            a, s, ds, spos, sub, place, sums,
-            [&](int q4) { return *reinterpret_cast<const floatx4*>(sl + sub + 8 * q4 + 4 * half); },
-            [&](int q4) { return *reinterpret_cast<const floatx4*>(sd + sub + 8 * q4 + 4 * half); });
+      with_kind<KIND>(a, cap, s, [&](auto kind, auto bs) {
+        if constexpr (PART == kValues) {
+          score_tile<decltype(kind)::value, decltype(bs)::value, R>(cap, c2, s, spos, sub, place);
+          const float unit = decltype(kind)::value == kNoCap && !decltype(bs)::value ? c2 : 1.f;
+#pragma unroll
+          for (int q4 = 0; q4 < G::kQuads; ++q4) {
+            const floatx4 m4 = *reinterpret_cast<const floatx4*>(sl + sub + G::first_row(q4));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s.set(4 * q4 + e, exp2_fast(fmaf(s.get(4 * q4 + e), unit, -m4[e])));
+          }
+          return;
+        }
+        grad_tile<decltype(kind)::value, decltype(bs)::value, R>(
+            cap, c2, s, ds, spos, sub, place, sums,
+            [&](int q4) { return *reinterpret_cast<const floatx4*>(sl + sub + G::first_row(q4)); },
+            [&](int q4) { return *reinterpret_cast<const floatx4*>(sd + sub + G::first_row(q4)); });
       });
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
-        float pv[8], dv[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          pv[e] = s[8 * kk + e];
-          dv[e] = ds[8 * kk + e];
+      for (int st = 0; st < kRegs / 8; ++st) {
+        bf16x8 p[3];
+        if constexpr (PART != kKeys) {
+          weights_frag<3>(s, st, p, consts);
+          gv.template add<3, 3, R>(sg, sub, st, p);
         }
-        bf16x8 p[3], dp[3];
-        split<3>(pv, p);
-        split<3>(dv, dp);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          bf16x8 f3[3], f[P];
-          cols_frag<3, DC, R>(sg, sub + 16 * kk, 32 * n, f3);
-          mul<3, 3>(f3, p, gv[n]);
-          cols_frag<P, DC, R>(sq, sub + 16 * kk, 32 * n, f);
-          mul<P, 3>(f, dp, gk[n]);
+        if constexpr (PART != kValues) {
+          weights_frag<3>(ds, st, p, consts);
+          gk.template add<P, 3, R>(sq, sub, st, p);
         }
       }
     }
   }
-  put_pos(a, w, a.Nk, key, mine, sums, 1.f);
+  if constexpr (PART != kValues) put_pos<CT>(a, bias, w, a.Nk, key, mine, sums, 1.f);
   if (!mine) return;
-  if (a.gk) put_column<DC, VEC>(gk, a.scale, at_qk, Dqk, a.gk + ((int64_t)w.part * a.Nk + key) * a.ldgk);
-  if (a.gv) put_column<DC, VEC>(gv, 1.f, at_v, Dv, a.gv + ((int64_t)w.part * a.Nk + key) * a.ldgv);
+  if (PART != kValues && a.gk) gk.template put<VEC>(a.scale, at_qk, Dqk, a.gk + ((int64_t)w.part * a.Nk + key) * a.ldgk);
+  if (PART != kKeys && a.gv) gv.template put<VEC>(1.f, at_v, Dv, a.gv + ((int64_t)w.part * a.Nk + key) * a.ldgv);
 }
 
 }  // namespace attn
