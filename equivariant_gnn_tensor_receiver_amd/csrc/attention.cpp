@@ -105,15 +105,15 @@ tpconv_status plan_of(const tpconv_attention_s& h, int op, const tpconv_attentio
   const int D = std::max(h.qk.D, h.v.D);
   Taker take;
   if (op == TPCONV_OP_FORWARD) {
-    p.fwd = attn_shape(D, Nq, Nk, b.num_graphs, h.heads);
+    p.fwd = attn_shape(D, Nq, Nk, b.num_graphs, h.heads, h.y_dtype == TPCONV_F32);
     if (too_many(p.fwd, h.heads)) return TPCONV_ERROR_UNSUPPORTED;
     if (p.fwd.nsplit > 1) {
       p.part_o = take((size_t)p.fwd.nsplit * Nq * h.v.F);
       p.part_ml = take((size_t)p.fwd.nsplit * H * Nq * 2);
     }
   } else {
-    p.q = attn_shape(D, Nq, Nk, b.num_graphs, h.heads);
-    p.kv = attn_shape(D, Nk, Nq, b.num_graphs, h.heads);
+    p.q = attn_shape(D, Nq, Nk, b.num_graphs, h.heads, true);
+    p.kv = attn_shape(D, Nk, Nq, b.num_graphs, h.heads, true);
     if (too_many(p.q, h.heads) || too_many(p.kv, h.heads)) return TPCONV_ERROR_UNSUPPORTED;
     p.delta = take((size_t)H * Nq);
     if (p.q.nsplit > 1) p.gq = take((size_t)p.q.nsplit * Nq * h.qk.F);

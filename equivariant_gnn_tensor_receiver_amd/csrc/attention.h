@@ -77,8 +77,8 @@ struct AttnShape {
   int nsplit;
   int64_t tiles;
 };
-// The shape of a launch whose rows are `rows` and whose long axis is `other`.
-AttnShape attn_shape(int D, int64_t rows, int64_t other, int64_t graphs, int heads);
+// The shape of a launch whose rows are `rows` and whose long axis is `other`; exact: its results stay fp32.
+AttnShape attn_shape(int D, int64_t rows, int64_t other, int64_t graphs, int heads, bool exact);
 
 hipError_t launch_attn_forward(AttnArgs& a, const AttnShape& s, hipStream_t st);
 hipError_t launch_attn_combine(AttnArgs& a, const AttnShape& s, hipStream_t st);

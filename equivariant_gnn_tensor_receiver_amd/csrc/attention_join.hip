@@ -25,6 +25,10 @@ constexpr int kWidth[kClasses] = {32, 64, 96, 128, 160, 256};
 const ClassLauncher kLaunch[kClasses] = {launch_attn_class_32,  launch_attn_class_64,  launch_attn_class_96,
                                          launch_attn_class_128, launch_attn_class_160, launch_attn_class_256};
 
+__device__ __forceinline__ bool covered(const int32_t* off, int G, int64_t N, int64_t row) {
+  return !off || (row >= clamp_row(off[0], N) && row < clamp_row(off[G], N));
+}
+
 // Head of feature f of a side.
 __device__ __forceinline__ int head_of(const AttnSide& s, int f) {
   int i = 0;
@@ -32,52 +36,61 @@ __device__ __forceinline__ int head_of(const AttnSide& s, int f) {
   return (f - s.ir[i].off) % s.ir[i].mul / s.ir[i].cph;
 }
 
-// out = sum over the parts of w o / sum of w l, w = 2^(m - largest m).  One block per 32 rows.
+// out = sum over the parts of w o / sum of w l, w = 2^(m - largest m).  A block takes one
+// query at a time: its threads first turn the parts' (m, l) into factors w / sum of w l
+// per part and head, then add the parts of a feature each.
+constexpr int kMaxParts = 64, kCombineHeads = 64;  // heads per step
 __global__ __launch_bounds__(256) void combine_kernel(const AttnArgs a) {
-  Tile t;
-  if (!find_tile(a.qo, a.G, a.Nq, 5, blockIdx.x, t)) return;
-  const int F = a.sv.F;
-  for (int i = threadIdx.x; i < t.rows * F; i += 256) {
-    const int row = i / F, f = i - row * F;
-    const int64_t query = t.row0 + row;
-    const int h = head_of(a.sv, f);
-    float top = -INFINITY;
-    for (int p = 0; p < a.nsplit; ++p) top = fmaxf(top, a.part_ml[2 * (((int64_t)p * a.H + h) * a.Nq + query)]);
-    const float ref = top == -INFINITY ? 0.f : top;
-    float l = 0.f, o = 0.f;
-    for (int p = 0; p < a.nsplit; ++p) {
-      const float* ml = a.part_ml + 2 * (((int64_t)p * a.H + h) * a.Nq + query);
-      if (ml[0] == -INFINITY && ml[1] == 0.f) continue;  // a part without keys
-      const float w = exp2_fast(ml[0] - ref);
-      l = fmaf(w, ml[1], l);
-      o = fmaf(w, a.part_o[((int64_t)p * a.Nq + query) * F + f], o);
+  __shared__ float f[kCombineHeads * kMaxParts];
+  const int F = a.sv.F, S = a.nsplit;
+  for (int64_t query = blockIdx.x; query < a.Nq; query += gridDim.x) {
+    if (!covered(a.qo, a.G, a.Nq, query)) continue;
+    for (int h0 = 0; h0 < a.H; h0 += kCombineHeads) {
+      const int heads = min(kCombineHeads, a.H - h0);
+      // a wave per head: lane p holds part p
+      for (int hh = threadIdx.x >> 6; hh < heads; hh += 4) {
+        const int p = lane_id(), h = h0 + hh;
+        float m = -INFINITY, l = 0.f;
+        if (p < S) {
+          const float* ml = a.part_ml + 2 * (((int64_t)p * a.H + h) * a.Nq + query);
+          m = ml[0];
+          l = ml[1];
+        }
+        float top = m;
+#pragma unroll
+        for (int i = 32; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor(top, i));
+        const bool none = m == -INFINITY && l == 0.f;  // a part without keys
+        const float w = none ? 0.f : exp2_fast(m - (top == -INFINITY ? 0.f : top));
+        float sum = w * l;
+#pragma unroll
+        for (int i = 32; i > 0; i >>= 1) sum += __shfl_xor(sum, i);
+        const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+        f[hh * kMaxParts + p] = none ? 0.f : w * inv;
+        if (a.stat && p == 0) {
+          a.stat[(int64_t)h * a.Nq + query] = top;
+          a.stat[(int64_t)(a.H + h) * a.Nq + query] = inv;
+        }
+      }
+      __syncthreads();
+      for (int i = threadIdx.x; i < F; i += 256) {
+        const int h = head_of(a.sv, i);
+        if (h < h0 || h >= h0 + heads) continue;
+        const float* w = f + (h - h0) * kMaxParts;
+        float o = 0.f;
+#pragma unroll 8
+        for (int p = 0; p < S; ++p) {
+          const float v = a.part_o[((int64_t)p * a.Nq + query) * F + i];
+          o = w[p] != 0.f ? fmaf(w[p], v, o) : o;
+        }
+        if (a.out32) a.out32[query * F + i] = o;
+        if (a.y_bf16)
+          static_cast<uint16_t*>(a.out)[query * F + i] = __builtin_bit_cast(uint16_t, (__bf16)o);
+        else
+          static_cast<float*>(a.out)[query * F + i] = o;
+      }
+      __syncthreads();
     }
-    o *= l > 0.f || l != l ? 1.f / l : 0.f;
-    if (a.out32) a.out32[query * F + f] = o;
-    if (a.y_bf16)
-      static_cast<uint16_t*>(a.out)[query * F + f] = __builtin_bit_cast(uint16_t, (__bf16)o);
-    else
-      static_cast<float*>(a.out)[query * F + f] = o;
   }
-  if (!a.stat) return;
-  for (int i = threadIdx.x; i < t.rows * a.H; i += 256) {
-    const int h = i / t.rows;
-    const int64_t query = t.row0 + (i - h * t.rows);
-    float top = -INFINITY, l = 0.f;
-    for (int p = 0; p < a.nsplit; ++p) top = fmaxf(top, a.part_ml[2 * (((int64_t)p * a.H + h) * a.Nq + query)]);
-    const float ref = top == -INFINITY ? 0.f : top;
-    for (int p = 0; p < a.nsplit; ++p) {
-      const float* ml = a.part_ml + 2 * (((int64_t)p * a.H + h) * a.Nq + query);
-      if (ml[0] == -INFINITY && ml[1] == 0.f) continue;
-      l = fmaf(exp2_fast(ml[0] - ref), ml[1], l);
-    }
-    a.stat[(int64_t)h * a.Nq + query] = top;
-    a.stat[(int64_t)(a.H + h) * a.Nq + query] = l > 0.f || l != l ? 1.f / l : 0.f;
-  }
-}
-
-__device__ __forceinline__ bool covered(const int32_t* off, int G, int64_t N, int64_t row) {
-  return !off || (row >= clamp_row(off[0], N) && row < clamp_row(off[G], N));
 }
 
 // Sums of parts [n][rows][F] into rows of stride ld, in order.
@@ -153,7 +166,7 @@ hipError_t launch_class(int kind, AttnArgs& a, const AttnShape& s, hipStream_t s
 
 }  // namespace
 
-AttnShape attn_shape(int D, int64_t rows, int64_t other, int64_t graphs, int heads) {
+AttnShape attn_shape(int D, int64_t rows, int64_t other, int64_t graphs, int heads, bool exact) {
   AttnShape s;
   s.cls = 0;
   while (kWidth[s.cls] < D) ++s.cls;
@@ -161,10 +174,15 @@ AttnShape attn_shape(int D, int64_t rows, int64_t other, int64_t graphs, int hea
   s.cols = rows / g >= 96 ? 128 : attn_small_cols(kWidth[s.cls]);
   const int64_t m = s.cols;
   s.tiles = rows / m + g;
-  // too few blocks for the 256 CUs: cut the long axis, 64 rows of it at least per part
+  // too few blocks for the 256 CUs: cut the long axis, 64 rows of it at least per part, into as many
+  // blocks as the CUs hold at once (16 queries over 32768 keys of 288 values, 4 heads: 512 blocks
+  // 62 us, 768 53, 1024 64, 2048 71)
   const int64_t blocks = std::max<int64_t>((rows + m - 1) / m, std::min(rows, g)) * heads;
-  const int64_t most = std::max<int64_t>(1, other / g / 64), enough = s.cols < 128 ? 2048 : 512;
-  s.nsplit = (int)std::min<int64_t>(std::min<int64_t>(64, most), std::max<int64_t>(1, enough / std::max<int64_t>(1, blocks)));
+  const int64_t most = std::max<int64_t>(1, other / g / 64), enough = s.cols < 128 ? 768 : 512;
+  s.nsplit = (int)std::min<int64_t>(std::min<int64_t>(kMaxParts, most), std::max<int64_t>(1, enough / std::max<int64_t>(1, blocks)));
+  // fp32 sums along more than 4096 rows: in parts too, since the matrix instructions' roundings add up
+  // (16384 nodes in one graph, fp32, 4 heads of 64: gradients off by 4e-6 in one run of sums, 8e-7 in four)
+  if (exact) s.nsplit = (int)std::max<int64_t>(s.nsplit, std::min<int64_t>(8, (other / g + 4095) / 4096));
   return s;
 }
 
@@ -174,8 +192,8 @@ hipError_t launch_attn_grad_kv(AttnArgs& a, const AttnShape& s, hipStream_t st) 
 
 hipError_t launch_attn_combine(AttnArgs& a, const AttnShape& s, hipStream_t st) {
   TimingScope ts(kcAttention, st);
-  const int64_t tiles = a.Nq / 32 + std::max(1, a.G);
-  hipLaunchKernelGGL(combine_kernel, dim3((unsigned)tiles), dim3(256), 0, st, a);
+  a.nsplit = s.nsplit;
+  hipLaunchKernelGGL(combine_kernel, dim3((unsigned)std::min<int64_t>(a.Nq, 1 << 16)), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 

@@ -432,49 +432,57 @@ struct Result {
 // host.  The graph is found by a search with 64 probes per step.
 struct Tile {
   int g;
-  int64_t row0;  // first row
-  int rows;      // rows of the tile that are in the graph
+  int64_t row0;        // first row
+  int rows;            // rows of the tile that are in the graph
+  int64_t begin, end;  // the graph's rows
 };
 __device__ __forceinline__ int64_t clamp_row(int32_t v, int64_t N) { return v < 0 ? 0 : v > N ? N : v; }
 __device__ __forceinline__ bool find_tile(const int32_t* off, int G, int64_t N, int shift, int64_t t, Tile& o) {
   const int64_t M = int64_t(1) << shift;
-  int64_t b = 0, e = N, first = 0;
   o.g = 0;
+  o.begin = 0;
+  o.end = N;
+  int64_t first = 0;
   if (off) {
-    const int lane = threadIdx.x & 63;
+    const int lane = lane_id();
     int lo = 0, n = G;  // the last graph of [lo, lo + n) that starts at or before t
     while (true) {
       const int step = (n + 63) >> 6;
       const int i = lane * step;
       const int g = lo + (i < n ? i : 0);
-      const uint64_t m = __ballot(i < n && (clamp_row(off[g], N) >> shift) + g <= t);
+      const int32_t v = off[g];
+      const uint64_t m = __ballot(i < n && (clamp_row(v, N) >> shift) + g <= t);
       const int c = __popcll(m);
       if (c == 0) return false;  // before the first graph
       lo += (c - 1) * step;
-      n = min(step, n - (c - 1) * step);
-      if (step == 1) break;
+      const int left = n - (c - 1) * step;
+      if (step == 1) {
+        // one lane per graph: its rows begin at lane c - 1's value and end at the next one's
+        o.begin = clamp_row(__builtin_amdgcn_readlane(v, c - 1), N);
+        o.end = clamp_row(c < n && c < 64 ? __builtin_amdgcn_readlane(v, c < 64 ? c : 63) : off[lo + 1], N);
+        break;
+      }
+      n = min(step, left);
     }
     o.g = __builtin_amdgcn_readfirstlane(lo);
-    b = clamp_row(off[o.g], N);
-    e = clamp_row(off[o.g + 1], N);
-    first = (b >> shift) + o.g;
+    first = (o.begin >> shift) + o.g;
     if (t < first) return false;  // (offsets that decrease)
   }
-  o.row0 = b + ((t - first) << shift);
-  if (o.row0 >= e) return false;
-  o.rows = (int)(e - o.row0 < M ? e - o.row0 : M);
+  o.row0 = o.begin + ((t - first) << shift);
+  if (o.row0 >= o.end) return false;
+  o.rows = (int)(o.end - o.row0 < M ? o.end - o.row0 : M);
   return true;
 }
 
 // Rows [b, e) of graph g's other side, cut to part `part` of `nsplit` (whole tiles of R rows each).
 template <int R>
-__device__ __forceinline__ void other_rows(const int32_t* off, int g, int64_t N, int part, int nsplit, int64_t& b,
-                                           int64_t& e) {
-  b = 0;
-  e = N;
-  if (off) {
-    b = clamp_row(off[g], N);
-    e = clamp_row(off[g + 1], N);
+__device__ __forceinline__ void other_rows(const int32_t* off, const Tile& t, bool self, int64_t N, int part, int nsplit,
+                                           int64_t& b, int64_t& e) {
+  b = self ? t.begin : 0;
+  e = self ? t.end : N;
+  if (off && !self) {
+    b = clamp_row(off[t.g], N);
+    e = clamp_row(off[t.g + 1], N);
   }
   if (nsplit > 1) {
     const int64_t len = e > b ? e - b : 0;
@@ -750,11 +758,12 @@ constexpr int regs_for(int right, int results, int rest) {
 }
 
 // Whether a kernel holds the other side's next rows in registers while it works on
-// the present ones: not where wide heads leave none for it, nor for small graphs,
-// which take one or two steps.
+// the present ones: not where wide heads leave none for it, nor in the backward of
+// small graphs, which take one or two steps.  (The first rows are on their way before
+// the own row is wherever heads are not wide.)
 template <typename T, int DC, int COLS>
 constexpr bool rows_ahead(bool forward) {
-  return COLS == 128 && (forward ? DC <= 160 : DC <= 96);
+  return forward ? DC <= (COLS == 128 ? 160 : 96) : COLS == 128 && DC <= 96;
 }
 
 // ---- forward ----------------------------------------------------------------------
@@ -786,7 +795,7 @@ __global__ __launch_bounds__((Block<T, DC, COLS>::kThreads), (waves_for(regs_for
   const int Dqk = a.sqk.D, Dv = a.sv.D;
   const bool bias = has_bias<KIND>(a);
   int64_t kb, ke;
-  other_rows<R>(a.ko, t.g, a.Nk, w.part, a.nsplit, kb, ke);
+  other_rows<R>(a.ko, t, a.self, a.Nk, w.part, a.nsplit, kb, ke);
   Stage<T, DC, R, B::kThreads, VEC> rk(a.k, a.ldk, at_qk, Dqk), rv(a.v, a.ldv, at_v, Dv);
   StagePos<R, B::kThreads> rp;
   auto load = [&](int64_t k0) {
@@ -795,8 +804,8 @@ __global__ __launch_bounds__((Block<T, DC, COLS>::kThreads), (waves_for(regs_for
     rv.load(k0, valid);
     if (bias) rp.load(a.kpos, k0, valid);
   };
-  constexpr bool kAhead = rows_ahead<T, DC, COLS>(true);
-  if (kAhead && kb < ke) load(kb);
+  constexpr bool kAhead = rows_ahead<T, DC, COLS>(true), kFirst = kAhead || DC <= 96;
+  if (kFirst && kb < ke) load(kb);
   bf16x8 q[NC][P];
   own_row<T, DC, VEC, CT>(static_cast<const T*>(a.q) + query * a.ldq, at_qk, Dqk, q);
   const Place place = place_of(a, bias, a.qpos, query, w.h);
@@ -811,7 +820,7 @@ __global__ __launch_bounds__((Block<T, DC, COLS>::kThreads), (waves_for(regs_for
   float m = -INFINITY, l = 0.f;
   for (int64_t k0 = kb; k0 < ke; k0 += R) {
     const int valid = (int)(ke - k0 < R ? ke - k0 : R);
-    if (!kAhead) load(k0);
+    if (!kAhead && (!kFirst || k0 > kb)) load(k0);
     __syncthreads();
     rk.put(sk, k0, valid);
     rv.put(sv, k0, valid);
@@ -851,12 +860,14 @@ __global__ __launch_bounds__((Block<T, DC, COLS>::kThreads), (waves_for(regs_for
         m = next;
       }
       const float ref = m == -INFINITY ? 0.f : m;
+      float here = 0.f;  // (a tile's weights before the running sum: fewer roundings at its size)
 #pragma unroll
       for (int r = 0; r < kRegs; ++r) {
         const float p = exp2_fast(fmaf(s.get(r), unit, -ref));
         s.set(r, p);
-        l += p;
+        here += p;
       }
+      l += here;
 #pragma unroll
       for (int st = 0; st < kRegs / 8; ++st) {
         bf16x8 p[PP];
@@ -928,7 +939,7 @@ __global__ __launch_bounds__((Block<T, DC, COLS>::kThreads),
   const int Dqk = a.sqk.D, Dv = a.sv.D;
   const bool bias = has_bias<KIND>(a);
   int64_t kb, ke;
-  other_rows<R>(a.ko, t.g, a.Nk, w.part, a.nsplit, kb, ke);
+  other_rows<R>(a.ko, t, a.self, a.Nk, w.part, a.nsplit, kb, ke);
   Stage<T, DC, R, B::kThreads, VEC> rk(a.k, a.ldk, at_qk, Dqk), rv(a.v, a.ldv, at_v, Dv);
   StagePos<R, B::kThreads> rp;
   auto load = [&](int64_t k0) {
@@ -937,8 +948,8 @@ __global__ __launch_bounds__((Block<T, DC, COLS>::kThreads),
     rv.load(k0, valid);
     if (bias) rp.load(a.kpos, k0, valid);
   };
-  constexpr bool kAhead = rows_ahead<T, DC, COLS>(false);
-  if (kAhead && kb < ke) load(kb);
+  constexpr bool kAhead = rows_ahead<T, DC, COLS>(false), kFirst = kAhead || DC <= 96;
+  if (kFirst && kb < ke) load(kb);
   bf16x8 q[NC][P], g[NC][3];
   own_row<T, DC, VEC, CT>(static_cast<const T*>(a.q) + query * a.ldq, at_qk, Dqk, q);
   float delta = 0.f;
@@ -964,7 +975,7 @@ __global__ __launch_bounds__((Block<T, DC, COLS>::kThreads),
   acc.clear();
   for (int64_t k0 = kb; k0 < ke; k0 += R) {
     const int valid = (int)(ke - k0 < R ? ke - k0 : R);
-    if (!kAhead) load(k0);
+    if (!kAhead && (!kFirst || k0 > kb)) load(k0);
     __syncthreads();
     rk.put(sk, k0, valid);
     rv.put(sv, k0, valid);
@@ -1054,7 +1065,7 @@ __global__ __launch_bounds__((Block<T, DC, COLS>::kThreads),
   const int Dqk = a.sqk.D, Dv = a.sv.D;
   const bool bias = has_bias<KIND>(a);
   int64_t qb, qe;
-  other_rows<R>(a.qo, t.g, a.Nq, w.part, a.nsplit, qb, qe);
+  other_rows<R>(a.qo, t, a.self, a.Nq, w.part, a.nsplit, qb, qe);
   // rows of grad_out are taken times 1 / l, so that the weights need no factor of their own
   const float *ref = a.stat + (int64_t)w.h * a.Nq, *inv = ref + (int64_t)a.H * a.Nq, *delta = a.delta + (int64_t)w.h * a.Nq;
   Stage<T, DC, R, B::kThreads, VEC> rq(a.q, a.ldq, at_qk, Dqk);
@@ -1073,8 +1084,8 @@ __global__ __launch_bounds__((Block<T, DC, COLS>::kThreads),
       row_d = delta[q0 + threadIdx.x] * inv[q0 + threadIdx.x];
     }
   };
-  constexpr bool kAhead = rows_ahead<T, DC, COLS>(false);
-  if (kAhead && qb < qe) load(qb);
+  constexpr bool kAhead = rows_ahead<T, DC, COLS>(false), kFirst = kAhead || DC <= 96;
+  if (kFirst && qb < qe) load(qb);
   bf16x8 k[NC][P], v[NC][P];
   own_row<T, DC, VEC, CT>(static_cast<const T*>(a.k) + key * a.ldk, at_qk, Dqk, k);
   if constexpr (PART != kValues) own_row<T, DC, VEC, CT>(static_cast<const T*>(a.v) + key * a.ldv, at_v, Dv, v);
@@ -1088,7 +1099,7 @@ __global__ __launch_bounds__((Block<T, DC, COLS>::kThreads),
   gk.clear();
   for (int64_t q0 = qb; q0 < qe; q0 += R) {
     const int valid = (int)(qe - q0 < R ? qe - q0 : R);
-    if (!kAhead) load(q0);
+    if (!kAhead && (!kFirst || q0 > qb)) load(q0);
     __syncthreads();
     rq.put(sq, q0, valid);
     rg.put(sg, q0, valid);

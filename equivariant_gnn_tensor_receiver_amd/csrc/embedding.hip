@@ -6,16 +6,20 @@
 // shares, and lets one wave add the rows of a chunk, 64 lanes side by side over
 // the columns.  A run of equal types inside a chunk is written at once; the
 // parts of a run that crosses chunks go to the workspace and are added in order
-// by a second kernel.  Rows of types without nodes are zero: the whole table is
-// cleared beside the sort, by the blocks that do not sort.
+// by a second kernel.  Rows of types without nodes are cleared by blocks of their own
+// beside the sums (16383 nodes over 32000 x 1024: clearing the whole table beside the
+// sort wrote the rows of present types twice, 93 us for both directions where this takes 79).
 //
-// Up to kOneBlock nodes are sorted by one block in LDS, more of them by 8-bit
-// radix passes over blocks of kSortItems (count, scan, scatter).
+// Up to kOneBlock nodes are sorted by one block in LDS (4096 nodes 9 us), more of
+// them by 8-bit radix passes over many blocks: a count and a scatter per pass while a
+// block can add up the counts before its own (32768 nodes of 89 types: 4 and 6 us),
+// with a scan of the counts between them for longer lists.
 #include "attention.h"
 #include "device_common.h"
 #include "timing.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace tpconv {
 namespace {
@@ -25,11 +29,11 @@ typedef float floatx4_any __attribute__((ext_vector_type(4), aligned(4)));
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned int u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
 
-constexpr int kOneBlock = 16384;  // nodes that one block sorts
+constexpr int kOneBlock = 4096;  // nodes that one block sorts
 constexpr int kSortThreads = 1024, kWaves = kSortThreads / 64;
-constexpr int kSortItems = 4096;  // nodes per block of a radix pass
+// nodes per thread of a block of a radix pass: one while there are few blocks, else four
+constexpr int kFewBlocks = 64, kManyK = 4;
 constexpr int kFew = 128;         // nodes that every block of a single launch sorts for itself
-constexpr int kFillBlocks = 2048;
 
 // ---- forward --------------------------------------------------------------------
 
@@ -57,7 +61,9 @@ __device__ __forceinline__ void store4(uint16_t* p, const float (&v)[4]) {
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store1(uint16_t* p, float v) { *p = (uint16_t)bf16_bits(v); }
 
-// `nodes` nodes per block and step, four columns per thread.
+// `nodes` nodes per block and step; a thread takes four columns of kInFlight nodes'
+// quads at a time, so that the index and the row of several are on their way together.
+constexpr int kInFlight = 4;
 template <typename TW, typename TY>
 __global__ __launch_bounds__(256) void embed_forward_kernel(const EmbedArgs a, int nodes) {
   const int F = a.features, quads = (F + 3) / 4;
@@ -65,20 +71,46 @@ __global__ __launch_bounds__(256) void embed_forward_kernel(const EmbedArgs a, i
   TY* y = static_cast<TY*>(a.y);
   for (int64_t base = (int64_t)blockIdx.x * nodes; base < a.N; base += (int64_t)gridDim.x * nodes) {
     const int here = (int)(a.N - base < nodes ? a.N - base : nodes), items = here * quads;
-    for (int idx = threadIdx.x; idx < items; idx += 256) {
-      const int nd = idx / quads, c = (idx - nd * quads) * 4;
-      const int32_t t = a.index[base + nd];
-      const bool there = t >= 0 && t < a.rows;
-      const TW* w = W + (int64_t)(there ? t : 0) * F + c;
-      TY* o = y + (base + nd) * F + c;
-      if (c + 4 <= F) {
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
-        if (there) load4(w, v);
+    for (int idx0 = threadIdx.x; idx0 < items; idx0 += 256 * kInFlight) {
+      int nd[kInFlight], c[kInFlight];
+      int32_t t[kInFlight];
+      float v[kInFlight][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] *= a.scale;
-        store4(o, v);
-      } else {
-        for (int e = 0; c + e < F; ++e) store1(o + e, there ? load_feat(w, e) * a.scale : 0.f);
+      for (int k = 0; k < kInFlight; ++k) {
+        const int idx = min(idx0 + 256 * k, items - 1);
+        nd[k] = idx / quads;
+        c[k] = (idx - nd[k] * quads) * 4;
+        t[k] = a.index[base + nd[k]];
+      }
+#pragma unroll
+      for (int k = 0; k < kInFlight; ++k) {
+        const bool there = t[k] >= 0 && t[k] < a.rows;
+        const TW* w = W + (int64_t)(there ? t[k] : 0) * F + c[k];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[k][e] = 0.f;
+        if (there) {
+          if (c[k] + 4 <= F) {
+            load4(w, v[k]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+              if (c[k] + e < F) v[k][e] = load_feat(w, e);
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kInFlight; ++k) {
+        if (idx0 + 256 * k >= items) continue;
+        TY* o = y + (base + nd[k]) * F + c[k];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[k][e] *= a.scale;
+        if (c[k] + 4 <= F) {
+          store4(o, v[k]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 3; ++e)
+            if (c[k] + e < F) store1(o + e, v[k][e]);
+        }
       }
     }
   }
@@ -108,12 +140,17 @@ __device__ __forceinline__ void block_ranks(const uint32_t (&key)[K], const bool
     pre[k] = 0;
     if (k >= used) continue;
     const uint32_t d = (key[k] >> shift) & 255u;
-    uint64_t peers = __ballot(there[k]);
+    // the lanes whose digits agree in every bit
+    const uint64_t all = __ballot(there[k]);
+    uint32_t lo = (uint32_t)all, hi = (uint32_t)(all >> 32);
 #pragma unroll
     for (int b = 0; b < 8; ++b) {
+      const uint32_t own = (uint32_t)((int32_t)(d << (31 - b)) >> 31);  // the bit in all places
       const uint64_t m = __ballot((d >> b) & 1u);
-      peers &= (d >> b) & 1u ? m : ~m;
+      lo &= ~((uint32_t)m ^ own);
+      hi &= ~((uint32_t)(m >> 32) ^ own);
     }
+    const uint64_t peers = lo | ((uint64_t)hi << 32);
     const int below = __popcll(peers & ((uint64_t(1) << lane) - 1));
     const int32_t old = mine[d];
     __builtin_amdgcn_wave_barrier();  // every lane of the wave has read before the first writes
@@ -150,24 +187,12 @@ __device__ __forceinline__ void scan256(int32_t* v) {
   __syncthreads();
 }
 
-// Clears n floats with the blocks b = 0 .. blocks - 1.
-__device__ __forceinline__ void clear(float* p, int64_t n, int64_t b, int64_t blocks) {
-  const int64_t quads = n / 4;
-  for (int64_t i = b * blockDim.x + threadIdx.x; i < quads; i += blocks * blockDim.x)
-    *reinterpret_cast<floatx4_any*>(p + 4 * i) = (floatx4){0.f, 0.f, 0.f, 0.f};
-  if (b == 0 && threadIdx.x < n - 4 * quads) p[4 * quads + threadIdx.x] = 0.f;
-}
-
-// Block 0 sorts all nodes (at most kOneBlock) in LDS; the others clear the table.
+// One block sorts all nodes (at most kOneBlock) in LDS.
 __global__ __launch_bounds__(kSortThreads) void sort_one_kernel(const EmbedArgs a, int bits, int32_t* skey,
                                                                  int32_t* order) {
   __shared__ uint32_t s_key[kOneBlock];
   __shared__ uint16_t s_idx[kOneBlock];
   __shared__ int32_t cnt[kWaves * 256], total[256];
-  if (blockIdx.x > 0) {
-    clear(a.gW, (int64_t)a.rows * a.features, blockIdx.x - 1, gridDim.x - 1);
-    return;
-  }
   constexpr int K = kOneBlock / kSortThreads;
   const int n = (int)a.N, used = (n + kSortThreads - 1) / kSortThreads;
   const int first = (threadIdx.x >> 6) * used * 64 + (threadIdx.x & 63);
@@ -210,33 +235,32 @@ __global__ __launch_bounds__(kSortThreads) void sort_one_kernel(const EmbedArgs 
     }
 }
 
-constexpr int kPassK = kSortItems / kSortThreads;
-
-__device__ __forceinline__ void load_items(const EmbedArgs& a, const int32_t* in_key, int64_t base, uint32_t (&key)[kPassK],
-                                           bool (&there)[kPassK]) {
-  const int first = (threadIdx.x >> 6) * kPassK * 64 + (threadIdx.x & 63);
+template <int K>
+__device__ __forceinline__ void load_items(const EmbedArgs& a, const int32_t* in_key, int64_t base, uint32_t (&key)[K],
+                                           bool (&there)[K]) {
+  const int first = (threadIdx.x >> 6) * K * 64 + (threadIdx.x & 63);
 #pragma unroll
-  for (int k = 0; k < kPassK; ++k) {
+  for (int k = 0; k < K; ++k) {
     const int64_t i = base + first + 64 * k;
     there[k] = i < a.N;
     key[k] = !there[k] ? 0 : in_key ? (uint32_t)in_key[i] : sort_key(a.index[i], a.rows);
   }
 }
 
-// Digit counts of every block, [digit][block]; in the first pass the blocks from nblocks on clear the table.
+// Digit counts of every block: few blocks [block][digit], many [digit][block] (for the
+// scan).
+template <int K>
 __global__ __launch_bounds__(kSortThreads) void count_kernel(const EmbedArgs a, const int32_t* in_key, int shift,
                                                               int nblocks, int32_t* counts) {
   __shared__ int32_t cnt[kWaves * 256], total[256];
-  if ((int)blockIdx.x >= nblocks) {
-    clear(a.gW, (int64_t)a.rows * a.features, blockIdx.x - nblocks, gridDim.x - nblocks);
-    return;
-  }
-  uint32_t key[kPassK];
-  int32_t pre[kPassK];
-  bool there[kPassK];
-  load_items(a, in_key, (int64_t)blockIdx.x * kSortItems, key, there);
-  block_ranks<kPassK>(key, there, kPassK, shift, pre, cnt, total);
-  if (threadIdx.x < 256) counts[(int64_t)threadIdx.x * nblocks + blockIdx.x] = total[threadIdx.x];
+  uint32_t key[K];
+  int32_t pre[K];
+  bool there[K];
+  load_items<K>(a, in_key, (int64_t)blockIdx.x * kSortThreads * K, key, there);
+  block_ranks<K>(key, there, K, shift, pre, cnt, total);
+  if (threadIdx.x < 256)
+    counts[K == 1 ? (int64_t)blockIdx.x * 256 + threadIdx.x : (int64_t)threadIdx.x * nblocks + blockIdx.x] =
+        total[threadIdx.x];
 }
 
 // Exclusive scan of n counts in place, one block.
@@ -272,23 +296,46 @@ __global__ __launch_bounds__(1024) void scan_counts_kernel(int32_t* v, int64_t n
   }
 }
 
+// K = 1: `counts` are the blocks' counts, and every block adds up what lies before its
+// own items; else they are scanned.
+template <int K>
 __global__ __launch_bounds__(kSortThreads) void scatter_kernel(const EmbedArgs a, const int32_t* in_key,
                                                                 const int32_t* in_idx, int shift, int nblocks,
-                                                                const int32_t* base, int32_t* out_key, int32_t* out_idx) {
-  __shared__ int32_t cnt[kWaves * 256], total[256];
-  uint32_t key[kPassK];
-  int32_t pre[kPassK];
-  bool there[kPassK];
-  const int64_t b0 = (int64_t)blockIdx.x * kSortItems;
-  load_items(a, in_key, b0, key, there);
-  block_ranks<kPassK>(key, there, kPassK, shift, pre, cnt, total);
-  const int first = (threadIdx.x >> 6) * kPassK * 64 + (threadIdx.x & 63);
+                                                                const int32_t* counts, int32_t* out_key,
+                                                                int32_t* out_idx) {
+  __shared__ int32_t cnt[kWaves * 256], total[256], base[256];
+  uint32_t key[K];
+  int32_t pre[K];
+  bool there[K];
+  const int64_t b0 = (int64_t)blockIdx.x * kSortThreads * K;
+  load_items<K>(a, in_key, b0, key, there);
+  int32_t before = 0, all = 0;
+  if (threadIdx.x < 256) {
+    if constexpr (K == 1) {
+#pragma unroll 8
+      for (int b = 0; b < nblocks; ++b) {
+        const int32_t c = counts[(int64_t)b * 256 + threadIdx.x];
+        all += c;
+        before += b < (int)blockIdx.x ? c : 0;
+      }
+    } else {
+      before = counts[(int64_t)threadIdx.x * nblocks + blockIdx.x];
+    }
+    base[threadIdx.x] = all;
+  }
+  if constexpr (K == 1) {
+    __syncthreads();
+    scan256(base);
+  }
+  if (threadIdx.x < 256) base[threadIdx.x] = (K == 1 ? base[threadIdx.x] : 0) + before;
+  block_ranks<K>(key, there, K, shift, pre, cnt, total);
+  const int first = (threadIdx.x >> 6) * K * 64 + (threadIdx.x & 63);
 #pragma unroll
-  for (int k = 0; k < kPassK; ++k)
+  for (int k = 0; k < K; ++k)
     if (there[k]) {
       const uint32_t d = (key[k] >> shift) & 255u;
       const int64_t i = b0 + first + 64 * k;
-      const int32_t at = base[(int64_t)d * nblocks + blockIdx.x] + cnt[(threadIdx.x >> 6) * 256 + d] + pre[k];
+      const int32_t at = base[d] + cnt[(threadIdx.x >> 6) * 256 + d] + pre[k];
       out_key[at] = (int32_t)key[k];
       out_idx[at] = in_idx ? in_idx[i] : (int32_t)i;
     }
@@ -336,6 +383,8 @@ struct SumArgs {
   int32_t rows, F, slices;  // slices of 64 C columns
   int32_t chunk;            // sorted nodes per wave
   int64_t N, chunks;
+  int64_t sum_blocks;       // the blocks behind them clear `clear_rows` rows per wave
+  int32_t clear_rows;
   float scale;
   const int32_t *skey, *order;
   const float* gy;
@@ -343,10 +392,37 @@ struct SumArgs {
   float* part;  // [chunks][2][F]: the run that began before the chunk, the run that goes on behind it
 };
 
+// Clears the rows of types without nodes among the `unit`-th clear_rows rows: a lane
+// looks for each, and the wave writes those that are not there.
+__device__ __forceinline__ void clear_absent(const SumArgs& a, int64_t unit) {
+  const int lane = threadIdx.x & 63;
+  const int64_t row0 = unit * a.clear_rows;
+  const int64_t row = row0 + lane;
+  bool absent = false;
+  if (lane < a.clear_rows && row < a.rows) {
+    int64_t lo = 0, hi = a.N;  // the first position whose type is not below the row
+    while (lo < hi) {
+      const int64_t mid = (lo + hi) >> 1;
+      if (a.skey[mid] < row) lo = mid + 1; else hi = mid;
+    }
+    absent = lo == a.N || a.skey[lo] != row;
+  }
+  for (uint64_t m = __ballot(absent); m; m &= m - 1) {
+    float* p = a.gW + (row0 + __ffsll((unsigned long long)m) - 1) * a.F;
+    int c = lane * 4;
+    for (; c + 4 <= a.F; c += 256) *reinterpret_cast<floatx4_any*>(p + c) = (floatx4){0.f, 0.f, 0.f, 0.f};
+    for (; c < a.F; ++c) p[c] = 0.f;
+  }
+}
+
 // One wave per (chunk, slice): its sorted nodes, added run by run.
 template <int C>
 __global__ __launch_bounds__(256) void sum_kernel(const SumArgs a) {
   const int lane = threadIdx.x & 63;
+  if (blockIdx.x >= a.sum_blocks) {
+    clear_absent(a, ((int64_t)blockIdx.x - a.sum_blocks) * 4 + (threadIdx.x >> 6));
+    return;
+  }
   const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   const int64_t c = unit / a.slices;
   if (c >= a.chunks) return;
@@ -398,32 +474,48 @@ __global__ __launch_bounds__(256) void sum_kernel(const SumArgs a) {
   finish(run == behind);
 }
 
-// Runs that cross chunks.  One block per (chunk in which such a run begins, slice):
-// its waves add equal parts of the list of partial sums, then the waves' sums in order.
-template <int C>
-__global__ __launch_bounds__(512) void join_kernel(const SumArgs a) {
-  __shared__ float red[8][64 * C];
+// Runs that cross chunks: a block's waves add equal parts of the list of partial sums,
+// then the waves' sums in order.  One block per (type, slice), or where there are more
+// types than chunks per (chunk in which such a run begins, slice).
+template <int C, int WAVES, bool BY_TYPE>
+__global__ __launch_bounds__(64 * WAVES) void join_kernel(const SumArgs a) {
+  __shared__ float red[WAVES][64 * C];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t c = blockIdx.x / a.slices;
-  const int slice = (int)(blockIdx.x - c * a.slices);
-  const int64_t next = (c + 1) * a.chunk;
-  if (next >= a.N) return;
-  const int32_t run = a.skey[next - 1];
-  if (run >= a.rows || a.skey[next] != run) return;
-  if (c > 0 && a.skey[c * a.chunk - 1] == run) return;  // began earlier
-  // the last position of the run: a search with 64 probes per step
-  int64_t lo = next, n = a.N - next;  // skey[lo] == run
-  while (n > 1) {
-    const int64_t step = (n + 63) / 64, i = lane * step;
-    const int count = __popcll(__ballot(i < n && a.skey[lo + (i < n ? i : 0)] == run));
-    lo += (count - 1) * step;
-    n = step == 1 ? 1 : min(step, n - (count - 1) * step);
+  const int64_t item = blockIdx.x / a.slices;
+  const int slice = (int)(blockIdx.x - item * a.slices);
+  // searches with 64 probes per step: the first position whose type is not below `t`
+  auto first_of = [&](int64_t from, int32_t t) {
+    int64_t lo = from, n = a.N - from;  // in [lo, lo + n]
+    while (n > 0) {
+      const int64_t step = (n + 63) / 64, i = lane * step;
+      const int count = __popcll(__ballot(i < n && a.skey[lo + (i < n ? i : 0)] < t));
+      if (count == 0) break;
+      lo += (count - 1) * step + 1;
+      n = min(step - 1, n - (count - 1) * step - 1);
+    }
+    return lo;
+  };
+  int32_t run;
+  int64_t begin, end;
+  if (BY_TYPE) {
+    run = (int32_t)item;
+    begin = first_of(0, run);
+    if (begin >= a.N || a.skey[begin] != run) return;
+  } else {
+    const int64_t next = (item + 1) * a.chunk;
+    if (next >= a.N) return;
+    run = a.skey[next - 1];
+    if (run >= a.rows || a.skey[next] != run) return;
+    if (item > 0 && a.skey[item * a.chunk - 1] == run) return;  // began earlier
+    begin = next - 1;  // (any place of the run in its first chunk)
   }
-  const int64_t last = lo / a.chunk;  // chunks c .. last
+  end = first_of(begin, run + 1);
+  const int64_t c = begin / a.chunk, last = (end - 1) / a.chunk;  // chunks c .. last
+  if (last == c) return;
   const int c0 = slice * 64 * C + lane * C, left = a.F - c0;
   Cols<C> acc;
   acc.clear();
-  const int64_t total = last - c + 1, per = (total + 7) / 8;
+  const int64_t total = last - c + 1, per = (total + WAVES - 1) / WAVES;
   const int64_t b = c + wave * per, e = b + per < c + total ? b + per : c + total;
   if (left > 0) {
     constexpr int U = 8;
@@ -442,7 +534,7 @@ __global__ __launch_bounds__(512) void join_kernel(const SumArgs a) {
   for (int k = 0; k < C; ++k) red[wave][lane * C + k] = acc.v[k];
   __syncthreads();
   if (wave > 0 || left <= 0) return;
-  for (int w = 1; w < 8; ++w)
+  for (int w = 1; w < WAVES; ++w)
 #pragma unroll
     for (int k = 0; k < C; ++k) acc.v[k] += red[w][lane * C + k];
   acc.store(a.gW + (int64_t)run * a.F + c0, left, a.scale);
@@ -483,7 +575,7 @@ struct EmbedPlan {
   int slices, cols;  // column slices of 64 * cols
   int chunk;
   int64_t chunks;
-  int nblocks;       // of a radix pass
+  int k, nblocks;    // nodes per thread and blocks of a radix pass
   size_t key, order, key2, order2, counts, part, bytes;
 };
 
@@ -495,7 +587,8 @@ EmbedPlan make_plan(int32_t features, int64_t N) {
   p.chunk = 8;
   while ((p.chunk < 256 && N / (2 * p.chunk) * p.slices >= 2048) || N / p.chunk * p.slices >= 1 << 20) p.chunk *= 2;
   p.chunks = (N + p.chunk - 1) / p.chunk;
-  p.nblocks = (int)((N + kSortItems - 1) / kSortItems);
+  p.k = N <= (int64_t)kFewBlocks * kSortThreads ? 1 : kManyK;
+  p.nblocks = (int)((N + (int64_t)kSortThreads * p.k - 1) / ((int64_t)kSortThreads * p.k));
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t o = at;
@@ -521,7 +614,7 @@ size_t embed_workspace(int32_t rows, int32_t features, int64_t N) { return make_
 
 hipError_t launch_embed_forward(const EmbedArgs& a, hipStream_t s) {
   TimingScope ts(kcEmbed, s);
-  const int quads = (a.features + 3) / 4, nodes = std::max(1, 512 / quads);
+  const int quads = (a.features + 3) / 4, nodes = std::max(1, 256 * kInFlight / quads);
   const dim3 grid((unsigned)std::min<int64_t>((a.N + nodes - 1) / nodes, 1 << 20)), block(256);
   if (a.w_bf16 && a.y_bf16)
     hipLaunchKernelGGL((embed_forward_kernel<uint16_t, uint16_t>), grid, block, 0, s, a, nodes);
@@ -548,9 +641,8 @@ hipError_t launch_embed_backward(const EmbedArgs& a, void* ws, hipStream_t s) {
   int32_t *key = ints(p.key), *order = ints(p.order);
   int bits = 1;
   while ((int64_t(1) << bits) <= a.rows) ++bits;  // keys 0 .. rows
-  const int fill = (int)std::min<int64_t>(kFillBlocks, (table + 4 * kSortThreads - 1) / (4 * kSortThreads));
   if (a.N <= kOneBlock) {
-    hipLaunchKernelGGL(sort_one_kernel, dim3(1 + fill), dim3(kSortThreads), 0, s, a, bits, key, order);
+    hipLaunchKernelGGL(sort_one_kernel, dim3(1), dim3(kSortThreads), 0, s, a, bits, key, order);
   } else {
     const int passes = (bits + 7) / 8;
     int32_t *k2 = ints(p.key2), *o2 = ints(p.order2), *counts = ints(p.counts);
@@ -558,11 +650,16 @@ hipError_t launch_embed_backward(const EmbedArgs& a, void* ws, hipStream_t s) {
     const int32_t *in_k = nullptr, *in_o = nullptr;
     for (int i = 0; i < passes; ++i) {
       int32_t *out_k = (passes - 1 - i) % 2 == 0 ? key : k2, *out_o = (passes - 1 - i) % 2 == 0 ? order : o2;
-      hipLaunchKernelGGL(count_kernel, dim3(p.nblocks + (i == 0 ? fill : 0)), dim3(kSortThreads), 0, s, a, in_k, 8 * i,
-                         p.nblocks, counts);
-      hipLaunchKernelGGL(scan_counts_kernel, dim3(1), dim3(1024), 0, s, counts, (int64_t)p.nblocks * 256);
-      hipLaunchKernelGGL(scatter_kernel, dim3(p.nblocks), dim3(kSortThreads), 0, s, a, in_k, in_o, 8 * i, p.nblocks,
-                         counts, out_k, out_o);
+      const dim3 grid(p.nblocks), threads(kSortThreads);
+      if (p.k == 1) {
+        hipLaunchKernelGGL(count_kernel<1>, grid, threads, 0, s, a, in_k, 8 * i, p.nblocks, counts);
+        hipLaunchKernelGGL(scatter_kernel<1>, grid, threads, 0, s, a, in_k, in_o, 8 * i, p.nblocks, counts, out_k, out_o);
+      } else {
+        hipLaunchKernelGGL(count_kernel<kManyK>, grid, threads, 0, s, a, in_k, 8 * i, p.nblocks, counts);
+        hipLaunchKernelGGL(scan_counts_kernel, dim3(1), dim3(1024), 0, s, counts, (int64_t)p.nblocks * 256);
+        hipLaunchKernelGGL(scatter_kernel<kManyK>, grid, threads, 0, s, a, in_k, in_o, 8 * i, p.nblocks, counts, out_k,
+                           out_o);
+      }
       in_k = out_k;
       in_o = out_o;
     }
@@ -580,17 +677,25 @@ hipError_t launch_embed_backward(const EmbedArgs& a, void* ws, hipStream_t s) {
   m.gy = a.gy;
   m.gW = a.gW;
   m.part = reinterpret_cast<float*>(w + p.part);
-  const dim3 sum_grid((unsigned)((p.chunks * p.slices + 3) / 4)), join_grid((unsigned)(p.chunks * p.slices));
-  if (p.cols == 1) {
-    hipLaunchKernelGGL(sum_kernel<1>, sum_grid, dim3(256), 0, s, m);
-    hipLaunchKernelGGL(join_kernel<1>, join_grid, dim3(512), 0, s, m);
-  } else if (p.cols == 2) {
-    hipLaunchKernelGGL(sum_kernel<2>, sum_grid, dim3(256), 0, s, m);
-    hipLaunchKernelGGL(join_kernel<2>, join_grid, dim3(512), 0, s, m);
-  } else {
-    hipLaunchKernelGGL(sum_kernel<4>, sum_grid, dim3(256), 0, s, m);
-    hipLaunchKernelGGL(join_kernel<4>, join_grid, dim3(512), 0, s, m);
-  }
+  m.sum_blocks = (p.chunks * p.slices + 3) / 4;
+  m.clear_rows = a.features >= 256 ? 16 : 64;  // rows that a wave clears: about as long as its search
+  const dim3 sum_grid((unsigned)(m.sum_blocks + (a.rows + 4 * m.clear_rows - 1) / (4 * m.clear_rows)));
+  const bool by_type = a.rows <= p.chunks;
+  auto sums = [&](auto c) {
+    constexpr int C = decltype(c)::value;
+    hipLaunchKernelGGL(sum_kernel<C>, sum_grid, dim3(256), 0, s, m);
+    if (p.chunks == 1) return;  // no run crosses chunks
+    if (by_type)
+      hipLaunchKernelGGL((join_kernel<C, 8, true>), dim3((unsigned)((int64_t)a.rows * p.slices)), dim3(512), 0, s, m);
+    else
+      hipLaunchKernelGGL((join_kernel<C, 4, false>), dim3((unsigned)(p.chunks * p.slices)), dim3(256), 0, s, m);
+  };
+  if (p.cols == 1)
+    sums(std::integral_constant<int, 1>{});
+  else if (p.cols == 2)
+    sums(std::integral_constant<int, 2>{});
+  else
+    sums(std::integral_constant<int, 4>{});
   return hipGetLastError();
 }
 
