@@ -272,7 +272,7 @@ struct Stage {
   static constexpr int P = pieces<T>(), LD = row_len(DC), plane = R * LD, per = DC / 8, total = R * per;
   static constexpr int passes = (total + THREADS - 1) / THREADS;
   // Without whole quads the loads are many: each is stored before the next, to keep the code short.
-  static constexpr bool held = VEC;
+  static constexpr bool held = VEC || passes == 1;
   Octet<T> o[held ? passes : 1];
   const T* base;
   const float* factor;
@@ -729,6 +729,10 @@ struct Block {
   static constexpr int CT = col_tile<T, DC>(), kWaves = COLS / CT, kThreads = 64 * kWaves;
   static constexpr int kShift = COLS == 128 ? 7 : COLS == 64 ? 6 : 5;
   static_assert(COLS == 128 || COLS == attn_small_cols(DC), "rows per block");
+  // whether none of the wave's columns is there: it helps with the rows and skips the products
+  static __device__ __forceinline__ bool idle(int rows) {
+    return __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)) * CT >= rows;
+  }
   // the block's column of this lane
   static __device__ __forceinline__ int col() { return (int)(threadIdx.x >> 6) * CT + Geo<CT>::col(); }
 };
@@ -790,7 +794,7 @@ __global__ __launch_bounds__((Block<T, DC, COLS>::kThreads), (waves_for(regs_for
   fill_table<DC>(at_v, a.sv, w.h);
   __syncthreads();
   const int col = B::col();
-  const bool mine = col < t.rows;
+  const bool mine = col < t.rows, idle = B::idle(t.rows);
   const int64_t query = t.row0 + min(col, t.rows - 1);
   const int Dqk = a.sqk.D, Dv = a.sv.D;
   const bool bias = has_bias<KIND>(a);
@@ -830,7 +834,7 @@ __global__ __launch_bounds__((Block<T, DC, COLS>::kThreads), (waves_for(regs_for
       load(k0 + R);
       __builtin_amdgcn_sched_barrier(0);  // the loads stay ahead of the products
     }
-    for (int sub = 0; sub < valid; sub += 32) {
+    for (int sub = idle ? valid : 0; sub < valid; sub += 32) {
       Tile32<CT> s;
       s.clear();
 #pragma unroll
@@ -934,7 +938,7 @@ __global__ __launch_bounds__((Block<T, DC, COLS>::kThreads),
   fill_table<DC>(at_v, a.sv, w.h);
   __syncthreads();
   const int col = B::col();
-  const bool mine = col < t.rows;
+  const bool mine = col < t.rows, idle = B::idle(t.rows);
   const int64_t query = t.row0 + min(col, t.rows - 1);
   const int Dqk = a.sqk.D, Dv = a.sv.D;
   const bool bias = has_bias<KIND>(a);
@@ -985,7 +989,7 @@ __global__ __launch_bounds__((Block<T, DC, COLS>::kThreads),
       load(k0 + R);
       __builtin_amdgcn_sched_barrier(0);
     }
-    for (int sub = 0; sub < valid; sub += 32) {
+    for (int sub = idle ? valid : 0; sub < valid; sub += 32) {
       Tile32<CT> s, ds;
       s.clear();
       ds.clear();
@@ -1060,7 +1064,7 @@ __global__ __launch_bounds__((Block<T, DC, COLS>::kThreads),
   fill_table<DC>(at_v, a.sv, w.h);
   __syncthreads();
   const int col = B::col();
-  const bool mine = col < t.rows;
+  const bool mine = col < t.rows, idle = B::idle(t.rows);
   const int64_t key = t.row0 + min(col, t.rows - 1);
   const int Dqk = a.sqk.D, Dv = a.sv.D;
   const bool bias = has_bias<KIND>(a);
@@ -1113,7 +1117,7 @@ __global__ __launch_bounds__((Block<T, DC, COLS>::kThreads),
       load(q0 + R);
       __builtin_amdgcn_sched_barrier(0);
     }
-    for (int sub = 0; sub < valid; sub += 32) {
+    for (int sub = idle ? valid : 0; sub < valid; sub += 32) {
       Tile32<CT> s, ds;
       s.clear();
       ds.clear();

@@ -197,6 +197,26 @@ def test_blocks_of_four_waves(at, lens):
         Case("64x0e+32x1o", "64x0e+32x1o", heads, lens, None, xb, False, 0.0, True, 5).check(at)
 
 
+# graphs of more than 96 rows: blocks of 128 columns, in every width class
+WIDTHS = [("32x0e", "32x0e", 1), ("64x0e", "60x0e", 1), ("96x0e", "12x0e+20x1o", 1), ("100x0e", "128x0e", 1),
+          ("160x0e", "16x0e+16x1o+16x2e", 1), ("200x0e", "256x0e", 1), ("37x0e", "101x0e", 1), ("161x0e", "3x0e", 1)]
+
+
+@pytest.mark.parametrize("qk,v,heads", WIDTHS)
+@pytest.mark.parametrize("xb,yb", [(False, False), (True, True), (True, False)])
+def test_large_graphs_in_every_width_class(at, qk, v, heads, xb, yb):
+    for i in range(4):
+        say(f"[case] large graphs {qk} {v} x={'bf16' if xb else 'f32'} y={'bf16' if yb else 'f32'} kind={i}")
+        Case(qk, v, heads, (140, 99), None, xb, yb, cap=4.0 if i & 2 else 0.0, bias=bool(i & 1), seed=20 + i).check(at)
+
+
+@pytest.mark.parametrize("xb", [False, True])
+@pytest.mark.parametrize("lens,key_lens", [((2, 0), (9000, 5)), ((9000,), (3,))])
+def test_sums_over_many_rows_are_cut(at, xb, lens, key_lens):
+    say(f"[case] many rows {lens} {key_lens} x={'bf16' if xb else 'f32'}")
+    Case("16x0e", "16x0e", 2, lens, key_lens, xb, False, 0.0, True, 30).check(at)
+
+
 @pytest.mark.parametrize("spread", [1e-18, 30.0])
 def test_very_small_and_very_large_scores(at, spread):
     """Scores that vanish beside the others, and a softmax of few keys: the largest weights are near one."""
@@ -404,7 +424,8 @@ def test_embedding_matches_definition(at, n, rows, features):
 
 
 @pytest.mark.parametrize("n,rows,features,hot", [(20000, 4, 257, 0.9), (3000, 1000, 515, 0.5), (50000, 89, 32, 0.3),
-                                                 (16384, 3, 1024, 1.0), (129, 2, 70, 1.0)])
+                                                 (16384, 3, 1024, 1.0), (129, 2, 70, 1.0),
+                                                 (70001, 300, 5, 0.2), (70001, 70000, 2, 0.1), (200000, 10, 16, 0.5)])
 def test_embedding_of_uneven_types(at, n, rows, features, hot):
     say(f"[case] embed n={n} rows={rows} features={features} hot={hot}")
     embed_case(at, n, rows, features, False, False, n, hot)
