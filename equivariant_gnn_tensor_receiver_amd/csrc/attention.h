@@ -27,6 +27,7 @@ struct AttnArgs {
   int32_t H, G, self;
   int32_t x_bf16, y_bf16;
   int32_t nsplit;           // parts the long axis is cut into, joined by a second kernel
+  int32_t heads_inner;      // order of the work: the heads of a tile together, or the tiles of a head
   int64_t tiles;            // row tiles of the launch
   float scale, cap;
   int64_t Nq, Nk;

@@ -161,6 +161,9 @@ hipError_t launch_class(int kind, AttnArgs& a, const AttnShape& s, hipStream_t s
   TimingScope ts(kcAttention, st);
   a.tiles = s.tiles;
   a.nsplit = s.nsplit;
+  // the other side of a graph, all heads: in an XCD's L2 (4 MiB) beside what else passes through it
+  const int64_t rows = (kind == 2 ? a.Nq : a.Nk) / std::max(1, a.G);
+  a.heads_inner = rows * (a.sqk.F + a.sv.F) * 4 <= int64_t(2) << 20;
   return kLaunch[s.cls](kind, a, s.cols, st);
 }
 
