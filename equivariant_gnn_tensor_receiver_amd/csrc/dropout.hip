@@ -87,33 +87,40 @@ __global__ __launch_bounds__(kThreads) void dropout_kernel(const DropArgs a, int
       while (i + 1 < a.nirr && g >= a.ir[i + 1].first) ++i;
       const int c = (g - a.ir[i].first) * 8, mul = a.ir[i].mul, n = a.ir[i].n;
       const uint64_t b = (uint64_t)(base + nd) * (uint64_t)a.groups + (uint64_t)g;
+      int64_t at = (base + nd) * a.F + a.ir[i].off + c;
+      const bool whole = c + 8 <= mul;
+      // the first row is on its way while the mask is drawn, the next one while a row is written
+      float v[8], q[8];
+      auto load = [&](int64_t p) {
+        load8(x + p, v);
+        if (a.has_res) load8(res + p, q);
+      };
+      if (whole) load(at);
       const u32x4 w = philox((uint32_t)b, (uint32_t)(b >> 32), (uint32_t)offset, (uint32_t)(offset >> 32),
                              (uint32_t)seed, (uint32_t)(seed >> 32));
-      float f[8];
       bool keep[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) keep[e] = ((w[e >> 1] >> (16 * (e & 1))) & 0xffffu) >= limit;
-      int64_t at = (base + nd) * a.F + a.ir[i].off + c;
-      for (int r = 0; r < n; ++r, at += mul) {
-        if (c + 8 <= mul) {
-          float v[8], q[8];
-          load8(x + at, v);
-          if (a.has_res) load8(res + at, q);
+      if (whole) {
+        for (int r = 0; r < n; ++r, at += mul) {
+          float o[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            v[e] = keep[e] ? v[e] * a.factor : 0.f;
-            if (a.has_res) v[e] += q[e];
+            o[e] = keep[e] ? v[e] * a.factor : 0.f;
+            if (a.has_res) o[e] += q[e];
           }
-          store8(y + at, v);
-        } else {
+          if (r + 1 < n) load(at + mul);
+          store8(y + at, o);
+        }
+      } else {
+        for (int r = 0; r < n; ++r, at += mul)
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             if (c + e < mul) {
-              float v = keep[e] ? load_feat(x, at + e) * a.factor : 0.f;
-              if (a.has_res) v += load_feat(res, at + e);
-              store1(y + at + e, v);
+              float o = keep[e] ? load_feat(x, at + e) * a.factor : 0.f;
+              if (a.has_res) o += load_feat(res, at + e);
+              store1(y + at + e, o);
             }
-        }
       }
     }
   }
