@@ -21,7 +21,7 @@
 // SIMD.  fp32, and bf16 heads wider than 96, take 16 columns and v_mfma_f32_16x16x32_bf16, eight waves per block:
 // its three pieces per operand would leave room for one wave of 32 columns per SIMD
 // only, whose products and vector work then follow one another (8192 nodes of
-// 128x0e+128x1o+128x2e, 8 heads: forward 369 us, gradients 725 and 1130; now 263, 463 and 710).
+// 128x0e+128x1o+128x2e, 8 heads: forward 369 us, gradients 725 and 1130; now 265, 420 and 668).
 //
 // Precision: an fp32 operand is the sum of three bf16 pieces, each the rounded
 // rest of those before (|p1| <= 2^-9 |x|, |p2| <= 2^-18 |x|, 2^-27 |x| is left out),
