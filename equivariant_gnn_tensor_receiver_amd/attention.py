@@ -169,7 +169,14 @@ class Batch:
         self.struct = AttentionBatch(self.num_graphs, num_queries, ly._ptr(offsets), ly._ptr(pos), self.num_keys,
                                      ly._ptr(key_offsets), ly._ptr(key_pos))
         self.ref = byref(self.struct)
+        self._made = tuple((t, t.data_ptr(), t.numel()) for t in (offsets, pos, key_offsets, key_pos) if t is not None)
         self.key = (self.num_graphs, num_queries, self.num_keys, self.cross, pos is not None, key_pos is not None)
+
+    def check(self):
+        """Raises if a tensor of the batch has since been given other memory (``.data``, ``set_``, ``resize_``)."""
+        for t, at, numel in self._made:
+            if t.data_ptr() != at or t.numel() != numel:
+                raise ValueError("batch: a tensor of it has other memory than when it was made")
 
 
 def _rows(t, name, dtype, n, features, device):
@@ -189,6 +196,7 @@ def _rows(t, name, dtype, n, features, device):
 def _attention_inputs(attn, batch, q, k, v, slope, dev):
     if batch.device is not None and batch.device != dev:
         raise ValueError(f"batch: on {batch.device}, expected {dev}")
+    batch.check()
     nq, nk = batch.num_queries, batch.num_keys
     s = (_rows(q, "q", attn.x_dtype, nq, attn.feat_qk, dev), _rows(k, "k", attn.x_dtype, nk, attn.feat_qk, dev),
          _rows(v, "v", attn.x_dtype, nk, attn.feat_v, dev))

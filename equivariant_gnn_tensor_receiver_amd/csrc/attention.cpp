@@ -188,8 +188,10 @@ extern "C" {
 tpconv_status tpconv_attention_create(tpconv_attention* out, const tpconv_attention_desc* desc) {
   if (!out || !desc) return TPCONV_ERROR_INVALID_VALUE;
   *out = nullptr;
-  if (desc->num_heads < 1 || desc->num_heads > 256 || !std::isfinite(desc->scale) || !(desc->score_cap >= 0.f) ||
-      std::isinf(desc->score_cap) || bad_dtype(desc->x_dtype) || bad_dtype(desc->y_dtype))
+  const float cap = desc->score_cap, most = 0x1p100f;  // with these, what the kernels make of them is in range
+  if (desc->num_heads < 1 || desc->num_heads > 256 || !(std::fabs(desc->scale) <= most) ||
+      !(cap == 0.f || (cap >= 1.f / most && cap <= most && std::isfinite(desc->scale / cap))) ||
+      bad_dtype(desc->x_dtype) || bad_dtype(desc->y_dtype))
     return TPCONV_ERROR_INVALID_VALUE;
   try {
     auto h = std::make_unique<tpconv_attention_s>();
@@ -198,7 +200,7 @@ tpconv_status tpconv_attention_create(tpconv_attention* out, const tpconv_attent
     if (st != TPCONV_SUCCESS) return st;
     h->heads = desc->num_heads;
     h->scale = desc->scale;
-    h->cap = desc->score_cap;
+    h->cap = cap;
     h->x_dtype = desc->x_dtype;
     h->y_dtype = desc->y_dtype;
     *out = h.release();

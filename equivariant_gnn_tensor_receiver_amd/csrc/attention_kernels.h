@@ -44,6 +44,7 @@
 #include "attention.h"
 #include "device_common.h"
 
+#include <cfloat>
 #include <type_traits>
 
 namespace tpconv {
@@ -550,6 +551,18 @@ struct StagePos {
   }
 };
 
+// The reference that the forward's weights are taken against moves only when a score
+// passes it by more than 2^kSlack, so that the sums are rarely scaled again; weights
+// stay below 2^kSlack, which fp32 sums and bf16 pieces hold as well as below 1.
+constexpr float kSlack = 8.f;
+
+// A weight made again from its score in the backward: the products come in another order
+// there, and scores of 1e9 and more differ by so much that the weight would be infinite
+// (one instruction, which keeps NaN).
+__device__ __forceinline__ float weight_again(float v) {
+  return exp2_fast(__builtin_elementwise_minimum(v, kSlack + 1.f));
+}
+
 // A column's (lane's) side of the distance bias.
 struct Place {
   float x, y, z, slope2;  // position, slope in units of log2
@@ -575,34 +588,33 @@ struct BiasSums {
 // the odd series of tanh does (the next term is below 2^-26 there); any.
 enum CapKind { kNoCap, kSmall, kAnyCap };
 
-// cap tanh(scale s / cap) log2(e), accurate relative to its value.
+// cap tanh(scale s / cap) log2(e), accurate relative to its value.  The series is in
+// x = scale s / cap: its coefficients times powers of scale / cap instead would save a
+// product per score, but leave fp32's range for caps below about 2e-4 scale, and their
+// products with a score of zero are NaN.
 struct Cap {
   float in, out, unout;  // scale / cap, cap log2(e), 1 / out
-  float k[6];            // of the series in s^2, times s
+  float k[6];            // of the series in x^2, times x
   __device__ __forceinline__ Cap(const AttnArgs& a) {
     in = uniform(a.cap > 0.f ? a.scale / a.cap : 0.f);
     out = uniform(a.cap * kLog2e);
     unout = uniform(a.cap > 0.f ? 1.f / out : 0.f);
-    const float i2 = in * in;
-    float f = in * out;
     const float c[6] = {1.f, -1.f / 3.f, 2.f / 15.f, -17.f / 315.f, 62.f / 2835.f, -1382.f / 155925.f};
 #pragma unroll
-    for (int i = 0; i < 6; ++i) {
-      k[i] = uniform(c[i] * f);
-      f *= i2;
-    }
+    for (int i = 0; i < 6; ++i) k[i] = uniform(c[i] * out);
   }
-  __device__ __forceinline__ float series(float s) const {
-    const float t = s * s;
+  __device__ __forceinline__ float series(float x) const {
+    const float t = x * x;
     float v = k[5];
 #pragma unroll
     for (int i = 4; i >= 0; --i) v = fmaf(v, t, k[i]);
-    return v * s;
+    return v * x;
   }
+  __device__ __forceinline__ float small(float s) const { return series(s * in); }
   __device__ __forceinline__ float any(float s) const {
     const float x = s * in, e = exp2_fast(-2.f * kLog2e * fabsf(x));
     const float big = copysignf((1.f - e) * __builtin_amdgcn_rcpf(1.f + e) * out, x);
-    return fabsf(x) < 0.25f ? series(s) : big;
+    return fabsf(x) < 0.25f ? series(x) : big;
   }
 };
 
@@ -659,7 +671,7 @@ __device__ __forceinline__ void score_tile(const Cap& cap, float c, Tile32<CT>& 
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       float v = s.get(4 * q + e);
-      if constexpr (CAP == kSmall) v = cap.series(v);
+      if constexpr (CAP == kSmall) v = cap.small(v);
       if constexpr (CAP == kAnyCap) v = cap.any(v);
       if constexpr (BIAS) {
         const float dx = p.x - x[e], dy = p.y - y[e], dz = p.z - z[e];
@@ -692,16 +704,16 @@ __device__ __forceinline__ void grad_tile(const Cap& cap, float c, Tile32<CT>& s
     for (int e = 0; e < 4; ++e) {
       const int r = 4 * q + e;
       float u = s.get(r);
-      if constexpr (CAP == kSmall) u = cap.series(u);
+      if constexpr (CAP == kSmall) u = cap.small(u);
       if constexpr (CAP == kAnyCap) u = cap.any(u);
       float v = CAP != kNoCap ? u - m4[e] : fmaf(u, c, -m4[e]);
       float g;
       if constexpr (BIAS) {
         const float dx = p.x - x[e], dy = p.y - y[e], dz = p.z - z[e];
         const float d2 = fmaf(dx, dx, fmaf(dy, dy, dz * dz));
-        const float over = d2 > 0.f ? __builtin_amdgcn_rsqf(d2) : 0.f;
+        const float over = d2 >= FLT_MIN ? __builtin_amdgcn_rsqf(d2) : 0.f;  // (of a subnormal: infinity)
         const float dist = d2 * over;
-        v = exp2_fast(fmaf(-p.slope2, dist, v));
+        v = weight_again(fmaf(-p.slope2, dist, v));
         g = v * (ds.get(r) - d4[e]);
         b.sd = fmaf(g, dist, b.sd);
         b.s += g;
@@ -711,7 +723,7 @@ __device__ __forceinline__ void grad_tile(const Cap& cap, float c, Tile32<CT>& s
         b.y = fmaf(w, dy, b.y);
         b.z = fmaf(w, dz, b.z);
       } else {
-        v = exp2_fast(v);
+        v = weight_again(v);
         g = v * (ds.get(r) - d4[e]);
       }
       if constexpr (CAP != kNoCap) {
@@ -783,11 +795,6 @@ constexpr bool rows_ahead(bool forward) {
 }
 
 // ---- forward ----------------------------------------------------------------------
-
-// The reference that the weights are taken against moves only when a score passes
-// it by more than 2^kSlack, so that the sums are rarely scaled again; weights
-// stay below 2^kSlack, which fp32 sums and bf16 pieces hold as well as below 1.
-constexpr float kSlack = 8.f;
 
 template <typename T, int DC, int COLS, int PP, bool VEC, int KIND>
 __global__ __launch_bounds__((Block<T, DC, COLS>::kThreads), (waves_for(regs_for<T, DC>(pieces<T>(), 1, (KIND & kCapped) != 0 ? 80 : 60)))) void forward_kernel(
@@ -1146,7 +1153,7 @@ __global__ __launch_bounds__((Block<T, DC, COLS>::kThreads),
           for (int q4 = 0; q4 < G::kQuads; ++q4) {
             const floatx4 m4 = *reinterpret_cast<const floatx4*>(sl + sub + G::first_row(q4));
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s.set(4 * q4 + e, exp2_fast(fmaf(s.get(4 * q4 + e), unit, -m4[e])));
+            for (int e = 0; e < 4; ++e) s.set(4 * q4 + e, weight_again(fmaf(s.get(4 * q4 + e), unit, -m4[e])));
           }
           return;
         }

@@ -41,7 +41,8 @@ extern "C" {
  * The inner product runs over all rows of the irreps, so that scores do not
  * change under rotations and outputs rotate as the values do.  A query whose
  * graph has no keys gets zeros.  Products of fp32 operands are within 2^-25 of
- * their values; inputs must stay below 3.38e38 and scores within fp32 range.  A
+ * their values; inputs must stay below 3.38e38, scores within fp32 range and distances below
+ * 1.8e19.  A
  * value that is not finite shows in results of its own graph and head alone.
  * For bf16 inputs with a bf16 output and without `saved` the
  * weights exp(s_ij) enter the sum over j with 17 bits. */
@@ -51,8 +52,8 @@ typedef struct {
   const char* irreps_qk; /* l <= 3, at most 16 blocks, all multiplicities divisible by num_heads */
   const char* irreps_v;  /* the same rules */
   int32_t num_heads;     /* 1..256; at most 256 values per head on either side (UNSUPPORTED) */
-  float scale;           /* finite; usually one over the square root of the values per head */
-  float score_cap;       /* >= 0; 0: scores are not capped */
+  float scale;           /* -2^100..2^100; usually one over the square root of the values per head */
+  float score_cap;       /* 0: scores are not capped; or 2^-100..2^100, and scale / score_cap finite */
   int32_t x_dtype;       /* tpconv_dtype of q, k and v */
   int32_t y_dtype;       /* tpconv_dtype of out (bf16: rounded once, to nearest even) */
 } tpconv_attention_desc;
@@ -110,7 +111,7 @@ tpconv_status tpconv_attention_forward(tpconv_attention attention, const tpconv_
 /* Where the gradients go (each may be NULL, at least one must be given), all
  * fp32.  grad_pos: of the queries' positions, in the self form of the nodes'
  * (both ends of a pair); grad_key_pos: of the keys' positions, cross form only.
- * A pair of nodes in the same place has no direction and adds nothing. */
+ * A pair of nodes in the same place (closer than 1e-19) has no direction and adds nothing. */
 typedef struct {
   float* grad_q;
   float* grad_k;

@@ -63,6 +63,30 @@ def test_refused_descriptors():
     assert status(lambda: at.Dropout("8x0e", 0.1, 0, 5)) == 1
 
 
+def test_refused_scales_and_caps():
+    """What the kernels would make of them (scale / cap, 1 / cap, both times log2(e)) has to be in fp32's range."""
+    for scale, cap in ((2.0 ** 101, 0.0), (-2.0 ** 101, 0.0), (1.0, 2.0 ** -101), (1.0, 2.0 ** 101), (2.0 ** 100, 2.0 ** -100),
+                       (1.0, 1e-45)):
+        assert status(lambda: at.Attention("8x0e", "8x0e", 2, scale, cap)) == 1
+    for scale, cap in ((2.0 ** 100, 0.0), (-1.0, 0.0), (0.0, 1.0), (1.0, 2.0 ** -100), (1.0, 2.0 ** 100)):
+        assert at.Attention("8x0e", "8x0e", 2, scale, cap).scale == scale
+
+
+def test_a_batch_notices_replaced_memory():
+    off, pos = torch.tensor([0, 2, 5], dtype=torch.int32), torch.zeros(5, 3)
+    b = at.Batch(5, off, pos)
+    b.check()
+    pos[0] = 1.0  # new values are fine
+    b.check()
+    pos.data = torch.zeros(5, 3)
+    with pytest.raises(ValueError, match="other memory"):
+        b.check()
+    b = at.Batch(5, off)
+    off.data = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="other memory"):
+        b.check()
+
+
 def test_sizes():
     h = at.Attention("16x0e+8x1o", "32x0e+8x2e", 8)
     assert (h.feat_qk, h.feat_v, h.head_qk, h.head_v) == (irreps("16x0e+8x1o")[1], irreps("32x0e+8x2e")[1], 5, 9)

@@ -224,6 +224,45 @@ def test_very_small_and_very_large_scores(at, spread):
     Case("32x0e", "32x0e", 2, (50, 40), None, False, False, 0.0, False, 6, spread).check(at)
 
 
+@pytest.mark.parametrize("xb", [False, True])
+@pytest.mark.parametrize("cap,spread", [(2.0 ** -100, 1.0), (1e-6, 1.0), (1e-4, 1.0), (1e20, 1.0), (1e22, 1e5)])
+def test_very_small_and_very_large_caps(at, xb, cap, spread):
+    """Scores of zero under caps far below them, tiles that end early, caps far above."""
+    say(f"[case] cap {cap} spread {spread} bf16 {xb}")
+    c = Case("32x0e", "32x0e", 2, (50, 33), None, xb, False, cap, cap < 1.0, 8, spread)
+    c.q[3] = 0
+    c.k[60] = 0
+    c.check(at)
+
+
+def test_nodes_in_nearly_the_same_place(at):
+    """Squared distances below the smallest normal fp32 value: as if the places were the same."""
+    import torch
+
+    say("[case] nearly the same place")
+    c = Case("8x0e+8x1o", "8x0e+8x1o", 2, (40,), bias=True, seed=9)
+    c.pos[:2] = 0
+    out, _, _, ref = c.run(at)
+    c.pos[1, 0] = 1e-20
+    again, _, _, got = c.run(at)
+    assert torch.equal(out, again)
+    for t, r in zip(got, ref):
+        assert t is None and r is None or torch.equal(t, r) and torch.isfinite(t).all()
+
+
+def test_a_batch_whose_tensors_were_replaced_is_refused(at):
+    import torch
+
+    say("[case] batch replaced")
+    c = Case("8x0e+8x1o", "8x0e+8x1o", 2, (40,), bias=True, seed=9)
+    h, b = c.layer(at), c.batch(at)
+    at.tpconv_attention_forward(h, b, c.q, c.k, c.v, slope=c.slope)
+    c.pos.data = c.pos.clone()
+    with pytest.raises(ValueError, match="other memory"):
+        at.tpconv_attention_forward(h, b, c.q, c.k, c.v, slope=c.slope)
+    torch.cuda.synchronize()
+
+
 def test_rows_outside_of_graphs(at):
     """They are not read and stay as they were: NaN in the inputs, marks in the outputs; a first row behind row 0."""
     import torch
