@@ -24,11 +24,9 @@ hipError_t TP_CAT(launch_attn_class_, TP_DC)(int kind, const AttnArgs& a, int co
     constexpr int C = decltype(c)::value, S = decltype(score)::value;
     constexpr bool V = decltype(vec)::value;
     constexpr int f32 = Block<float, TP_DC, C>::kThreads, b16 = Block<uint16_t, TP_DC, C>::kThreads;
-    if (kind == 0) {
-      if (!a.x_bf16) return launch(forward_kernel<float, TP_DC, C, 3, V, S>, a, f32, st);
-      if (a.y_bf16 && !a.stat) return launch(forward_kernel<uint16_t, TP_DC, C, 2, V, S>, a, b16, st);
-      return launch(forward_kernel<uint16_t, TP_DC, C, 3, V, S>, a, b16, st);
-    }
+    if (kind == 0)
+      return a.x_bf16 ? launch(forward_kernel<uint16_t, TP_DC, C, V, S>, a, b16, st)
+                      : launch(forward_kernel<float, TP_DC, C, V, S>, a, f32, st);
     if (kind == 1)
       return a.x_bf16 ? launch(grad_q_kernel<uint16_t, TP_DC, C, V, S>, a, b16, st)
                       : launch(grad_q_kernel<float, TP_DC, C, V, S>, a, f32, st);

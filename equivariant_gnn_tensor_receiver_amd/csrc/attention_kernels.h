@@ -27,8 +27,7 @@
 // rest of those before (|p1| <= 2^-9 |x|, |p2| <= 2^-18 |x|, 2^-27 |x| is left out),
 // and the products of the pieces whose ranks add up to at most two are added in
 // fp32, smallest first: 2^-25 of a term is left out, of either sign.  bf16
-// operands are one piece.  P and dS are fp32 and split like inputs, except in a
-// bf16 forward that saves nothing, where P is two pieces (2^-18).
+// operands are one piece.  P and dS are fp32 and split like inputs.
 //
 // The forward saves the reference m that a row's weights were taken against and
 // 1 / l, not log(l) + m: the rounding of that sum would leave the weights of a
@@ -796,7 +795,7 @@ constexpr bool rows_ahead(bool forward) {
 
 // ---- forward ----------------------------------------------------------------------
 
-template <typename T, int DC, int COLS, int PP, bool VEC, int KIND>
+template <typename T, int DC, int COLS, bool VEC, int KIND>
 __global__ __launch_bounds__((Block<T, DC, COLS>::kThreads), (waves_for(regs_for<T, DC>(pieces<T>(), 1, (KIND & kCapped) != 0 ? 80 : 60)))) void forward_kernel(
     const AttnArgs a) {
   using B = Block<T, DC, COLS>;
@@ -893,9 +892,9 @@ __global__ __launch_bounds__((Block<T, DC, COLS>::kThreads), (waves_for(regs_for
       l += here;
 #pragma unroll
       for (int st = 0; st < kRegs / 8; ++st) {
-        bf16x8 p[PP];
-        weights_frag<PP>(s, st, p, consts);
-        acc.template add<P, PP, R>(sv, sub, st, p);
+        bf16x8 p[3];
+        weights_frag<3>(s, st, p, consts);
+        acc.template add<P, 3, R>(sv, sub, st, p);
       }
     }
   }

@@ -42,10 +42,7 @@ extern "C" {
  * change under rotations and outputs rotate as the values do.  A query whose
  * graph has no keys gets zeros.  Products of fp32 operands are within 2^-25 of
  * their values; inputs must stay below 3.38e38, scores within fp32 range and distances below
- * 1.8e19.  A
- * value that is not finite shows in results of its own graph and head alone.
- * For bf16 inputs with a bf16 output and without `saved` the
- * weights exp(s_ij) enter the sum over j with 17 bits. */
+ * 1.8e19.  A value that is not finite shows in results of its own graph and head alone. */
 typedef struct tpconv_attention_s* tpconv_attention;
 
 typedef struct {

@@ -1,0 +1,32 @@
+"""GPU tests of the attention at the edges of its arguments: forwards that save and that do not, scales of zero and below,
+values that are not finite in launches cut into parts, long graphs among many small ones, offsets that decrease.  Tolerances
+not derived here are those of test_gpu_attention."""
+import numpy as np
+import pytest
+
+from gpu_cases import say
+from test_gpu_attention import Case, U, at, cuda, f64, near, offsets  # noqa: F401  (at: a fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+# ---- forwards that save and that do not ---------------------------------------------
+
+
+@pytest.mark.parametrize("qk,v,heads", [("32x0e", "32x0e", 1), ("64x0e+32x1o", "64x0e+32x1o", 8), ("100x0e", "128x0e", 1),
+                                        ("200x0e", "256x0e", 1), ("7x0e+5x1o", "3x0e+31x1o", 1)])
+@pytest.mark.parametrize("lens,key_lens", [((5, 0, 33, 1), None), ((1200,), None), ((400, 200, 100), None),
+                                           ((1, 2), (700, 900)), ((40,), (9000,))])
+def test_a_bf16_forward_is_the_same_whether_it_saves_or_not(at, qk, v, heads, lens, key_lens):  # noqa: F811
+    """One result of one set of inputs: the weights enter the sums with the same bits either way."""
+    import torch
+
+    for cap, bias in ((0.0, True), (4.0, False), (0.0, False)):
+        say(f"[case] saving or not {qk} {v} {lens} {key_lens} cap={cap} bias={bias}")
+        c = Case(qk, v, heads, lens, key_lens, True, True, cap, bias, 31)
+        h, b = c.layer(at), c.batch(at)
+        saved = torch.empty(h.saved_size(c.nq), device="cuda")
+        out = at.tpconv_attention_forward(h, b, c.q, c.k, c.v, slope=c.slope, saved=saved)
+        assert torch.equal(out, at.tpconv_attention_forward(h, b, c.q, c.k, c.v, slope=c.slope))
+        # the saved fp32 output is the one that was rounded
+        assert torch.equal(out, saved[2 * heads * c.nq:].view(c.nq, -1).bfloat16())
