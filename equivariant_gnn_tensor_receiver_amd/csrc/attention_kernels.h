@@ -836,7 +836,9 @@ __global__ __launch_bounds__((Block<T, DC, COLS>::kThreads), (waves_for(regs_for
   // scores are multiplied by this on their way into the exponent
   const float c2 = uniform(a.scale * kLog2e);
   const bool raw = !bias && !has_cap<KIND>(a);
-  const float unit = uniform(raw ? c2 : 1.f);
+  // unless they are (next to) zero then: rows that are not there would not stay at minus infinity
+  const bool flat = raw && fabsf(c2) < FLT_MIN;
+  const float unit = uniform(raw && !flat ? c2 : 1.f);
   Result<CT, DC> acc;
   acc.clear();
   float m = -INFINITY, l = 0.f;
@@ -861,6 +863,9 @@ __global__ __launch_bounds__((Block<T, DC, COLS>::kThreads), (waves_for(regs_for
         with_kind<KIND>(a, cap, s, [&](auto kind, auto bs) {
           score_tile<decltype(kind)::value, decltype(bs)::value, R>(cap, c2, s, spos, sub, place);
         });
+      if (flat)
+#pragma unroll
+        for (int r = 0; r < kRegs; ++r) s.set(r, s.get(r) * c2);
       if (valid - sub < 32)
 #pragma unroll
         for (int r = 0; r < kRegs; ++r)

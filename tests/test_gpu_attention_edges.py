@@ -30,3 +30,40 @@ def test_a_bf16_forward_is_the_same_whether_it_saves_or_not(at, qk, v, heads, le
         assert torch.equal(out, at.tpconv_attention_forward(h, b, c.q, c.k, c.v, slope=c.slope))
         # the saved fp32 output is the one that was rounded
         assert torch.equal(out, saved[2 * heads * c.nq:].view(c.nq, -1).bfloat16())
+
+# ---- scales of zero and below ---------------------------------------------------------
+
+SCALED = [("8x0e", "8x0e", 2), ("66x0e", "62x0e", 2), ("32x0e+32x1o+32x2e", "32x0e+32x1o+32x2e", 2), ("100x0e", "128x0e", 1)]
+
+
+class Negated(Case):
+    """The scores of a case from its queries with the other sign and its scale with the other sign."""
+
+    def run(self, at, **kw):  # noqa: F811
+        self.scale, self.q = -self.scale, -self.q
+        out, plain, saved, grads = super().run(at, **kw)
+        self.scale, self.q = -self.scale, -self.q
+        return out, plain, saved, (-grads[0], *grads[1:])
+
+
+@pytest.mark.parametrize("qk,v,heads", SCALED)
+@pytest.mark.parametrize("xb", [False, True])
+@pytest.mark.parametrize("lens,key_lens", [((1,), None), ((33, 65), None), ((130, 3), None), ((1111,), None),
+                                           ((2, 1), (700, 31))])
+def test_scales_of_zero(at, qk, v, heads, xb, lens, key_lens):  # noqa: F811
+    """All keys weigh the same (or by their distance alone); rows of a tile that are not there weigh nothing."""
+    for cap, bias in ((0.0, False), (0.0, True), (4.0, False)):
+        for scale in (0.0, 1e-42):
+            say(f"[case] scale {scale} {qk} {v} {lens} {key_lens} x={'bf16' if xb else 'f32'} cap={cap} bias={bias}")
+            c = Case(qk, v, heads, lens, key_lens, xb, xb, cap, bias, 32)
+            c.scale = scale
+            c.check(at)
+
+
+@pytest.mark.parametrize("qk,v,heads", SCALED)
+@pytest.mark.parametrize("xb", [False, True])
+@pytest.mark.parametrize("lens,key_lens", [((33, 65), None), ((130, 3), None), ((1111,), None), ((2, 1), (700, 31))])
+def test_scales_below_zero(at, qk, v, heads, xb, lens, key_lens):  # noqa: F811
+    for cap, bias in ((0.0, False), (0.0, True), (4.0, False)):
+        say(f"[case] negated {qk} {v} {lens} {key_lens} x={'bf16' if xb else 'f32'} cap={cap} bias={bias}")
+        Negated(qk, v, heads, lens, key_lens, xb, xb, cap, bias, 33).check(at)
