@@ -80,7 +80,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const AttnArgs a) {
 #pragma unroll 8
         for (int p = 0; p < S; ++p) {
           const float v = a.part_o[((int64_t)p * a.Nq + query) * F + i];
-          o = w[p] != 0.f ? fmaf(w[p], v, o) : o;
+          o = fmaf(w[p], v, o);  // (also under a factor of zero: a NaN shows as in a launch without parts)
         }
         if (a.out32) a.out32[query * F + i] = o;
         if (a.y_bf16)

@@ -67,3 +67,28 @@ def test_scales_below_zero(at, qk, v, heads, xb, lens, key_lens):  # noqa: F811
     for cap, bias in ((0.0, False), (0.0, True), (4.0, False)):
         say(f"[case] negated {qk} {v} {lens} {key_lens} x={'bf16' if xb else 'f32'} cap={cap} bias={bias}")
         Negated(qk, v, heads, lens, key_lens, xb, xb, cap, bias, 33).check(at)
+
+# ---- values that are not finite -----------------------------------------------------------
+
+
+@pytest.mark.parametrize("xb", [False, True])
+def test_a_nan_under_a_weight_of_zero_shows_whether_the_launch_is_cut_into_parts_or_not(at, xb):  # noqa: F811
+    """Two keys' worth of scores, 300 apart: the low half of the keys has weights that vanish, 0 * NaN is NaN all the same."""
+    import torch
+
+    for graphs in (1, 1000):  # a few blocks, cut into parts; enough blocks without
+        say(f"[case] NaN under a weight of zero graphs={graphs} x={'bf16' if xb else 'f32'}")
+        n = 2560
+        h = at.Attention("8x0e", "8x0e", 1, 1.0, 0.0, at.TPCONV_BF16 if xb else at.TPCONV_F32)
+        off, key_off = offsets((1,) * graphs), offsets((n,) + (1,) * (graphs - 1))
+        b = at.Batch(graphs, off, None, n + graphs - 1, key_off)
+        assert (h.workspace_size(b, at.OP_FORWARD) > 0) == (graphs == 1)
+        q, k, v = (cuda(np.ones((m, 8)), xb) for m in (graphs, n + graphs - 1, n + graphs - 1))
+        k[:] = 0
+        k[n // 2:n, 0] = 300.0
+        v[7, 3] = float("nan")
+        out = at.tpconv_attention_forward(h, b, q, k, v)
+        assert out[0, 3].isnan()
+        # the others are a sum times 1 / l, which is rounded, as each of the at most 64 parts' products is: 65 U off, not 0
+        out[0, 3] = 1.0
+        assert torch.all((out - 1.0).abs() <= 65 * U)
