@@ -99,7 +99,8 @@ bool too_many(const AttnShape& s, int heads) {
          (s.tiles * heads * s.nsplit + 8) * 4 * s.cols >= (int64_t(1) << 32);
 }
 
-tpconv_status plan_of(const tpconv_attention_s& h, int op, const tpconv_attention_batch& b, AttnPlan& p) {
+// saves: a forward that leaves fp32 results (or saves them), in which the sums of a graph's runs fit
+tpconv_status plan_of(const tpconv_attention_s& h, int op, const tpconv_attention_batch& b, bool saves, AttnPlan& p) {
   std::memset(&p, 0, sizeof(p));
   const int64_t Nq = b.num_queries, Nk = keys_of(b), H = h.heads;
   const int D = std::max(h.qk.D, h.v.D);
@@ -110,6 +111,8 @@ tpconv_status plan_of(const tpconv_attention_s& h, int op, const tpconv_attentio
     if (p.fwd.nsplit > 1) {
       p.part_o = take((size_t)p.fwd.nsplit * Nq * h.v.F);
       p.part_ml = take((size_t)p.fwd.nsplit * H * Nq * 2);
+    } else if (Nk > kAttnRun && !saves) {
+      p.part_o = take((size_t)Nq * h.v.F);
     }
   } else {
     p.q = attn_shape(D, Nq, Nk, b.num_graphs, h.heads, true);
@@ -238,7 +241,7 @@ tpconv_status tpconv_attention_workspace_size(tpconv_attention attention, int32_
   if (st != TPCONV_SUCCESS) return st;
   if (!bytes || (op != TPCONV_OP_FORWARD && op != TPCONV_OP_BACKWARD)) return TPCONV_ERROR_INVALID_VALUE;
   AttnPlan p;
-  st = plan_of(*attention, op, *batch, p);
+  st = plan_of(*attention, op, *batch, attention->y_dtype == TPCONV_F32, p);
   if (st == TPCONV_SUCCESS) *bytes = p.floats * sizeof(float);
   return st;
 }
@@ -254,7 +257,7 @@ tpconv_status tpconv_attention_forward(tpconv_attention attention, const tpconv_
   if (a.Nq == 0 || a.G == 0) return TPCONV_SUCCESS;
   if (!out) return TPCONV_ERROR_INVALID_VALUE;
   AttnPlan p;
-  st = plan_of(*attention, TPCONV_OP_FORWARD, *batch, p);
+  st = plan_of(*attention, TPCONV_OP_FORWARD, *batch, saved || !a.y_bf16, p);
   if (st != TPCONV_SUCCESS) return st;
   if (bad_workspace(workspace, workspace_bytes, p.floats * sizeof(float))) return TPCONV_ERROR_WORKSPACE;
   float* ws = static_cast<float*>(workspace);
@@ -290,7 +293,7 @@ tpconv_status tpconv_attention_backward(tpconv_attention attention, const tpconv
   if (a.G == 0 || (a.Nq == 0 && a.Nk == 0)) return g.grad_slope ? dev(launch_fill(g.grad_slope, a.H, 0.f, s)) : TPCONV_SUCCESS;
   if (a.Nq > 0 && (!out || !saved || !grad_out)) return TPCONV_ERROR_INVALID_VALUE;
   AttnPlan p;
-  st = plan_of(h, TPCONV_OP_BACKWARD, *batch, p);
+  st = plan_of(h, TPCONV_OP_BACKWARD, *batch, true, p);
   if (st != TPCONV_SUCCESS) return st;
   if (bad_workspace(workspace, workspace_bytes, p.floats * sizeof(float))) return TPCONV_ERROR_WORKSPACE;
   float* ws = static_cast<float*>(workspace);

@@ -39,7 +39,7 @@ struct AttnArgs {
   void* out;
   float* stat;              // [2][H][Nq]: the references of the rows' weights and 1 / their sums; NULL: not saved
   float* out32;             // fp32 output of a bf16 forward that saves, or NULL
-  float *part_o, *part_ml;  // [nsplit][Nq][F_v], [nsplit][H][Nq][2]
+  float *part_o, *part_ml;  // [nsplit][Nq][F_v], [nsplit][H][Nq][2]; one part: sums of runs where no result is fp32
   // backward
   const float* go;
   const float* o;           // fp32 output
@@ -67,6 +67,7 @@ struct AttnJoinArgs {
 };
 
 constexpr int kAttnMaxHead = 256;
+constexpr int64_t kAttnRun = 4096;  // rows in one accumulator; a multiple of the 64 that a block takes at a time
 
 // Rows per block where the graphs are small: 32, but blocks of wide heads need LDS for
 // several waves' worth of registers (a CU's LDS holds two of 160 values, one of 256).
@@ -78,7 +79,7 @@ struct AttnShape {
   int nsplit;
   int64_t tiles;
 };
-// The shape of a launch whose rows are `rows` and whose long axis is `other`; exact: its results stay fp32.
+// The shape of a launch whose rows are `rows` and whose long axis is `other`; exact: its results are fp32.
 AttnShape attn_shape(int D, int64_t rows, int64_t other, int64_t graphs, int heads, bool exact);
 
 hipError_t launch_attn_forward(AttnArgs& a, const AttnShape& s, hipStream_t st);

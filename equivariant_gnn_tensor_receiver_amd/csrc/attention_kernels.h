@@ -35,6 +35,13 @@
 // keys with a common part) do not forgive (gradient of the slopes of 8192 nodes in
 // 16 graphs: 1.1e-5 off in place of 1e-6).
 //
+// Sums over more than kAttnRun rows of the other side are made in runs of that many: the
+// matrix instructions' roundings of one accumulator add up along a run (16384 nodes in one
+// graph, fp32, 4 heads of 64: gradients off by 4e-6 in one run, 8e-7 in four).  A run's
+// sums are added to what the block left of those before in its own rows of the result,
+// which costs a read and a write of them per run (forward of 16384 nodes in bf16, 8 heads
+// of 64, in four runs: 1654 us in one, 1749).
+//
 // The rows of the other side go through LDS as planes of pieces, [row][value],
 // padded so that 16-byte reads of rows and the transposing reads of columns
 // both touch every bank once.
@@ -392,6 +399,27 @@ struct Result {
       cols_frag<CT, PA, DC, R>(lds, row, step, G::kRows * t, f);
       mul<PA, PB>(f, b, a[t]);
     }
+  }
+  // Adds f times a lane's row of features to its column.
+  template <bool VEC>
+  __device__ __forceinline__ void fold(float f, const int* at, int D, const float* row) {
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+      for (int q = 0; q < kQuads; ++q) {
+        const int e0 = G::kRows * t + (CT == 32 ? 8 * q : 0) + 4 * G::group();
+        if constexpr (VEC) {
+          if (e0 < D) {
+            const floatx4 x = *reinterpret_cast<const floatx4_any*>(row + at[e0]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) a[t][4 * q + e] = fmaf(f, x[e], a[t][4 * q + e]);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (e0 + e < D) a[t][4 * q + e] = fmaf(f, row[at[e0 + e]], a[t][4 * q + e]);
+        }
+      }
   }
   // Writes a lane's column, times f, to its row of features.
   template <bool VEC, typename O>
@@ -758,6 +786,13 @@ struct Block {
   }
   // the block's column of this lane
   static __device__ __forceinline__ int col() { return (int)(threadIdx.x >> 6) * CT + Geo<CT>::col(); }
+  // the same where the compiler cannot tell: what a run's end needs of it is made there and takes no
+  // registers in the loop before
+  static __device__ __forceinline__ int col_again() {
+    int t = threadIdx.x;
+    asm volatile("" : "+v"(t));
+    return (t >> 6) * CT + (t & (CT - 1));
+  }
 };
 
 // A column's right operand: values of the row at p.
@@ -805,15 +840,15 @@ __global__ __launch_bounds__((Block<T, DC, COLS>::kThreads), (waves_for(regs_for
   __shared__ __align__(16) uint16_t sk[P * R * LD], sv[P * R * LD];
   __shared__ int at_qk[DC], at_v[DC];
   __shared__ __align__(16) float spos[3 * R];
+  __shared__ float runs[2][B::kThreads];  // what the sums of the runs so far are taken against, and of their weights
   Work w;
   Tile t;
   if (!find_work(a, w) || !find_tile(a.qo, a.G, a.Nq, B::kShift, w.tile, t)) return;
   fill_table<DC>(at_qk, a.sqk, w.h);
   fill_table<DC>(at_v, a.sv, w.h);
   __syncthreads();
-  const int col = B::col();
-  const bool mine = col < t.rows, idle = B::idle(t.rows);
-  const int64_t query = t.row0 + min(col, t.rows - 1);
+  const bool idle = B::idle(t.rows);
+  const int64_t query = t.row0 + min(B::col(), t.rows - 1);
   const int Dqk = a.sqk.D, Dv = a.sv.D;
   const bool bias = has_bias<KIND>(a);
   int64_t kb, ke;
@@ -842,94 +877,120 @@ __global__ __launch_bounds__((Block<T, DC, COLS>::kThreads), (waves_for(regs_for
   Result<CT, DC> acc;
   acc.clear();
   float m = -INFINITY, l = 0.f;
-  for (int64_t k0 = kb; k0 < ke; k0 += R) {
-    const int valid = (int)(ke - k0 < R ? ke - k0 : R);
-    if (!kAhead && (!kFirst || k0 > kb)) load(k0);
-    __syncthreads();
-    rk.put(sk, k0, valid);
-    rv.put(sv, k0, valid);
-    if (bias) rp.put(spos);
-    __syncthreads();
-    if (kAhead && k0 + R < ke) {
-      load(k0 + R);
-      __builtin_amdgcn_sched_barrier(0);  // the loads stay ahead of the products
+  for (int64_t k0 = kb;;) {
+    const int64_t begin = k0, stop = ke - k0 < kAttnRun ? ke : k0 + kAttnRun;
+    for (; k0 < stop; k0 += R) {
+      const int valid = (int)(ke - k0 < R ? ke - k0 : R);
+      if (!kAhead && (!kFirst || k0 > kb)) load(k0);
+      __syncthreads();
+      rk.put(sk, k0, valid);
+      rv.put(sv, k0, valid);
+      if (bias) rp.put(spos);
+      __syncthreads();
+      if (kAhead && k0 + R < ke) {
+        load(k0 + R);
+        __builtin_amdgcn_sched_barrier(0);  // the loads stay ahead of the products
+      }
+      for (int sub = idle ? valid : 0; sub < valid; sub += 32) {
+        Tile32<CT> s;
+        s.clear();
+#pragma unroll
+        for (int c = 0; c < NC; ++c) add_scores<CT, P, P, DC, R>(sk, sub, c, q[c], s);
+        if (!raw)
+          with_kind<KIND>(a, cap, s, [&](auto kind, auto bs) {
+            score_tile<decltype(kind)::value, decltype(bs)::value, R>(cap, c2, s, spos, sub, place);
+          });
+        if (flat)
+#pragma unroll
+          for (int r = 0; r < kRegs; ++r) s.set(r, s.get(r) * c2);
+        if (valid - sub < 32)
+#pragma unroll
+          for (int r = 0; r < kRegs; ++r)
+            if (sub + G::first_row(r / 4) + r % 4 >= valid) s.set(r, unit < 0.f ? INFINITY : -INFINITY);
+        float top = s.get(0);
+        if (unit < 0.f) {
+#pragma unroll
+          for (int r = 1; r < kRegs; ++r) top = fminf(top, s.get(r));
+        } else {
+#pragma unroll
+          for (int r = 1; r < kRegs; ++r) top = fmaxf(top, s.get(r));
+        }
+        top = col_max<CT>(top * unit);
+        if (__any(top > m + kSlack)) {
+          const float next = fmaxf(m, top);
+          const float f = m == -INFINITY ? 0.f : exp2_fast(m - next);
+          l *= f;
+          acc.scale(f);
+          m = next;
+        }
+        const float ref = m == -INFINITY ? 0.f : m;
+        float here = 0.f;  // (a tile's weights before the running sum: fewer roundings at its size)
+#pragma unroll
+        for (int r = 0; r < kRegs; ++r) {
+          const float p = exp2_fast(fmaf(s.get(r), unit, -ref));
+          s.set(r, p);
+          here += p;
+        }
+        l += here;
+#pragma unroll
+        for (int st = 0; st < kRegs / 8; ++st) {
+          bf16x8 p[3];
+          weights_frag<3>(s, st, p, consts);
+          acc.template add<P, 3, R>(sv, sub, st, p);
+        }
+      }
     }
-    for (int sub = idle ? valid : 0; sub < valid; sub += 32) {
-      Tile32<CT> s;
-      s.clear();
-#pragma unroll
-      for (int c = 0; c < NC; ++c) add_scores<CT, P, P, DC, R>(sk, sub, c, q[c], s);
-      if (!raw)
-        with_kind<KIND>(a, cap, s, [&](auto kind, auto bs) {
-          score_tile<decltype(kind)::value, decltype(bs)::value, R>(cap, c2, s, spos, sub, place);
-        });
-      if (flat)
-#pragma unroll
-        for (int r = 0; r < kRegs; ++r) s.set(r, s.get(r) * c2);
-      if (valid - sub < 32)
-#pragma unroll
-        for (int r = 0; r < kRegs; ++r)
-          if (sub + G::first_row(r / 4) + r % 4 >= valid) s.set(r, unit < 0.f ? INFINITY : -INFINITY);
-      float top = s.get(0);
-      if (unit < 0.f) {
-#pragma unroll
-        for (int r = 1; r < kRegs; ++r) top = fminf(top, s.get(r));
-      } else {
-#pragma unroll
-        for (int r = 1; r < kRegs; ++r) top = fmaxf(top, s.get(r));
-      }
-      top = col_max<CT>(top * unit);
-      if (__any(top > m + kSlack)) {
-        const float next = fmaxf(m, top);
-        const float f = m == -INFINITY ? 0.f : exp2_fast(m - next);
-        l *= f;
-        acc.scale(f);
-        m = next;
-      }
-      const float ref = m == -INFINITY ? 0.f : m;
-      float here = 0.f;  // (a tile's weights before the running sum: fewer roundings at its size)
-#pragma unroll
-      for (int r = 0; r < kRegs; ++r) {
-        const float p = exp2_fast(fmaf(s.get(r), unit, -ref));
-        s.set(r, p);
-        here += p;
-      }
-      l += here;
-#pragma unroll
-      for (int st = 0; st < kRegs / 8; ++st) {
-        bf16x8 p[3];
-        weights_frag<3>(s, st, p, consts);
-        acc.template add<P, 3, R>(sv, sub, st, p);
-      }
+    // the end of a run
+    const int col = B::col_again();
+    const bool mine = col < t.rows, last = k0 >= ke;
+    const int64_t query = t.row0 + min(col, t.rows - 1);
+    const int F = a.sv.F;
+    float* const row = a.nsplit > 1 ? a.part_o + ((int64_t)w.part * a.Nq + query) * F
+                       : a.out32    ? a.out32 + query * F
+                       : a.y_bf16   ? a.part_o + query * F
+                                    : static_cast<float*>(a.out) + query * F;
+    if (begin > kb) {
+      const float then = runs[0][threadIdx.x], f = then == -INFINITY ? 0.f : exp2_fast(then - m);
+      l = fmaf(runs[1][threadIdx.x], f, l);
+      if (mine) acc.template fold<VEC>(f, at_v, Dv, row);
     }
-  }
-  l = col_sum<CT>(l);
-  if (!mine) return;
-  if (a.nsplit > 1) {
-    const int64_t at = ((int64_t)w.part * a.H + w.h) * a.Nq + query;
-    if (G::group() == 0) {
-      a.part_ml[2 * at] = m;
-      a.part_ml[2 * at + 1] = l;
+    if (!last) {
+      runs[0][threadIdx.x] = m;
+      runs[1][threadIdx.x] = l;
+      if (mine) acc.template put<VEC>(1.f, at_v, Dv, row);
+      acc.clear();
+      l = 0.f;
+      continue;
     }
-    acc.template put<VEC>(1.f, at_v, Dv, a.part_o + ((int64_t)w.part * a.Nq + query) * a.sv.F);
+    l = col_sum<CT>(l);
+    if (!mine) return;
+    if (a.nsplit > 1) {
+      const int64_t at = ((int64_t)w.part * a.H + w.h) * a.Nq + query;
+      if (G::group() == 0) {
+        a.part_ml[2 * at] = m;
+        a.part_ml[2 * at + 1] = l;
+      }
+      acc.template put<VEC>(1.f, at_v, Dv, row);
+      return;
+    }
+    const float f = l > 0.f || l != l ? 1.f / l : 0.f;
+    if (a.stat && G::group() == 0) {
+      a.stat[(int64_t)w.h * a.Nq + query] = m;
+      a.stat[(int64_t)(a.H + w.h) * a.Nq + query] = f;
+    }
+    if (a.out32 || !a.y_bf16) acc.template put<VEC>(f, at_v, Dv, row);
+    if (a.y_bf16) acc.template put<VEC>(f, at_v, Dv, static_cast<uint16_t*>(a.out) + query * F);
     return;
   }
-  const float f = l > 0.f || l != l ? 1.f / l : 0.f;
-  if (a.stat && G::group() == 0) {
-    a.stat[(int64_t)w.h * a.Nq + query] = m;
-    a.stat[(int64_t)(a.H + w.h) * a.Nq + query] = f;
-  }
-  if (a.out32) acc.template put<VEC>(f, at_v, Dv, a.out32 + query * a.sv.F);
-  if (a.y_bf16)
-    acc.template put<VEC>(f, at_v, Dv, static_cast<uint16_t*>(a.out) + query * a.sv.F);
-  else
-    acc.template put<VEC>(f, at_v, Dv, static_cast<float*>(a.out) + query * a.sv.F);
 }
+
+// A value of a run after the first joins what is there of those before.
+__device__ __forceinline__ void put_sum(float* o, bool first, float v) { *o = first ? v : *o + v; }
 
 // A column's share of its position's gradient, per part and head.
 template <int CT>
 __device__ __forceinline__ void put_pos(const AttnArgs& a, bool bias, const Work& w, int64_t rows, int64_t row, bool mine,
-                                        BiasSums& b, float f) {
+                                        bool first, BiasSums& b, float f) {
   if (!bias || !a.part_pos) return;
   b.x = col_sum<CT>(b.x);
   b.y = col_sum<CT>(b.y);
@@ -937,9 +998,9 @@ __device__ __forceinline__ void put_pos(const AttnArgs& a, bool bias, const Work
   if (!mine || Geo<CT>::group() != 0) return;
   float* o = a.part_pos + (((int64_t)w.part * a.H + w.h) * rows + row) * 3;
   f *= -a.slope[w.h];
-  o[0] = f * b.x;
-  o[1] = f * b.y;
-  o[2] = f * b.z;
+  put_sum(o, first, f * b.x);
+  put_sum(o + 1, first, f * b.y);
+  put_sum(o + 2, first, f * b.z);
 }
 
 // ---- gradient of the queries ----------------------------------------------------------
@@ -960,9 +1021,8 @@ __global__ __launch_bounds__((Block<T, DC, COLS>::kThreads),
   fill_table<DC>(at_qk, a.sqk, w.h);
   fill_table<DC>(at_v, a.sv, w.h);
   __syncthreads();
-  const int col = B::col();
-  const bool mine = col < t.rows, idle = B::idle(t.rows);
-  const int64_t query = t.row0 + min(col, t.rows - 1);
+  const bool idle = B::idle(t.rows);
+  const int64_t query = t.row0 + min(B::col(), t.rows - 1);
   const int Dqk = a.sqk.D, Dv = a.sv.D;
   const bool bias = has_bias<KIND>(a);
   int64_t kb, ke;
@@ -990,7 +1050,7 @@ __global__ __launch_bounds__((Block<T, DC, COLS>::kThreads),
     for (int e = 0; e < 8; ++e) delta = fmaf(go.v[e], y.v[e], delta);
   }
   delta = col_sum<CT>(delta);
-  if (mine && G::group() == 0 && w.part == 0) a.delta[(int64_t)w.h * a.Nq + query] = delta;
+  if (B::col() < t.rows && G::group() == 0 && w.part == 0) a.delta[(int64_t)w.h * a.Nq + query] = delta;
   const float m = a.stat[(int64_t)w.h * a.Nq + query], inv = a.stat[(int64_t)(a.H + w.h) * a.Nq + query];
   const Place place = place_of(a, bias, a.qpos, query, w.h);
   const floatx4 delta4 = {delta, delta, delta, delta};
@@ -1000,62 +1060,74 @@ __global__ __launch_bounds__((Block<T, DC, COLS>::kThreads),
   BiasSums sums;
   Result<CT, DC> acc;
   acc.clear();
-  for (int64_t k0 = kb; k0 < ke; k0 += R) {
-    const int valid = (int)(ke - k0 < R ? ke - k0 : R);
-    if (!kAhead && (!kFirst || k0 > kb)) load(k0);
-    __syncthreads();
-    rk.put(sk, k0, valid);
-    rv.put(sv, k0, valid);
-    if (bias) rp.put(spos);
-    __syncthreads();
-    if (kAhead && k0 + R < ke) {
-      load(k0 + R);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    for (int sub = idle ? valid : 0; sub < valid; sub += 32) {
-      Tile32<CT> s, ds;
-      s.clear();
-      ds.clear();
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        add_scores<CT, P, P, DC, R>(sk, sub, c, q[c], s);
-        add_scores<CT, P, 3, DC, R>(sv, sub, c, g[c], ds);
+  for (int64_t k0 = kb;;) {
+    const int64_t begin = k0, stop = ke - k0 < kAttnRun ? ke : k0 + kAttnRun;
+    for (; k0 < stop; k0 += R) {
+      const int valid = (int)(ke - k0 < R ? ke - k0 : R);
+      if (!kAhead && (!kFirst || k0 > kb)) load(k0);
+      __syncthreads();
+      rk.put(sk, k0, valid);
+      rv.put(sv, k0, valid);
+      if (bias) rp.put(spos);
+      __syncthreads();
+      if (kAhead && k0 + R < ke) {
+        load(k0 + R);
+        __builtin_amdgcn_sched_barrier(0);
       }
-      with_kind<KIND>(a, cap, s, [&](auto kind, auto bs) {
-        grad_tile<decltype(kind)::value, decltype(bs)::value, R>(
-            cap, c2, s, ds, spos, sub, place, sums,
-            [&](int q4) {  // keys that are not there: a weight of zero
-              floatx4 v;
+      for (int sub = idle ? valid : 0; sub < valid; sub += 32) {
+        Tile32<CT> s, ds;
+        s.clear();
+        ds.clear();
 #pragma unroll
-              for (int e = 0; e < 4; ++e) v[e] = sub + G::first_row(q4) + e < valid ? m : INFINITY;
-              return v;
-            },
-            [&](int) { return delta4; });
-      });
+        for (int c = 0; c < NC; ++c) {
+          add_scores<CT, P, P, DC, R>(sk, sub, c, q[c], s);
+          add_scores<CT, P, 3, DC, R>(sv, sub, c, g[c], ds);
+        }
+        with_kind<KIND>(a, cap, s, [&](auto kind, auto bs) {
+          grad_tile<decltype(kind)::value, decltype(bs)::value, R>(
+              cap, c2, s, ds, spos, sub, place, sums,
+              [&](int q4) {  // keys that are not there: a weight of zero
+                floatx4 v;
 #pragma unroll
-      for (int st = 0; st < kRegs / 8; ++st) {
-        bf16x8 p[3];
-        weights_frag<3>(ds, st, p, consts);
-        acc.template add<P, 3, R>(sk, sub, st, p);
+                for (int e = 0; e < 4; ++e) v[e] = sub + G::first_row(q4) + e < valid ? m : INFINITY;
+                return v;
+              },
+              [&](int) { return delta4; });
+        });
+#pragma unroll
+        for (int st = 0; st < kRegs / 8; ++st) {
+          bf16x8 p[3];
+          weights_frag<3>(ds, st, p, consts);
+          acc.template add<P, 3, R>(sk, sub, st, p);
+        }
       }
     }
-  }
-  put_pos<CT>(a, bias, w, a.Nq, query, mine, sums, inv);
-  if (bias && a.part_slope) {
-    // sum dS d = sum dS (d - mean d) as far as the sum of dS is zero, which it is but for
-    // rounding: the join takes sum dS d - sum dS * sum P d, which does not see that rounding
-    sums.sd = col_sum<CT>(sums.sd);
-    sums.s = col_sum<CT>(sums.s);
-    sums.pd = col_sum<CT>(sums.pd);
-    if (mine && G::group() == 0) {
-      float* o = a.part_slope + (((int64_t)w.part * a.H + w.h) * a.Nq + query) * 3;
-      o[0] = sums.sd * inv;
-      o[1] = sums.s * inv;
-      o[2] = sums.pd * inv;
+    const int col = B::col_again();
+    const bool mine = col < t.rows, first = begin == kb, last = k0 >= ke;
+    const int64_t query = t.row0 + min(col, t.rows - 1);
+    put_pos<CT>(a, bias, w, a.Nq, query, mine, first, sums, inv);
+    if (bias && a.part_slope) {
+      // sum dS d = sum dS (d - mean d) as far as the sum of dS is zero, which it is but for
+      // rounding: the join takes sum dS d - sum dS * sum P d, which does not see that rounding
+      sums.sd = col_sum<CT>(sums.sd);
+      sums.s = col_sum<CT>(sums.s);
+      sums.pd = col_sum<CT>(sums.pd);
+      if (mine && G::group() == 0) {
+        float* o = a.part_slope + (((int64_t)w.part * a.H + w.h) * a.Nq + query) * 3;
+        put_sum(o, first, sums.sd * inv);
+        put_sum(o + 1, first, sums.s * inv);
+        put_sum(o + 2, first, sums.pd * inv);
+      }
     }
+    if (a.gq && mine) {
+      float* const row = a.gq + ((int64_t)w.part * a.Nq + query) * a.ldgq;
+      if (!first) acc.template fold<VEC>(1.f, at_qk, Dqk, row);
+      acc.template put<VEC>(last ? a.scale * inv : 1.f, at_qk, Dqk, row);
+    }
+    if (last) break;
+    acc.clear();
+    sums = BiasSums();
   }
-  if (a.gq && mine)
-    acc.template put<VEC>(a.scale * inv, at_qk, Dqk, a.gq + ((int64_t)w.part * a.Nq + query) * a.ldgq);
 }
 
 // ---- gradients of keys and values --------------------------------------------------------
@@ -1086,9 +1158,8 @@ __global__ __launch_bounds__((Block<T, DC, COLS>::kThreads),
   fill_table<DC>(at_qk, a.sqk, w.h);
   fill_table<DC>(at_v, a.sv, w.h);
   __syncthreads();
-  const int col = B::col();
-  const bool mine = col < t.rows, idle = B::idle(t.rows);
-  const int64_t key = t.row0 + min(col, t.rows - 1);
+  const bool idle = B::idle(t.rows);
+  const int64_t key = t.row0 + min(B::col(), t.rows - 1);
   const int Dqk = a.sqk.D, Dv = a.sv.D;
   const bool bias = has_bias<KIND>(a);
   int64_t qb, qe;
@@ -1124,66 +1195,86 @@ __global__ __launch_bounds__((Block<T, DC, COLS>::kThreads),
   Result<CT, DC> gv, gk;
   gv.clear();
   gk.clear();
-  for (int64_t q0 = qb; q0 < qe; q0 += R) {
-    const int valid = (int)(qe - q0 < R ? qe - q0 : R);
-    if (!kAhead && (!kFirst || q0 > qb)) load(q0);
-    __syncthreads();
-    rq.put(sq, q0, valid);
-    rg.put(sg, q0, valid);
-    if (bias) rp.put(spos);
-    if ((int)threadIdx.x < R) {
-      sl[threadIdx.x] = row_m;
-      sd[threadIdx.x] = row_d;
-    }
-    __syncthreads();
-    if (kAhead && q0 + R < qe) {
-      load(q0 + R);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    for (int sub = idle ? valid : 0; sub < valid; sub += 32) {
-      Tile32<CT> s, ds;
-      s.clear();
-      ds.clear();
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        add_scores<CT, P, P, DC, R>(sq, sub, c, k[c], s);
-        if constexpr (PART != kValues) add_scores<CT, 3, P, DC, R>(sg, sub, c, v[c], ds);
+  for (int64_t q0 = qb;;) {
+    const int64_t begin = q0, stop = qe - q0 < kAttnRun ? qe : q0 + kAttnRun;
+    for (; q0 < stop; q0 += R) {
+      const int valid = (int)(qe - q0 < R ? qe - q0 : R);
+      if (!kAhead && (!kFirst || q0 > qb)) load(q0);
+      __syncthreads();
+      rq.put(sq, q0, valid);
+      rg.put(sg, q0, valid);
+      if (bias) rp.put(spos);
+      if ((int)threadIdx.x < R) {
+        sl[threadIdx.x] = row_m;
+        sd[threadIdx.x] = row_d;
       }
-      with_kind<KIND>(a, cap, s, [&](auto kind, auto bs) {
-        if constexpr (PART == kValues) {
-          score_tile<decltype(kind)::value, decltype(bs)::value, R>(cap, c2, s, spos, sub, place);
-          const float unit = decltype(kind)::value == kNoCap && !decltype(bs)::value ? c2 : 1.f;
+      __syncthreads();
+      if (kAhead && q0 + R < qe) {
+        load(q0 + R);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      for (int sub = idle ? valid : 0; sub < valid; sub += 32) {
+        Tile32<CT> s, ds;
+        s.clear();
+        ds.clear();
 #pragma unroll
-          for (int q4 = 0; q4 < G::kQuads; ++q4) {
-            const floatx4 m4 = *reinterpret_cast<const floatx4*>(sl + sub + G::first_row(q4));
+        for (int c = 0; c < NC; ++c) {
+          add_scores<CT, P, P, DC, R>(sq, sub, c, k[c], s);
+          if constexpr (PART != kValues) add_scores<CT, 3, P, DC, R>(sg, sub, c, v[c], ds);
+        }
+        with_kind<KIND>(a, cap, s, [&](auto kind, auto bs) {
+          if constexpr (PART == kValues) {
+            score_tile<decltype(kind)::value, decltype(bs)::value, R>(cap, c2, s, spos, sub, place);
+            const float unit = decltype(kind)::value == kNoCap && !decltype(bs)::value ? c2 : 1.f;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s.set(4 * q4 + e, weight_again(fmaf(s.get(4 * q4 + e), unit, -m4[e])));
+            for (int q4 = 0; q4 < G::kQuads; ++q4) {
+              const floatx4 m4 = *reinterpret_cast<const floatx4*>(sl + sub + G::first_row(q4));
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s.set(4 * q4 + e, weight_again(fmaf(s.get(4 * q4 + e), unit, -m4[e])));
+            }
+            return;
           }
-          return;
-        }
-        grad_tile<decltype(kind)::value, decltype(bs)::value, R>(
-            cap, c2, s, ds, spos, sub, place, sums,
-            [&](int q4) { return *reinterpret_cast<const floatx4*>(sl + sub + G::first_row(q4)); },
-            [&](int q4) { return *reinterpret_cast<const floatx4*>(sd + sub + G::first_row(q4)); });
-      });
+          grad_tile<decltype(kind)::value, decltype(bs)::value, R>(
+              cap, c2, s, ds, spos, sub, place, sums,
+              [&](int q4) { return *reinterpret_cast<const floatx4*>(sl + sub + G::first_row(q4)); },
+              [&](int q4) { return *reinterpret_cast<const floatx4*>(sd + sub + G::first_row(q4)); });
+        });
 #pragma unroll
-      for (int st = 0; st < kRegs / 8; ++st) {
-        bf16x8 p[3];
-        if constexpr (PART != kKeys) {
-          weights_frag<3>(s, st, p, consts);
-          gv.template add<3, 3, R>(sg, sub, st, p);
-        }
-        if constexpr (PART != kValues) {
-          weights_frag<3>(ds, st, p, consts);
-          gk.template add<P, 3, R>(sq, sub, st, p);
+        for (int st = 0; st < kRegs / 8; ++st) {
+          bf16x8 p[3];
+          if constexpr (PART != kKeys) {
+            weights_frag<3>(s, st, p, consts);
+            gv.template add<3, 3, R>(sg, sub, st, p);
+          }
+          if constexpr (PART != kValues) {
+            weights_frag<3>(ds, st, p, consts);
+            gk.template add<P, 3, R>(sq, sub, st, p);
+          }
         }
       }
     }
+    const int col = B::col_again();
+    const bool mine = col < t.rows, first = begin == qb, last = q0 >= qe;
+    const int64_t key = t.row0 + min(col, t.rows - 1);
+    if constexpr (PART != kValues) {
+      put_pos<CT>(a, bias, w, a.Nk, key, mine, first, sums, 1.f);
+      if (a.gk && mine) {
+        float* const row_k = a.gk + ((int64_t)w.part * a.Nk + key) * a.ldgk;
+        if (!first) gk.template fold<VEC>(1.f, at_qk, Dqk, row_k);
+        gk.template put<VEC>(last ? a.scale : 1.f, at_qk, Dqk, row_k);
+      }
+    }
+    if constexpr (PART != kKeys)
+      if (a.gv && mine) {
+        float* const row_v = a.gv + ((int64_t)w.part * a.Nk + key) * a.ldgv;
+        if (!first) gv.template fold<VEC>(1.f, at_v, Dv, row_v);
+        gv.template put<VEC>(1.f, at_v, Dv, row_v);
+      }
+    if (last) break;
+    gk.clear();
+    gv.clear();
+    sums = BiasSums();
   }
-  if constexpr (PART != kValues) put_pos<CT>(a, bias, w, a.Nk, key, mine, sums, 1.f);
-  if (!mine) return;
-  if (PART != kValues && a.gk) gk.template put<VEC>(a.scale, at_qk, Dqk, a.gk + ((int64_t)w.part * a.Nk + key) * a.ldgk);
-  if (PART != kKeys && a.gv) gv.template put<VEC>(1.f, at_v, Dv, a.gv + ((int64_t)w.part * a.Nk + key) * a.ldgv);
 }
 
 }  // namespace attn

@@ -41,7 +41,8 @@ extern "C" {
  * The inner product runs over all rows of the irreps, so that scores do not
  * change under rotations and outputs rotate as the values do.  A query whose
  * graph has no keys gets zeros.  Products of fp32 operands are within 2^-25 of
- * their values; inputs must stay below 3.38e38, scores within fp32 range and distances below
+ * their values, and sums over more than 4096 rows of a graph are made in runs of
+ * so many; inputs must stay below 3.38e38, scores within fp32 range and distances below
  * 1.8e19.  A value that is not finite shows in results of its own graph and head alone. */
 typedef struct tpconv_attention_s* tpconv_attention;
 
@@ -95,8 +96,11 @@ typedef struct {
  * bf16 output, [num_queries][feat_v], the output before its rounding. */
 tpconv_status tpconv_attention_saved_size(tpconv_attention attention, int64_t num_queries, int64_t* values);
 
-/* Bytes of workspace of TPCONV_OP_FORWARD (may be 0) and TPCONV_OP_BACKWARD for
- * a batch of these counts (its pointers are only compared with NULL). */
+/* Bytes of workspace of TPCONV_OP_FORWARD (may be 0; with `saved` it may need
+ * less) and TPCONV_OP_BACKWARD for a batch of these counts (its pointers are only
+ * compared with NULL).  At most 64 fp32 copies of the results: where there are few
+ * rows, which are then worked on in parts of the other side, and up to eight where
+ * the mean graph has more than 4096 rows. */
 tpconv_status tpconv_attention_workspace_size(tpconv_attention attention, int32_t op,
                                               const tpconv_attention_batch* batch, size_t* bytes);
 

@@ -92,3 +92,78 @@ def test_a_nan_under_a_weight_of_zero_shows_whether_the_launch_is_cut_into_parts
         # the others are a sum times 1 / l, which is rounded, as each of the at most 64 parts' products is: 65 U off, not 0
         out[0, 3] = 1.0
         assert torch.all((out - 1.0).abs() <= 65 * U)
+
+# ---- long graphs among many small ones ------------------------------------------------------
+
+LONG, GRAPHS = 40000, 128
+
+
+@pytest.mark.parametrize("xb", [False, True])
+def test_sums_of_a_long_graph_among_small_ones(at, xb):  # noqa: F811
+    """Equal weights over LONG keys.  fp32: values 1 + 2^-16, whose second pieces the matrix instructions add eight at a time
+    (2^-13): exact while the sum is below 2^11, and lost beside it from there on, half a unit in its last place or less.  A run
+    of 4096 keys loses 2^-16 (4096 - 2^11) / 4096 = 2^-17 of itself at most; one run over the graph would lose 2^-16 (LONG -
+    2^11) / LONG = 1.45e-5, twice as much as is allowed.  bf16: every other value 2^-14 in place of one, eight at a time 4 +
+    2^-12: exact below 2^12, which a run's sum of 2^11 does not reach; one run over the graph would lose 4.8e-5.  The runs'
+    sums, the division and the product are rounded: LONG / 4096 + 2 roundings, relative to a mean of terms of one sign."""
+    import torch
+
+    say(f"[case] long graph forward x={'bf16' if xb else 'f32'}")
+    n = LONG + 30 * (GRAPHS - 1)
+    row = np.full(n, 1 + 2.0 ** -16) if not xb else np.where(np.arange(n) % 2 == 0, 1.0, 2.0 ** -14)
+    v = cuda(np.repeat(row[:, None], 64, 1), xb)
+    assert np.all(f64(v[:, 0]) == row)  # exact in its type
+    code = (at.TPCONV_F32, at.TPCONV_BF16)[xb]
+    h = at.Attention("64x0e", "64x0e", 8, 1.0, 0.0, code, code)
+    b = at.Batch(GRAPHS, offsets((1,) * GRAPHS), None, n, offsets((LONG,) + (30,) * (GRAPHS - 1)))
+    q, k = torch.zeros_like(v[:GRAPHS]), torch.randn(n, 64, device="cuda").to(v.dtype)
+    saved = torch.empty(h.saved_size(GRAPHS), device="cuda")
+    out = at.tpconv_attention_forward(h, b, q, k, v, saved=saved)
+    got = f64(saved[2 * 8 * GRAPHS:].view(GRAPHS, 64)[0] if xb else out[0])
+    mean = row[:LONG].mean()
+    lost = 0.0 if xb else 2.0 ** -17
+    assert np.all(np.abs(got - mean) <= (lost + (LONG / 4096 + 2) * U) * mean), np.abs(got / mean - 1).max()
+    assert torch.equal(out, at.tpconv_attention_forward(h, b, q, k, v))
+
+
+@pytest.mark.parametrize("xb", [False, True])
+def test_gradient_sums_of_a_long_graph_among_small_ones(at, xb):  # noqa: F811
+    """The same with LONG queries of one key each: the gradient of its value is the sum of their grad_out, 1 + 2^-16, in
+    three pieces whatever the inputs' type."""
+    import torch
+
+    say(f"[case] long graph gradient x={'bf16' if xb else 'f32'}")
+    n = LONG + 30 * (GRAPHS - 1)
+    code = (at.TPCONV_F32, at.TPCONV_BF16)[xb]
+    h = at.Attention("64x0e", "64x0e", 8, 1.0, 0.0, code, code)
+    b = at.Batch(n, offsets((LONG,) + (30,) * (GRAPHS - 1)), None, GRAPHS, offsets((1,) * GRAPHS))
+    q, k = (torch.randn(m, 64, device="cuda").to((torch.float32, torch.bfloat16)[xb]) for m in (n, GRAPHS))
+    saved = torch.empty(h.saved_size(n), device="cuda")
+    out = at.tpconv_attention_forward(h, b, q, k, k, saved=saved)
+    go = torch.full((n, 64), 1 + 2.0 ** -16, device="cuda")
+    _, _, gv, *_ = at.tpconv_attention_backward(h, b, q, k, k, out, saved, go, want=("v",))
+    want = LONG * (1 + 2.0 ** -16)
+    allowed = (2.0 ** -17 + (LONG / 4096 + 2) * U) * want
+    assert np.all(np.abs(f64(gv[0]) - want) <= allowed), np.abs(f64(gv[0]) / want - 1).max()
+
+
+@pytest.mark.parametrize("qk,v,heads", [("16x0e", "8x0e+8x1o", 2), ("5x0e+2x1o", "3x0e+2x1o", 1), ("160x0e", "100x0e", 1)])
+@pytest.mark.parametrize("xb,yb", [(False, False), (True, True)])
+@pytest.mark.parametrize("cap,bias", [(0.0, True), (3.0, False)])
+def test_several_runs_of_rows(at, qk, v, heads, xb, yb, cap, bias):  # noqa: F811
+    """Graphs longer than one run, in whole runs and beyond: references that move from run to run, sums kept in the results."""
+    for lens, key_lens in (((4500, 7), None), ((3, 40), (8192, 9)), ((4097, 1), (33, 2))):
+        say(f"[case] runs {qk} {v} {lens} {key_lens} x={'bf16' if xb else 'f32'} cap={cap} bias={bias}")
+        Case(qk, v, heads, lens, key_lens, xb, yb, cap, bias, 34).check(at)
+
+
+@pytest.mark.parametrize("xb", [False, True])
+def test_scores_that_grow_from_run_to_run(at, xb):  # noqa: F811
+    """The largest score of each run far above those before, and far below: keys times 1, 20, 3 and 60."""
+    import torch
+
+    say(f"[case] growing scores x={'bf16' if xb else 'f32'}")
+    c = Case("16x0e", "16x0e", 1, (40, 900), (13000, 5), xb, xb, 0.0, False, 35)
+    for run in range(4):
+        c.k[4096 * run:4096 * (run + 1)] *= (1, 20, 3, 60)[run]
+    c.check(at)
