@@ -167,3 +167,66 @@ def test_scores_that_grow_from_run_to_run(at, xb):  # noqa: F811
     for run in range(4):
         c.k[4096 * run:4096 * (run + 1)] *= (1, 20, 3, 60)[run]
     c.check(at)
+
+# ---- offsets that decrease or leave the rows ------------------------------------------------
+
+
+class Guarded:
+    """Tensors between margins of marks, which no kernel may touch."""
+
+    def __init__(self):
+        self.made = []
+
+    def __call__(self, shape, fill=0.0, dtype=None, margin=4096):
+        import torch
+
+        dtype = dtype or torch.float32
+        n = int(np.prod(shape))
+        whole = torch.full((n + 2 * margin,), 77, dtype=dtype, device="cuda")
+        t = whole[margin:margin + n].view(shape)
+        t.fill_(fill)
+        self.made.append((whole, margin, n))
+        return t
+
+    def check(self):
+        for whole, margin, n in self.made:
+            assert bool((whole[:margin] == 77).all()) and bool((whole[margin + n:] == 77).all())
+
+
+BAD = [[0, 50, 20, 64], [-5, 10, 1000, 2000], [64, 0, 64, 0], [2 ** 31 - 1, -2 ** 31, 5, 64], [64, 64, 0, 0], [3, 3, 3, 3]]
+
+
+@pytest.mark.parametrize("xb", [False, True])
+@pytest.mark.parametrize("n,heads", [(64, 2), (700, 1)])  # whole, and cut into parts both ways
+@pytest.mark.parametrize("bias", [False, True])
+def test_bad_offsets_write_inside_their_tensors(at, xb, n, heads, bias):  # noqa: F811
+    """Outputs, saved values, every gradient and a workspace of just the size that is needed keep their margins; self form and
+    cross form, offsets of the queries, of the keys, and of both."""
+    import torch
+
+    code = (at.TPCONV_F32, at.TPCONV_BF16)[xb]
+    h = at.Attention("8x0e", "8x0e", heads, 0.3, 0.0, code, code)
+    good = [0, n // 3, n // 2, n]
+    for bad in BAD:
+        bad = [v * (n // 64) if 0 <= v <= 64 else v for v in bad]
+        for mine, keys in ((bad, None), (bad, good), (good, bad), (bad, bad)):
+            say(f"[case] bad offsets {mine} {keys} n={n} x={'bf16' if xb else 'f32'} bias={bias}")
+            g = Guarded()
+            off = [None if o is None else torch.tensor(o, dtype=torch.int64).to(torch.int32).cuda() for o in (mine, keys)]
+            x = [cuda(np.random.default_rng(i).standard_normal((n, 8)), xb) for i in range(3)]
+            pos = cuda(np.random.default_rng(3).standard_normal((n, 3))) if bias else None
+            slope = torch.full((heads,), 0.5, device="cuda") if bias else None
+            batch = at.Batch(n, off[0], pos, *(() if keys is None else (n, off[1], pos)))
+            out, saved = g((n, 8), dtype=x[0].dtype), g((h.saved_size(n),))
+            size = lambda op: g((h.workspace_size(batch, op),), 0, torch.uint8)  # noqa: E731
+            at.tpconv_attention_forward(h, batch, *x, slope=slope, out=out, saved=saved, workspace=size(at.OP_FORWARD))
+            at.tpconv_attention_forward(h, batch, *x, slope=slope, out=out, workspace=size(at.OP_FORWARD))
+            grads = dict(grad_q=g((n, 8)), grad_k=g((n, 8)), grad_v=g((n, 8)))
+            if bias:
+                grads.update(grad_slope=g((heads,)), grad_pos=g((n, 3)))
+                if keys is not None:
+                    grads["grad_key_pos"] = g((n, 3))
+            at.tpconv_attention_backward(h, batch, *x, out, saved, g((n, 8), 1.0), slope=slope, want=(),
+                                         workspace=size(at.OP_BACKWARD), **grads)
+            torch.cuda.synchronize()
+            g.check()
