@@ -266,7 +266,9 @@ def prepare(case, seed):
                                   code[case["y"]])
         s["batch"] = at.Batch(case["queries"], _offsets(lq), s.get("pos"),
                               *((case["keys"], _offsets(lk), s.get("key_pos")) if case["keys"] else ()))
-        size = s["layer"].workspace_size(s["batch"], at.OP_BACKWARD if case["mode"] == "train" else at.OP_FORWARD)
+        # one workspace for both directions of a training step: few queries over many keys need more in the forward
+        size = max(s["layer"].workspace_size(s["batch"], op)
+                   for op in ((at.OP_FORWARD, at.OP_BACKWARD) if case["mode"] == "train" else (at.OP_FORWARD,)))
     s["workspace"] = torch.empty(max(1, size), dtype=torch.uint8, device="cuda")
     return s
 
