@@ -265,10 +265,13 @@ tpconv_status tpconv_attention_forward(tpconv_attention attention, const tpconv_
   a.out = out;
   a.stat = saved;
   if (saved && a.y_bf16) a.out32 = saved + 2 * a.Nq * a.H;
-  a.part_o = ws + p.part_o;
+  const bool parts = p.fwd.nsplit > 1;
+  a.sums = parts || (a.y_bf16 && !saved) ? ws + p.part_o : a.y_bf16 ? a.out32 : static_cast<float*>(out);
+  a.put_f32 = parts || !a.y_bf16 || saved;
+  a.put_bf16 = !parts && a.y_bf16;
   a.part_ml = ws + p.part_ml;
   st = dev(launch_attn_forward(a, p.fwd, s));
-  if (st == TPCONV_SUCCESS && p.fwd.nsplit > 1) st = dev(launch_attn_combine(a, p.fwd, s));
+  if (st == TPCONV_SUCCESS && parts) st = dev(launch_attn_combine(a, p.fwd, s));
   return st;
 }
 

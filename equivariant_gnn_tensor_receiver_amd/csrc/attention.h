@@ -39,7 +39,8 @@ struct AttnArgs {
   void* out;
   float* stat;              // [2][H][Nq]: the references of the rows' weights and 1 / their sums; NULL: not saved
   float* out32;             // fp32 output of a bf16 forward that saves, or NULL
-  float *part_o, *part_ml;  // [nsplit][Nq][F_v], [nsplit][H][Nq][2]; one part: sums of runs where no result is fp32
+  float *sums, *part_ml;    // [nsplit][Nq][F_v], [nsplit][H][Nq][2]; sums: with one part the fp32 result, or room for runs
+  int32_t put_f32, put_bf16;  // whether the kernel's last sums go to `sums`, and rounded to out
   // backward
   const float* go;
   const float* o;           // fp32 output

@@ -79,7 +79,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const AttnArgs a) {
         float o = 0.f;
 #pragma unroll 8
         for (int p = 0; p < S; ++p) {
-          const float v = a.part_o[((int64_t)p * a.Nq + query) * F + i];
+          const float v = a.sums[((int64_t)p * a.Nq + query) * F + i];
           o = fmaf(w[p], v, o);  // (also under a factor of zero: a NaN shows as in a launch without parts)
         }
         if (a.out32) a.out32[query * F + i] = o;

@@ -945,43 +945,40 @@ __global__ __launch_bounds__((Block<T, DC, COLS>::kThreads), (waves_for(regs_for
     const bool mine = col < t.rows, last = k0 >= ke;
     const int64_t query = t.row0 + min(col, t.rows - 1);
     const int F = a.sv.F;
-    float* const row = a.nsplit > 1 ? a.part_o + ((int64_t)w.part * a.Nq + query) * F
-                       : a.out32    ? a.out32 + query * F
-                       : a.y_bf16   ? a.part_o + query * F
-                                    : static_cast<float*>(a.out) + query * F;
+    float* const row = a.sums + ((int64_t)w.part * a.Nq + query) * F;
     if (begin > kb) {
       const float then = runs[0][threadIdx.x], f = then == -INFINITY ? 0.f : exp2_fast(then - m);
       l = fmaf(runs[1][threadIdx.x], f, l);
       if (mine) acc.template fold<VEC>(f, at_v, Dv, row);
     }
-    if (!last) {
-      runs[0][threadIdx.x] = m;
-      runs[1][threadIdx.x] = l;
-      if (mine) acc.template put<VEC>(1.f, at_v, Dv, row);
-      acc.clear();
-      l = 0.f;
-      continue;
-    }
-    l = col_sum<CT>(l);
-    if (!mine) return;
-    if (a.nsplit > 1) {
-      const int64_t at = ((int64_t)w.part * a.H + w.h) * a.Nq + query;
-      if (G::group() == 0) {
-        a.part_ml[2 * at] = m;
-        a.part_ml[2 * at + 1] = l;
-      }
-      acc.template put<VEC>(1.f, at_v, Dv, row);
-      return;
-    }
-    const float f = l > 0.f || l != l ? 1.f / l : 0.f;
-    if (a.stat && G::group() == 0) {
-      a.stat[(int64_t)w.h * a.Nq + query] = m;
-      a.stat[(int64_t)(a.H + w.h) * a.Nq + query] = f;
-    }
-    if (a.out32 || !a.y_bf16) acc.template put<VEC>(f, at_v, Dv, row);
-    if (a.y_bf16) acc.template put<VEC>(f, at_v, Dv, static_cast<uint16_t*>(a.out) + query * F);
-    return;
+    if (last) break;
+    runs[0][threadIdx.x] = m;
+    runs[1][threadIdx.x] = l;
+    if (mine) acc.template put<VEC>(1.f, at_v, Dv, row);
+    acc.clear();
+    l = 0.f;
   }
+  l = col_sum<CT>(l);
+  const int col = B::col_again();
+  if (col >= t.rows) return;
+  const int64_t own = t.row0 + col;
+  const int F = a.sv.F;
+  float f = 1.f;
+  if (a.nsplit > 1) {
+    const int64_t at = ((int64_t)w.part * a.H + w.h) * a.Nq + own;
+    if (G::group() == 0) {
+      a.part_ml[2 * at] = m;
+      a.part_ml[2 * at + 1] = l;
+    }
+  } else {
+    f = l > 0.f || l != l ? 1.f / l : 0.f;
+    if (a.stat && G::group() == 0) {
+      a.stat[(int64_t)w.h * a.Nq + own] = m;
+      a.stat[(int64_t)(a.H + w.h) * a.Nq + own] = f;
+    }
+  }
+  if (a.put_f32) acc.template put<VEC>(f, at_v, Dv, a.sums + ((int64_t)w.part * a.Nq + own) * F);
+  if (a.put_bf16) acc.template put<VEC>(f, at_v, Dv, static_cast<uint16_t*>(a.out) + own * F);
 }
 
 // A value of a run after the first joins what is there of those before.
