@@ -211,7 +211,8 @@ def tpconv_attention_forward(attn: Attention, batch: Batch, q, k, v, slope=None,
                              stream=None):
     """out [num_queries][F_v].  slope: fp32 [num_heads], for the bias -slope |r_i - r_j| (needs the batch's positions).
     saved: fp32 tensor of attn.saved_size(num_queries) values for the backward.  Rows outside of all graphs are not
-    written."""
+    written: in a result that the call makes they hold anything, so that padded batches, whose next layer runs over all
+    rows, pass a cleared `out`."""
     dev = ly._device(q, "q")
     args = _attention_inputs(attn, batch, q, k, v, slope, dev)
     n = batch.num_queries
@@ -233,7 +234,7 @@ def tpconv_attention_backward(attn: Attention, batch: Batch, q, k, v, out, saved
     """(grad_q, grad_k, grad_v, grad_slope, grad_pos, grad_key_pos) for the names in `want` ("q", "k", "v", "slope",
     "pos"), fp32; the others are None.  grad_pos is of the queries' positions, and in the self form of the nodes';
     grad_key_pos comes with "pos" in the cross form.  out, saved: of the forward on the same inputs.  Rows outside of
-    all graphs are not written."""
+    all graphs are not written, in gradients that the call makes neither (padded batches pass cleared ones)."""
     dev = ly._device(q, "q")
     args = _attention_inputs(attn, batch, q, k, v, slope, dev)
     nq, nk, f32 = batch.num_queries, batch.num_keys, torch.float32
@@ -360,8 +361,8 @@ def _dropout_nodes(drop, t, name):
 
 
 def tpconv_dropout_forward(drop: Dropout, x, rng, residual=None, out=None, stream=None):
-    """residual + dropout(x), in x's shape.  rng: int64 [2] = (seed, offset) on the device, read when the kernel runs.
-    out may be residual, or x if their types agree."""
+    """residual + dropout(x), in x's shape.  rng: int64 [2] = (seed, offset) on the device, read when the kernel runs;
+    calls with the same values draw the same mask, so that every layer of every step needs an offset of its own.  out may be residual, or x if their types agree."""
     dev = ly._device(x, "x")
     n = _dropout_nodes(drop, x, "x")
     ly._need(x, "x", drop.x_dtype, n * drop.features, dev)

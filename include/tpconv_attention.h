@@ -65,7 +65,8 @@ tpconv_status tpconv_attention_info(tpconv_attention attention, int64_t* feat_qk
 
 /* Which rows belong together.  Graph g's queries are the rows offsets[g] ..
  * offsets[g + 1] - 1; rows outside of all graphs are left as they were in
- * every output.  offsets NULL: one graph of all rows (num_graphs = 1).
+ * every output (a caller that goes on with whole tensors, as a layer over padded
+ * batches does, clears them once).  offsets NULL: one graph of all rows (num_graphs = 1).
  * key_offsets NULL: the keys are the queries' own nodes (self form; num_keys
  * and key_pos are not read); otherwise graph g's keys are the rows
  * key_offsets[g] .. of k and v, and there may be none.  Offsets must not
@@ -163,7 +164,9 @@ tpconv_status tpconv_embed_backward(tpconv_embed embed, int64_t num_nodes, const
  * words each, low word first, and key seed (low word first): word w is the low
  * (w even) or high half of output w / 2.  u_i counts the groups of eight
  * channels of the irreps before i, U those of all.  The channel is kept if the
- * word is at least t = round(65536 p); p' = t / 65536.  t = 65536 keeps none. */
+ * word is at least t = round(65536 p); p' = t / 65536.  t = 65536 keeps none.
+ * The mask depends on seed, offset and irreps alone: every call that shall draw for
+ * itself (each layer of each step) needs an offset of its own. */
 typedef struct tpconv_dropout_s* tpconv_dropout;
 
 typedef struct {

@@ -230,3 +230,39 @@ def test_bad_offsets_write_inside_their_tensors(at, xb, n, heads, bias):  # noqa
                                          workspace=size(at.OP_BACKWARD), **grads)
             torch.cuda.synchronize()
             g.check()
+
+
+# ---- padded batches ---------------------------------------------------------------------------
+
+
+def test_a_padded_batch_with_cleared_results_through_the_next_layer(at):  # noqa: F811
+    """Rows behind the last graph: NaN in the inputs, zeros in the results that the caller made; the next layer runs over all
+    rows.  Its weight gradient is a sum of products within 2^-21 of theirs over 3 rows of N nodes, added in fp32."""
+    import torch
+    from equivariant_gnn_tensor_receiver_amd import layers
+    from oracle import layers as ol
+
+    say("[case] padded batch")
+    irreps, pad = "8x0e+8x1o", 61
+    c = Case(irreps, irreps, 2, (7, 40), bias=True, seed=36)
+    n, whole = c.nq, c.nq + pad
+    grown = lambda t, fill: torch.cat([t, torch.full((pad, t.shape[1]), fill, device="cuda")])  # noqa: E731
+    nan = float("nan")
+    q, k, v, pos, g = (grown(t, nan) for t in (c.q, c.k, c.v, c.pos, c.g))
+    h, batch = c.layer(at), at.Batch(whole, offsets(c.lens), pos)
+    zeros = lambda f: torch.zeros(whole, f, device="cuda")  # noqa: E731
+    saved = torch.empty(h.saved_size(whole), device="cuda")
+    out = at.tpconv_attention_forward(h, batch, q, k, v, slope=c.slope, out=zeros(32), saved=saved)
+    grads = at.tpconv_attention_backward(h, batch, q, k, v, out, saved, g, slope=c.slope, want=("slope",), grad_q=zeros(32),
+                                         grad_k=zeros(32), grad_v=zeros(32), grad_pos=zeros(3))
+    ref_out, _, _, ref = c.run(at)
+    for t, r in ((out, ref_out), *zip((*grads[:3], grads[4]), (*ref[:3], ref[4]))):
+        assert torch.equal(t[:n], r) and torch.all(t[n:] == 0)
+    assert torch.equal(grads[3], ref[3])
+    lin = layers.Linear(irreps, irreps, 1)
+    W = torch.randn(lin.w_shape, device="cuda")
+    _, gW = layers.tpconv_linear_backward(lin, layers.Groups(whole), out, W, grown(c.g, 1.0))
+    one = np.zeros(n, dtype=np.int64)
+    want = np.asarray(ol.linear_backward(irreps, irreps, one, f64(ref_out), f64(W), f64(c.g))[1])
+    mag = np.asarray(ol.linear_backward(irreps, irreps, one, np.abs(f64(ref_out)), np.abs(f64(W)), np.abs(f64(c.g)))[1])
+    near(gW.reshape(want.shape), want, (2.0 ** -21 + 3 * n * U) * mag, "weight gradient")
