@@ -177,15 +177,17 @@ AttnShape attn_shape(int D, int64_t rows, int64_t other, int64_t graphs, int hea
   s.cols = rows / g >= 96 ? 128 : attn_small_cols(kWidth[s.cls]);
   const int64_t m = s.cols;
   s.tiles = rows / m + g;
-  // too few blocks for the 256 CUs: cut the long axis, 64 rows of it at least per part, into as many
-  // blocks as the CUs hold at once (16 queries over 32768 keys of 288 values, 4 heads: 512 blocks
-  // 62 us, 768 53, 1024 64, 2048 71)
+  // too few blocks for the 256 CUs: cut the long axis, 64 rows of it at least per part, into 768 blocks, of
+  // 128 columns into 512, whatever a CU holds of the kernel.  us at 256, 512, 768 and 1024 blocks: 16 queries in
+  // 16 graphs over 32768 keys, fp32, 32 values per head 71, 47, 36, 30; 72 values 88, 56, 48, 56; bf16, 32 values
+  // 77, 47, 36, 30; 128 values 51, 32, 30, 26; fp32, 256 values (128 columns) 68, 76, 83, 90; training of
+  // 1024 nodes in one graph, 4 heads of 64 (128 columns), fp32 74, 95, 94, 94; bf16 67, 81, 81, 81
   const int64_t blocks = std::max<int64_t>((rows + m - 1) / m, std::min(rows, g)) * heads;
   const int64_t most = std::max<int64_t>(1, other / g / 64), enough = s.cols < 128 ? 768 : 512;
   s.nsplit = (int)std::min<int64_t>(std::min<int64_t>(kMaxParts, most), std::max<int64_t>(1, enough / std::max<int64_t>(1, blocks)));
   // more than 4096 rows: at least a part for each of them, up to eight, so that blocks which do not come out
   // even on the CUs are short (16384 nodes in one graph, fp32, 4 heads of 64, training: 12.1 ms in one
-  // part, 7.8 in four).  Not for bf16 results, which fp32 parts would be several times the size of.
+  // part, 7.8 in four; 8 heads of 144 38.6 and 38.7).  Not for bf16 results, which fp32 parts would be several times the size of.
   if (exact) s.nsplit = (int)std::max<int64_t>(s.nsplit, std::min<int64_t>(8, (other / g + 4095) / 4096));
   return s;
 }

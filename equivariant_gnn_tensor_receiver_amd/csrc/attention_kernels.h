@@ -21,7 +21,7 @@
 // SIMD.  fp32, and bf16 heads wider than 96, take 16 columns and v_mfma_f32_16x16x32_bf16, eight waves per block:
 // its three pieces per operand would leave room for one wave of 32 columns per SIMD
 // only, whose products and vector work then follow one another (8192 nodes of
-// 128x0e+128x1o+128x2e, 8 heads: forward 369 us, gradients 725 and 1130; now 265, 420 and 668).
+// 128x0e+128x1o+128x2e, 8 heads: forward 369 us, gradients 725 and 1130; this way 270, 334 and 593).
 //
 // Precision: an fp32 operand is the sum of three bf16 pieces, each the rounded
 // rest of those before (|p1| <= 2^-9 |x|, |p2| <= 2^-18 |x|, 2^-27 |x| is left out),
@@ -532,8 +532,8 @@ __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_ex
 // share its L2.  Large graphs: the tiles of a head together, whose other side the L2
 // then holds.  Small graphs: the heads of a tile together, since a line of memory holds
 // several heads' channels, and eight XCDs that each read every line, and write parts of
-// it, cost more than the work (128 graphs of 32 nodes, 8 heads of 36 values: forward
-// 25 us, 14 this way).
+// it, cost more than the work (128 graphs of 32 nodes, 8 heads of 36 values, fp32, biased:
+// forward and the two gradient kernels 33, 43 and 42 us, this way 24, 29 and 31).
 struct Work {
   int part, h;
   uint32_t tile;
@@ -646,7 +646,7 @@ struct Cap {
 };
 
 // What scores get, known to the compiler: the two kinds of branches around every
-// tile would keep copies of it in registers (16384 nodes x 512 in bf16: 1944 us of kernel, 1722 without).
+// tile would keep copies of it in registers (forward of 16384 nodes x 512 in bf16, when it was split: 1944 -> 1722 us).
 // kRuntime leaves both to the run: heads whose channels are not whole quads.
 enum ScoreKind { kRuntime = -1, kPlain = 0, kBiased = 1, kCapped = 2, kCappedBiased = 3 };
 template <int KIND>
@@ -774,7 +774,7 @@ __device__ __forceinline__ void weights_frag(const Tile32<CT>& s, int step, bf16
 
 // A block takes 128 columns of a head, or attn_small_cols where the graphs are small.  (64 for
 // wide fp32 heads, which lets a CU hold two blocks, splits the other side's rows
-// twice as often: 286, 523, 578 and 291 us where 128 take 264, 460, 449 and 267.)
+// twice as often: 8192 nodes of 128x0e+128x1o+128x2e, 8 heads: 269, 434, 434 and 274 us where 128 take 259, 332, 332 and 255.)
 template <typename T, int DC, int COLS>
 struct Block {
   static constexpr int CT = col_tile<T, DC>(), kWaves = COLS / CT, kThreads = 64 * kWaves;
@@ -1132,7 +1132,7 @@ __global__ __launch_bounds__((Block<T, DC, COLS>::kThreads),
 // Wide heads take the two gradients in two launches: the operands and sums of
 // both are 200 registers of the 256 that two waves per SIMD leave each, and what
 // went to scratch memory cost more than doing the scores twice (8192 nodes of
-// 128x0e+128x1o+128x2e, 8 heads: 952 us in one launch, 710 in two).
+// 128x0e+128x1o+128x2e, 8 heads, when they were split: 952 us in one launch, 710 in two; the two now take 593).
 enum KvPart { kBoth, kValues, kKeys };
 template <typename T, int DC>
 constexpr bool kv_in_two() {
